@@ -36,7 +36,10 @@ EXPORTS = ["gemm_f32", "gemm_f32_ex", "gemm_f32_ref_gpu", "gemm_f32_status_strin
            "gemm_f32_kernel_count", "gemm_f32_kernel_name", "gemm_f32_run_kernel",
            "gemm_f32_run_kernel_ex", "gemm_f32_release_workspaces", "gemm_f32_batched",
            "gemm_f32_selected_kernel_batched", "reduce_sum_f32", "gemm_f32_fused",
-           "gemm_f32_run_kernel_fused", "gemm_f32_noalloc", "gemm_f32_clock_probe"]
+           "gemm_f32_run_kernel_fused", "gemm_f32_noalloc", "gemm_f32_clock_probe",
+           "gemm_f32_group_rows", "gemm_f32_grouped", "gemm_f32_grouped_wgrad",
+           "gemm_f32_adapters"]
+MAX_GROUPS = 1024
 CLOCK_PROBE_WORKGROUPS = 1024
 
 
@@ -109,6 +112,18 @@ def load(lib_path=None):
     lib.gemm_f32_selected_kernel_batched.argtypes = [i64, i64, i64, i64, i64, i64, i64, i64,
                                                      i64, vp, vp]
     lib.gemm_f32_selected_kernel_batched.restype = ctypes.c_char_p
+    lib.gemm_f32_group_rows.argtypes = [i64, i64, i64, vp, vp, vp, vp, vp]
+    lib.gemm_f32_group_rows.restype = ci
+    lib.gemm_f32_grouped.argtypes = [ci, i64, i64, i64, i64, vp, f32, vp, i64, i64, vp,
+                                     vp, i64, i64, f32, vp, i64, i64, vp, vp, i64, ci, vp]
+    lib.gemm_f32_grouped.restype = ci
+    lib.gemm_f32_grouped_wgrad.argtypes = [i64, i64, i64, i64, vp, f32, vp, i64, i64, vp,
+                                           vp, i64, i64, vp, f32, vp, i64, i64, vp]
+    lib.gemm_f32_grouped_wgrad.restype = ci
+    lib.gemm_f32_adapters.argtypes = [ci, i64, i64, i64, i64, i64, i64, vp, vp, vp, vp, i64,
+                                      vp, i64, vp, i64, i64, vp, i64, i64, vp, vp, i64, vp, i64,
+                                      vp]
+    lib.gemm_f32_adapters.restype = ci
     _lib = lib
     return lib
 
@@ -172,6 +187,32 @@ def reduce_sum_f32(n, x, out, stream=0) -> int:
     return load().reduce_sum_f32(n, x, out, stream)
 
 
+def gemm_f32_group_rows(n, groups, per_row, index, offsets, order, rows, stream=0) -> int:
+    return load().gemm_f32_group_rows(n, groups, per_row, index, offsets, order, rows, stream)
+
+
+def gemm_f32_grouped(transB, rows, N, K, groups, offsets, alpha, A, lda, rowsA, indexA, B, ldb,
+                     strideB, beta, C, ldc, rowsC, indexC, bias, strideBias, act,
+                     stream=0) -> int:
+    return load().gemm_f32_grouped(transB, rows, N, K, groups, offsets, alpha, A, lda, rowsA,
+                                   indexA, B, ldb, strideB, beta, C, ldc, rowsC, indexC, bias,
+                                   strideBias, act, stream)
+
+
+def gemm_f32_grouped_wgrad(rows, M, N, groups, offsets, alpha, A, lda, rowsA, indexA, B, ldb,
+                           rowsB, indexB, beta, C, ldc, strideC, stream=0) -> int:
+    return load().gemm_f32_grouped_wgrad(rows, M, N, groups, offsets, alpha, A, lda, rowsA,
+                                         indexA, B, ldb, rowsB, indexB, beta, C, ldc, strideC,
+                                         stream)
+
+
+def gemm_f32_adapters(trans, M, N, K, R, groups, places, offsets, order, scale, X, ldx, W, ldw,
+                      D, ldd, strideD, U, ldu, strideU, bias, H, ldh, Y, ldy, stream=0) -> int:
+    return load().gemm_f32_adapters(trans, M, N, K, R, groups, places, offsets, order, scale, X,
+                                    ldx, W, ldw, D, ldd, strideD, U, ldu, strideU, bias, H, ldh,
+                                    Y, ldy, stream)
+
+
 def gemm_f32_ref_gpu(M, N, K, A, lda, B, ldb, C, ldc, stream=0) -> int:
     return load().gemm_f32_ref_gpu(M, N, K, A, lda, B, ldb, C, ldc, stream)
 
@@ -226,6 +267,9 @@ def _pitch(t, name):
         raise TypeError(f"{name} must be on a GPU (got {t.device})")
     if t.shape[1] > 1 and t.stride(1) != 1:
         raise ValueError(f"{name} rows must be contiguous (stride(1) == 1)")
+    if t.shape[0] > 1 and t.shape[1] > 0 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name} rows must not overlap (stride(0) >= the row length); an "
+                         "expanded tensor needs .contiguous()")
     return max(t.stride(0), t.shape[1], 1) if t.shape[0] > 1 else max(t.shape[1], 1)
 
 
@@ -449,6 +493,192 @@ def selected_kernel(A, B, C=None) -> str:
     return gemm_f32_selected_kernel(M, N, K, max(A.stride(0), K, 1), max(B.stride(0), N, 1),
                                     max(ldc, 1), A.data_ptr(), B.data_ptr(),
                                     0 if C is None else C.data_ptr())
+
+
+# ---- grouped products --------------------------------------------------------
+
+def _index(t, name, device, count=None):
+    """Pointer of a contiguous 1-D int32 tensor on ``device`` (0 for None)."""
+    import torch
+    if t is None:
+        return 0
+    if t.dtype != torch.int32 or t.dim() != 1 or (t.numel() > 1 and t.stride(0) != 1):
+        raise TypeError(f"{name} must be a contiguous 1-D int32 tensor")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device} (got {t.device})")
+    if count is not None and t.numel() != count:
+        raise ValueError(f"{name} must have {count} entries, got {t.numel()}")
+    return t.data_ptr()
+
+
+def _stack(t, name, device, shape):
+    """(pointer, pitch, stride) of a 3-D float32 tensor: one matrix per group."""
+    import torch
+    if t.dim() != 3 or t.dtype != torch.float32:
+        raise TypeError(f"{name} must be a 3-D float32 tensor")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device} (got {t.device})")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {'x'.join(map(str, shape))}, got {tuple(t.shape)}")
+    pitch = _pitch(t[0], name) if t.shape[0] > 0 else max(t.shape[2], 1)
+    return t.data_ptr(), pitch, t.stride(0)
+
+
+def _same_device(first, **others):
+    for name, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{name} must be on {first.device} (got {t.device})")
+
+
+def _groups_of(offsets):
+    if offsets.dim() != 1 or offsets.numel() < 1:
+        raise ValueError("offsets must hold one entry more than there are groups")
+    return offsets.numel() - 1
+
+
+def group_rows(index, groups, *, per_row=1):
+    """The entries of a 1-D int32 GPU tensor ordered by the group they name
+    (values outside [0, groups) name none).  Returns int32 tensors ``offsets``
+    (groups + 1), ``order`` (the entries by (group, entry)) and ``rows``
+    (order // per_row); both hold -1 from offsets[groups] on."""
+    import torch
+    if index.device.type != "cuda":
+        raise TypeError(f"index must be on a GPU (got {index.device})")
+    n, dev = index.numel(), index.device
+    ptr = _index(index, "index", dev)
+    offsets = torch.empty(max(int(groups), 0) + 1, dtype=torch.int32, device=dev)
+    order = torch.empty(n, dtype=torch.int32, device=dev)
+    rows = torch.empty(n, dtype=torch.int32, device=dev)
+    with _device(index):
+        rc = gemm_f32_group_rows(n, int(groups), int(per_row), ptr, offsets.data_ptr(),
+                                 order.data_ptr(), rows.data_ptr(),
+                                 torch.cuda.current_stream(dev).cuda_stream)
+    if rc != GEMM_F32_OK:
+        raise GemmError(rc, "gemm_f32_group_rows")
+    return offsets, order, rows
+
+
+def gemm_grouped(A, B, offsets, C=None, *, trans_b=False, alpha=1.0, beta=0.0, bias=None,
+                 act=ACT_NONE, index_a=None, index_c=None):
+    """C[index_c[i]] = act(alpha * A[index_a[i]] @ op(B[g]) + beta * C[index_c[i]]
+    + bias[g]) for every place i of group g (offsets[g] <= i < offsets[g + 1]).
+    B is groups x K x N (groups x N x K when trans_b), bias groups x N or None;
+    an index that is None is the identity.  The places are the indexes' length
+    (A's rows without any).  A new C has one row a place; rows that no place
+    names hold nothing in particular there, and keep what they held in a C that
+    is given.  Returns C."""
+    import torch
+    lda = _pitch(A, "A")
+    dev, groups = A.device, _groups_of(offsets)
+    K = A.shape[1]
+    N = B.shape[1 if trans_b else 2] if B.dim() == 3 else -1
+    b, ldb, sb = _stack(B, "B", dev, (groups, N, K) if trans_b else (groups, K, N))
+    rows = (index_a.numel() if index_a is not None else
+            index_c.numel() if index_c is not None else A.shape[0])
+    ia, ic = _index(index_a, "index_a", dev, rows), _index(index_c, "index_c", dev, rows)
+    if C is None:
+        C = torch.empty((rows, N), dtype=torch.float32, device=dev)
+    if C.dim() != 2 or C.shape[1] != N:
+        raise ValueError(f"C must have {N} columns, got {tuple(C.shape)}")
+    ldc = _pitch(C, "C")
+    bptr, sbias = 0, 0
+    if bias is not None:
+        if (bias.dtype != torch.float32 or tuple(bias.shape) != (groups, N)
+                or (N > 1 and bias.stride(1) != 1)):
+            raise ValueError(f"bias must be {groups}x{N} floats with contiguous rows")
+        bptr, sbias = bias.data_ptr(), bias.stride(0)
+    _same_device(A, C=C, bias=bias)
+    with _device(A):
+        rc = gemm_f32_grouped(int(bool(trans_b)), rows, N, K, groups,
+                              _index(offsets, "offsets", dev), alpha, A.data_ptr(), lda,
+                              A.shape[0], ia, b, ldb, sb, beta, C.data_ptr(), ldc, C.shape[0],
+                              ic, bptr, sbias, int(act),
+                              torch.cuda.current_stream(dev).cuda_stream)
+    if rc != GEMM_F32_OK:
+        raise GemmError(rc, "gemm_f32_grouped")
+    return C
+
+
+def gemm_grouped_wgrad(A, B, offsets, C=None, *, alpha=1.0, beta=0.0, index_a=None,
+                       index_b=None):
+    """C[g] = alpha * sum over the places i of group g of A[index_a[i]]^T
+    B[index_b[i]], plus beta * C[g]: the gradient of gemm_grouped's weights.
+    Returns C (groups x A's columns x B's columns)."""
+    import torch
+    lda, ldb = _pitch(A, "A"), _pitch(B, "B")
+    dev, groups = A.device, _groups_of(offsets)
+    M, N = A.shape[1], B.shape[1]
+    rows = (index_a.numel() if index_a is not None else
+            index_b.numel() if index_b is not None else A.shape[0])
+    ia, ib = _index(index_a, "index_a", dev, rows), _index(index_b, "index_b", dev, rows)
+    if C is None:
+        C = torch.empty((groups, M, N), dtype=torch.float32, device=dev)
+    c, ldc, sc = _stack(C, "C", dev, (groups, M, N))
+    _same_device(A, B=B)
+    with _device(A):
+        rc = gemm_f32_grouped_wgrad(rows, M, N, groups, _index(offsets, "offsets", dev), alpha,
+                                    A.data_ptr(), lda, A.shape[0], ia, B.data_ptr(), ldb,
+                                    B.shape[0], ib, beta, c, ldc, sc,
+                                    torch.cuda.current_stream(dev).cuda_stream)
+    if rc != GEMM_F32_OK:
+        raise GemmError(rc, "gemm_f32_grouped_wgrad")
+    return C
+
+
+def gemm_adapters(X, W, down, up, offsets, order, Y=None, H=None, *, trans=False, scale=None,
+                  bias=None):
+    """Y = X @ op(W) + bias, and for the rows order[i] of adapter g
+    (offsets[g] <= i < offsets[g + 1]) H[i] = scale[g] * X[order[i]] @ op(down[g]),
+    Y[order[i]] += H[i] @ op(up[g]).  W is K x N, down adapters x K x R and up
+    adapters x R x N, or with ``trans`` each matrix stored transposed; ``scale``
+    one float per adapter (None: 1), ``bias`` N floats or None.  Returns (Y, H);
+    H (one row a place) is what gemm_adapters_grad takes."""
+    import torch
+    ldx, ldw = _pitch(X, "X"), _pitch(W, "W")
+    dev, adapters = X.device, _groups_of(offsets)
+    M, K = X.shape
+    N = W.shape[0] if trans else W.shape[1]
+    if (W.shape[1] if trans else W.shape[0]) != K:
+        raise ValueError(f"inner sizes differ: X is {tuple(X.shape)}, W is {tuple(W.shape)}")
+    R = down.shape[1 if trans else 2] if down.dim() == 3 else -1
+    d, ldd, sd = _stack(down, "down", dev, (adapters, R, K) if trans else (adapters, K, R))
+    u, ldu, su = _stack(up, "up", dev, (adapters, N, R) if trans else (adapters, R, N))
+    places = order.numel()
+    if Y is None:
+        Y = torch.empty((M, N), dtype=torch.float32, device=dev)
+    if H is None:
+        H = torch.empty((places, R), dtype=torch.float32, device=dev)
+    if tuple(Y.shape) != (M, N) or tuple(H.shape) != (places, R):
+        raise ValueError(f"Y must be {M}x{N} and H {places}x{R}, got {tuple(Y.shape)} and "
+                         f"{tuple(H.shape)}")
+    ldy, ldh = _pitch(Y, "Y"), _pitch(H, "H")
+    for t, name, count in ((scale, "scale", adapters), (bias, "bias", N)):
+        if t is not None and (t.dtype != torch.float32 or t.dim() != 1 or t.numel() != count
+                              or (count > 1 and t.stride(0) != 1)):
+            raise ValueError(f"{name} must be a contiguous vector of {count} floats")
+    _same_device(X, W=W, Y=Y, H=H, scale=scale, bias=bias)
+    with _device(X):
+        rc = gemm_f32_adapters(int(bool(trans)), M, N, K, R, adapters, places,
+                               _index(offsets, "offsets", dev), _index(order, "order", dev),
+                               0 if scale is None else scale.data_ptr(), X.data_ptr(), ldx,
+                               W.data_ptr(), ldw, d, ldd, sd, u, ldu, su,
+                               0 if bias is None else bias.data_ptr(), H.data_ptr(), ldh,
+                               Y.data_ptr(), ldy, torch.cuda.current_stream(dev).cuda_stream)
+    if rc != GEMM_F32_OK:
+        raise GemmError(rc, "gemm_f32_adapters")
+    return Y, H
+
+
+def gemm_adapters_grad(dY, X, W, down, up, offsets, order, H, *, trans=False, scale=None):
+    """Gradients of gemm_adapters with the H it returned: (dX, d_down, d_up) for
+    the gradient dY of Y.  (W's is gemm_ex's product of X and dY, the bias's the
+    sum of dY's rows.)"""
+    dX, G = gemm_adapters(dY, W, up, down, offsets, order, trans=not trans, scale=scale)
+    if trans:
+        return (dX, gemm_grouped_wgrad(G, X, offsets, index_b=order),
+                gemm_grouped_wgrad(dY, H, offsets, index_a=order))
+    return (dX, gemm_grouped_wgrad(X, G, offsets, index_a=order),
+            gemm_grouped_wgrad(H, dY, offsets, index_b=order))
 
 
 class _device:

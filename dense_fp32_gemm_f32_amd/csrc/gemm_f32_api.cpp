@@ -665,6 +665,14 @@ Op make_op(int transA, int transB, float alpha, float beta, const float* bias = 
 
 }  // namespace
 
+namespace gemmf32 {
+int host_check_device(int* dev) { return check_device(dev); }
+int host_check_pointer(const void* p, int dev) { return check_pointer(p, dev); }
+int host_partials(int dev, hipStream_t s, size_t floats, float** out) {
+  return get_workspace(dev, s, floats, out);
+}
+}  // namespace gemmf32
+
 extern "C" {
 
 int gemm_f32(int64_t M, int64_t N, int64_t K, const float* A, int64_t lda, const float* B,
@@ -820,7 +828,7 @@ const char* gemm_f32_status_string(int status) {
     case GEMM_F32_ERR_LAUNCH: return "kernel launch failed";
     case GEMM_F32_ERR_BAD_KERNEL: return "kernel index unknown or unable to run these arguments";
     case GEMM_F32_ERR_POINTER: return "pointer is not device memory the current device can access";
-    case GEMM_F32_ERR_INVALID_ARG: return "unknown activation";
+    case GEMM_F32_ERR_INVALID_ARG: return "unknown activation, or entries per row below 1";
     case GEMM_F32_ERR_SCRATCH: return "the call needs more scratch than gemm_f32_noalloc's fixed array holds";
     default: return "unknown status";
   }

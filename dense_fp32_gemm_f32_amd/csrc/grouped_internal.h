@@ -1,0 +1,131 @@
+// Declarations shared by the grouped products' kernels and their C-ABI layer:
+// products whose rows (or, for the weights' gradient, whose K) are split over
+// groups by offsets that only the device knows.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "gemm_f32_internal.h"
+
+namespace gemmf32 {
+
+// Place i (0 <= i < rows) belongs to group g when offsets[g] <= i < offsets[g+1].
+// Product (launch_grouped):   C[ic(i)] = act(alpha s_g A[ia(i)] op(B_g) + beta C[ic(i)] + bias_g)
+// Gradient (launch_grouped_wgrad): C_g = alpha sum_i A[ia(i)]^T B[ib(i)] + beta C_g
+// An index array that is NULL is the identity.  s_g = gscale[g], 1 when NULL.
+struct GroupedProblem {
+  const float* A = nullptr;
+  const float* B = nullptr;
+  float* C = nullptr;
+  const int* offsets = nullptr;
+  const int* ia = nullptr;
+  const int* ib = nullptr;   // gradient only
+  const int* ic = nullptr;   // product only
+  const float* gscale = nullptr;
+  int64_t lda = 0, ldb = 0, ldc = 0;
+  int64_t sb = 0, sc = 0, sbias = 0;   // strides of B_g, C_g and bias_g
+  int rows = 0, groups = 0;
+  int M = 0, N = 0, K = 0;             // M: gradient only; K: product only
+  int rows_a = 0, rows_b = 0, rows_c = 0;
+  bool tb = false;                     // product: B_g stored N x K
+};
+
+hipError_t launch_grouped(const GroupedProblem& p, const Epilogue& e, hipStream_t s);
+hipError_t launch_grouped_wgrad(const GroupedProblem& p, const Epilogue& e, hipStream_t s);
+
+// offsets, order and rows (may be NULL) of gemm_f32_group_rows
+hipError_t launch_group_rows(int n, int groups, int per_row, const int* index, int* offsets,
+                             int* order, int* rows, hipStream_t s);
+
+constexpr int kMaxGroups = 1024;
+
+// A grid of n workgroups (n below 2^31): the launch takes fewer than 2^32
+// threads along x, so larger grids go on along y.  tile_id() numbers them.
+constexpr int64_t kGridX = 1 << 21;
+inline dim3 tile_grid(int64_t n) {
+  const int64_t x = n < kGridX ? n : kGridX;
+  return dim3((unsigned)x, (unsigned)((n + x - 1) / x));
+}
+
+#if defined(__HIP__)
+__device__ __forceinline__ unsigned tile_id() { return blockIdx.y * gridDim.x + blockIdx.x; }
+
+// Group g's places, taken into [0, rows]; a group that ends before it begins
+// is empty.
+__device__ __forceinline__ void group_span(const int* offsets, int g, int rows, int& begin,
+                                           int& end) {
+  begin = min(max(offsets[g], 0), rows);
+  end = max(begin, min(offsets[g + 1], rows));
+}
+
+// Inclusive sum over the lanes of a wave, held below `cap`.
+__device__ __forceinline__ unsigned wave_scan(unsigned x, unsigned cap, int lane) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const unsigned y = __shfl_up(x, d);
+    if (lane >= d) x = min(x + y, cap);
+  }
+  return x;
+}
+
+// The row tiles of all groups in order, bm places each (a group's last one
+// part full), as tile numbers 0 .. total - 1.  Each wave computes it alone from
+// the offsets: one load of 64 groups, a scan, a ballot.
+//   total()   the number of row tiles, held below cap
+//   find(t)   the group of row tile t < total(): its number, its places, and
+//             the first of its row tiles
+struct RowTiles {
+  const int* offsets;
+  int groups, rows, bm, lane;
+  unsigned cap;
+  unsigned first_incl;   // the scan of groups 0 .. 63, kept for find
+
+  __device__ __forceinline__ unsigned scan_at(int base) const {
+    unsigned x = 0;
+    if (base + lane < groups) {
+      int b, e;
+      group_span(offsets, base + lane, rows, b, e);
+      x = (unsigned)((e - b + bm - 1) / bm);
+    }
+    return wave_scan(x, cap, lane);
+  }
+  __device__ __forceinline__ unsigned total() {
+    unsigned sum = 0;
+    for (int base = 0; base < groups; base += 64) {
+      const unsigned incl = scan_at(base);
+      if (base == 0) first_incl = incl;
+      sum = min(sum + (unsigned)__builtin_amdgcn_readlane(incl, 63), cap);
+    }
+    return sum;
+  }
+  __device__ __forceinline__ bool find(unsigned t, int& g, int& begin, int& end,
+                                       unsigned& first) const {
+    unsigned sum = 0;
+    for (int base = 0; base < groups; base += 64) {
+      const unsigned incl = base == 0 ? first_incl : scan_at(base);
+      const unsigned long long past = __ballot(sum + incl > t);
+      if (past) {
+        const int l = __builtin_ctzll(past);
+        const unsigned before = l > 0 ? (unsigned)__builtin_amdgcn_readlane(incl, l - 1) : 0u;
+        g = base + l;
+        first = sum + before;
+        group_span(offsets, g, rows, begin, end);
+        begin = __builtin_amdgcn_readfirstlane(begin);
+        end = __builtin_amdgcn_readfirstlane(end);
+        return true;
+      }
+      sum = min(sum + (unsigned)__builtin_amdgcn_readlane(incl, 63), cap);
+    }
+    return false;
+  }
+};
+#endif
+
+// Most row tiles of bm places that `rows` places in `groups` groups can need.
+inline int64_t most_row_tiles(int64_t rows, int64_t groups, int bm) {
+  return rows / bm + (groups < rows ? groups : rows);
+}
+
+}  // namespace gemmf32

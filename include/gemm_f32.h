@@ -93,7 +93,7 @@ enum gemm_f32_status {
   GEMM_F32_ERR_LAUNCH = 7,        /* the kernel launch reported an error */
   GEMM_F32_ERR_BAD_KERNEL = 8,    /* unknown kernel index, or one that cannot run these arguments */
   GEMM_F32_ERR_POINTER = 9,       /* A, B or C not 4-byte aligned, or not memory the current device can access */
-  GEMM_F32_ERR_INVALID_ARG = 10,  /* an activation other than GEMM_F32_ACT_NONE / _RELU */
+  GEMM_F32_ERR_INVALID_ARG = 10,  /* an activation other than GEMM_F32_ACT_NONE / _RELU; per_row below 1 */
   GEMM_F32_ERR_SCRATCH = 11       /* gemm_f32_noalloc: the call needs more scratch than its fixed array */
 };
 
@@ -230,6 +230,131 @@ int gemm_f32_batched(int64_t M, int64_t N, int64_t K,
                      const float *B, int64_t ldb, int64_t strideB,
                      float *C, int64_t ldc, int64_t strideC,
                      int64_t batch, void *stream);
+
+/* Most groups of the grouped products (experts, adapters) in one call. */
+#define GEMM_F32_MAX_GROUPS 1024
+
+/*
+ * gemm_f32_group_rows -- rows ordered by the group that takes them: the plan
+ * of the grouped products below.  index: n int32 entries in device memory;
+ * entry i names the group of entry i, and any value outside [0, groups) means
+ * none (a dropped choice, a request without an adapter).  Writes
+ *   offsets[0 .. groups]  the number of entries of the groups below g, so
+ *                         group g owns places offsets[g] .. offsets[g+1] - 1;
+ *   order[0 .. n)         the entries in the order (group, i): a stable sort;
+ *   rows[0 .. n)          order[p] / per_row (NULL: not wanted) -- with a
+ *                         router's choices stored per_row to a token, the token.
+ * Places from offsets[groups] on (the entries of no group) hold -1 in order
+ * and rows.  All int32.  The result depends on the arguments only.
+ *
+ * Errors: n or groups negative, n above GEMM_F32_MAX_DIM, groups above
+ * GEMM_F32_MAX_GROUPS GEMM_F32_ERR_INVALID_DIM; per_row < 1
+ * GEMM_F32_ERR_INVALID_ARG; NULL offsets, or NULL index or order with n > 0
+ * GEMM_F32_ERR_NULL_PTR; pointers not 4-byte aligned GEMM_F32_ERR_POINTER; two
+ * of the arrays overlapping GEMM_F32_ERR_ALIAS; then the device, workspace
+ * and pointer checks of gemm_f32.  n == 0 writes zero offsets.
+ */
+int gemm_f32_group_rows(int64_t n, int64_t groups, int64_t per_row,
+                        const int32_t *index, int32_t *offsets,
+                        int32_t *order, int32_t *rows, void *stream);
+
+/*
+ * gemm_f32_grouped -- products whose rows belong to different weights (the
+ * experts of a sparse layer), ragged sizes, in one launch.  Place i of `rows`
+ * places belongs to group g when offsets[g] <= i < offsets[g+1], and then
+ *   C[ic(i)] = act(alpha * A[ia(i)] op(B_g) + beta * C[ic(i)] + bias_g)
+ * with B_g = B + g * strideB (K x N, or N x K when transB, pitch ldb), bias_g =
+ * bias + g * strideBias (N floats; bias NULL for none), ia(i) = indexA[i] and
+ * ic(i) = indexC[i], or i where that array is NULL.  A has rowsA rows of K
+ * floats, C rowsC rows of N.  offsets (groups + 1 entries) and the indexes
+ * (rows entries) are int32 device memory, as gemm_f32_group_rows writes them:
+ * nothing is read back to the host.  The same call with transB flipped
+ * and the roles of the indexes exchanged gives the gradient of A's rows.
+ *
+ * What no place names stays as it was: rows of C, groups without places,
+ * places from offsets[groups] on.  An index outside its matrix is never
+ * followed: such a row of A counts as zeros, such a row of C is not written.
+ * Offsets are taken into [0, rows] and a group that ends before it begins is
+ * empty; places named by two groups (offsets that fall) and rows of C named
+ * twice get one of the values, or none.  beta == 0 does not read C.
+ * Sums and the update are as gemm_f32_fused's; K == 0 gives the
+ * update of an empty sum.  The summation order depends on the sizes,
+ * alignments and offsets only.
+ *
+ * Errors as gemm_f32_fused: a negative size, one above GEMM_F32_MAX_DIM,
+ * groups above GEMM_F32_MAX_GROUPS, or rowsA / rowsC below rows where the
+ * index is NULL GEMM_F32_ERR_INVALID_DIM; a pitch below a row or a negative stride (0
+ * shares one matrix or bias) GEMM_F32_ERR_INVALID_LD; C overlapping anything that is read
+ * GEMM_F32_ERR_ALIAS.  rows, groups or N == 0 is a successful no-op.
+ */
+int gemm_f32_grouped(int transB, int64_t rows, int64_t N, int64_t K,
+                     int64_t groups, const int32_t *offsets, float alpha,
+                     const float *A, int64_t lda, int64_t rowsA,
+                     const int32_t *indexA,
+                     const float *B, int64_t ldb, int64_t strideB,
+                     float beta,
+                     float *C, int64_t ldc, int64_t rowsC,
+                     const int32_t *indexC,
+                     const float *bias, int64_t strideBias, int activation,
+                     void *stream);
+
+/*
+ * gemm_f32_grouped_wgrad -- the gradient of the grouped products' weights: for
+ * every group g, over its places i,
+ *   C_g = alpha * sum_i A[ia(i)]^T B[ib(i)] + beta * C_g
+ * with A of rowsA rows of M floats, B of rowsB rows of N, C_g = C + g *
+ * strideC (M x N, pitch ldc).  Offsets and indexes as gemm_f32_grouped; a row
+ * of A or B whose index is outside its matrix counts as zeros.  Every C_g is
+ * written: a group without places gets beta * C_g (+0.0 when beta == 0; C is
+ * not read then).  For weights stored transposed exchange A and B.  With a
+ * column of ones for A (M = 1) it sums B's rows: the gradient of the biases.
+ *
+ * Errors as gemm_f32_grouped; strideC below M rows of ldc GEMM_F32_ERR_ALIAS.
+ * groups, M or N == 0 is a successful no-op.
+ */
+int gemm_f32_grouped_wgrad(int64_t rows, int64_t M, int64_t N,
+                           int64_t groups, const int32_t *offsets, float alpha,
+                           const float *A, int64_t lda, int64_t rowsA,
+                           const int32_t *indexA,
+                           const float *B, int64_t ldb, int64_t rowsB,
+                           const int32_t *indexB,
+                           float beta,
+                           float *C, int64_t ldc, int64_t strideC,
+                           void *stream);
+
+/*
+ * gemm_f32_adapters -- low-rank adapters of many requests at once beside a
+ * shared projection: Y = X op(W) + bias for all M rows, then for every place i
+ * of adapter g (row x = order[i], places as in gemm_f32_grouped, `places` of
+ * them)
+ *   H[i] = scale_g * X[x] op(D_g)        (R floats, in place order)
+ *   Y[x] = Y[x] + H[i] op(U_g)
+ * with trans == 0: W K x N, D_g K x R, U_g R x N; trans != 0: all three stored
+ * transposed (W N x K, D_g R x K, U_g N x R), as checkpoints hold them.  D_g =
+ * D + g * strideD, U_g = U + g * strideU; scale: one float for each adapter in
+ * device memory (NULL: 1).  Rows that no place names get the projection only.
+ * A row may be named once at most.  H (places x R, pitch ldh) is written for
+ * the places of adapters and kept by a caller that trains:
+ *   the gradient of X   is this call on dY with trans flipped and U, D
+ *                       exchanged; its H is G, the gradient of X op(D) scaled;
+ *   the gradient of D_g is gemm_f32_grouped_wgrad of X (by order) and G,
+ *   the gradient of U_g that of H and dY (by order).
+ *
+ * Errors as gemm_f32_fused and gemm_f32_grouped; H or Y overlapping
+ * anything else GEMM_F32_ERR_ALIAS.  R, groups or places == 0 leaves the
+ * projection; M or N == 0 is a successful no-op.
+ */
+int gemm_f32_adapters(int trans, int64_t M, int64_t N, int64_t K, int64_t R,
+                      int64_t groups, int64_t places,
+                      const int32_t *offsets, const int32_t *order,
+                      const float *scale,
+                      const float *X, int64_t ldx,
+                      const float *W, int64_t ldw,
+                      const float *D, int64_t ldd, int64_t strideD,
+                      const float *U, int64_t ldu, int64_t strideU,
+                      const float *bias,
+                      float *H, int64_t ldh,
+                      float *Y, int64_t ldy, void *stream);
 
 /*
  * gemm_f32_ref_gpu -- the same operation with the naive one-thread-per-output

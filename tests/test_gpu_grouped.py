@@ -1,0 +1,648 @@
+"""GPU tests of the products whose rows belong to different weights
+(``gemm_f32_group_rows``, ``gemm_f32_grouped``, ``gemm_f32_grouped_wgrad``,
+``gemm_f32_adapters``) against their definitions in 64 bits.
+
+Gates.  Whole-number inputs (-2 .. 2, and halves where a factor scales them):
+every partial sum is exact in fp32, so the result equals the 64-bit one bit
+for bit whatever the order.  General inputs: a sum of K products and n further
+fp32 operations is off by at most (K + n) 2^-24 of the sum of magnitudes
+(each rounding half a step), in any order of summation.
+"""
+import pytest
+import torch
+
+from dense_fp32_gemm_f32_amd import binding
+from tests import gpu_helpers as H
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+
+
+def gen(seed):
+    g = torch.Generator()
+    g.manual_seed(seed)
+    return g
+
+
+def draw(g, *shape, integer):
+    if integer:
+        return torch.randint(-2, 3, shape, generator=g).float()
+    return torch.randn(*shape, generator=g)
+
+
+def device(x, pad=0, shift=0, fill=float("nan")):
+    """x on the GPU with its last-but-one stride padded and its start shifted,
+    NaN in between."""
+    *lead, rows, cols = x.shape
+    pitch = cols + pad
+    n = 1
+    for d in lead:
+        n *= d
+    flat = torch.full((n * rows * pitch + shift + 4,), fill)
+    view = torch.as_strided(flat, (n, rows, cols), (rows * pitch, pitch, 1), shift)
+    view.copy_(x.reshape(n, rows, cols))
+    return torch.as_strided(flat.cuda(), tuple(lead) + (rows, cols),
+                            (rows * pitch,) * len(lead) + (pitch, 1), shift)
+
+
+def spans(counts, spare=0):
+    """offsets of groups with these counts, and the number of places."""
+    off = [0]
+    for c in counts:
+        off.append(off[-1] + c)
+    return torch.tensor(off, dtype=torch.int32), off[-1] + spare
+
+
+def check(got, want, mag, ops, integer, what):
+    got = got.cpu().double()
+    if integer:
+        assert torch.equal(got, want), f"{what}: {(got != want).sum()} of {got.numel()} differ"
+    else:
+        err = (got - want).abs()
+        assert bool((err <= ops * U * mag).all()), \
+            f"{what}: off by {float((err / mag.clamp_min(1e-30)).max()) / U:.1f} of {ops} steps"
+
+
+# ---- rows ordered by group -------------------------------------------------------
+
+@pytest.mark.parametrize("n,groups,per_row", [
+    (0, 5, 1), (1, 1, 1), (3, 0, 1), (63, 2, 1), (64, 64, 2), (65, 3, 5), (1000, 7, 4),
+    (1024, 1, 1), (4099, 1024, 3), (5000, 257, 1), (70001, 64, 4), (300007, 33, 1)])
+def test_group_rows(gpu_lib, n, groups, per_row):
+    g = gen(n + groups)
+    index = torch.randint(-1, groups + 1, (n,), generator=g).int()
+    if n > 10:   # far outside, and the neighbours of the range
+        index[::7] = torch.tensor([-2 ** 31, 2 ** 31 - 1, groups, -1]).int().repeat(n)[:len(index[::7])]
+    H.say(f"group_rows n={n} groups={groups} per_row={per_row}")
+    offsets, order, rows = gpu_lib.group_rows(index.cuda(), groups, per_row=per_row)
+    torch.cuda.synchronize()
+    i = index.long()
+    kept = (i >= 0) & (i < groups)
+    places = torch.nonzero(kept)[:, 0]
+    want = places[torch.sort(i[places], stable=True).indices]
+    counts = torch.bincount(i[places], minlength=groups)[:groups]
+    assert offsets.cpu().tolist() == [0] + torch.cumsum(counts, 0).tolist()
+    tail = torch.full((n - want.numel(),), -1)
+    assert torch.equal(order.cpu().long(), torch.cat([want, tail]))
+    assert torch.equal(rows.cpu().long(), torch.cat([want // per_row, tail]))
+
+
+@pytest.mark.parametrize("value", [-1, 0, 4, 5])
+def test_group_rows_of_one_value(gpu_lib, value):
+    """All entries in one group, or in none."""
+    n, groups = 777, 5
+    H.say(f"group_rows all {value}")
+    offsets, order, _ = gpu_lib.group_rows(torch.full((n,), value, dtype=torch.int32).cuda(),
+                                           groups)
+    inside = 0 <= value < groups
+    assert offsets.cpu().tolist() == [n if inside and g > value else 0 for g in range(groups + 1)]
+    assert order.cpu().tolist() == (list(range(n)) if inside else [-1] * n)
+
+
+# ---- products grouped by expert ---------------------------------------------------
+
+COUNTS = {
+    "one": [1],
+    "few": [0, 3, 0, 1, 17, 0],
+    "even": [16, 16, 16, 16],
+    "skewed": [0, 130, 1, 64, 65, 0, 300, 7],
+    "many": [(7 * i) % 5 for i in range(150)],
+    "none": [0, 0, 0],
+    "long": [513, 700],
+    "most": [2 if i in (0, 700, 1023) else 0 for i in range(1024)],
+}
+
+
+def grouped_case(lib, counts, K, N, trans, gather, scatter, epilogue, integer, seed, pads=(0, 0, 0),
+                 shifts=(0, 0, 0), spare=3):
+    """One product against its definition; returns nothing, asserts everything:
+    values, and NaN wherever nothing may be written."""
+    g = gen(seed)
+    offsets, rows = spans(counts, spare)
+    G = len(counts)
+    rows_a = rows + 5 if not gather else max(1, rows // 2)
+    rows_c = rows + 9
+    A = draw(g, rows_a, K, integer=integer)
+    W = draw(g, G, *((N, K) if trans else (K, N)), integer=integer)
+    ia = torch.randint(0, rows_a, (rows,), generator=g).int() if gather else None
+    ic = torch.randperm(rows_c, generator=g)[:rows].int() if scatter else None
+    alpha, beta, bias, act = (0.5, -2.0, draw(g, G, N, integer=integer), 1) if epilogue else \
+        (1.0, 0.0, None, 0)
+    C0 = draw(g, rows_c, N, integer=integer)
+    Ad, Wd = device(A, pads[0], shifts[0]), device(W, pads[1], shifts[1])
+    Cd = device(C0 if epilogue else torch.full_like(C0, float("nan")), pads[2], shifts[2])
+    before = Cd.cpu().double()
+    H.say(f"grouped counts={counts[:8]} K={K} N={N} trans={trans} gather={gather} "
+          f"scatter={scatter} epilogue={epilogue} int={integer} pads={pads} shifts={shifts}")
+    lib.gemm_grouped(Ad, Wd, offsets.cuda(), Cd, trans_b=trans, alpha=alpha, beta=beta,
+                     bias=None if bias is None else bias.cuda(), act=act,
+                     index_a=None if ia is None else ia.cuda(),
+                     index_c=None if ic is None else ic.cuda())
+    torch.cuda.synchronize()
+    want, mag = before.clone(), torch.ones_like(before)
+    for e, (b, f) in enumerate(zip(offsets.tolist(), offsets.tolist()[1:])):
+        if f == b:
+            continue
+        at = torch.arange(b, f)
+        src = ia[b:f].long() if gather else at
+        dst = ic[b:f].long() if scatter else at
+        w = W[e].double().t() if trans else W[e].double()
+        v = alpha * (A[src].double() @ w)
+        m = abs(alpha) * (A[src].double().abs() @ w.abs())
+        if epilogue:
+            v = v + beta * before[dst] + bias[e].double()
+            m = m + (beta * before[dst]).abs() + bias[e].double().abs()
+            v = v.clamp_min(0)
+        want[dst], mag[dst] = v, m
+    named = ~torch.isnan(want)
+    got = Cd.cpu()
+    assert torch.equal(~torch.isnan(got), named), "a row that no place names was written"
+    check(got[named], want[named], mag[named], K + 4, integer, "grouped")
+
+
+@pytest.mark.parametrize("integer", [True, False])
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("counts", list(COUNTS))
+def test_grouped_counts(gpu_lib, counts, trans, integer):
+    grouped_case(gpu_lib, COUNTS[counts], 64, 96, trans, True, False, False, integer, 11)
+
+
+@pytest.mark.parametrize("gather,scatter,epilogue", [
+    (False, False, True), (True, True, False), (False, True, True), (True, True, True)])
+@pytest.mark.parametrize("counts", ["few", "skewed"])
+def test_grouped_indexes_and_epilogue(gpu_lib, counts, gather, scatter, epilogue):
+    for trans in (False, True):
+        for integer in (True, False):
+            grouped_case(gpu_lib, COUNTS[counts], 48, 132, trans, gather, scatter, epilogue,
+                         integer, 12)
+
+
+@pytest.mark.parametrize("K", [0, 1, 3, 4, 15, 16, 17, 31, 36, 100, 127, 260, 1031])
+def test_grouped_inner_sizes(gpu_lib, K):
+    for counts in ("few", "skewed"):
+        for trans in (False, True):
+            grouped_case(gpu_lib, COUNTS[counts], K, 68, trans, True, True, True, True, 13)
+            grouped_case(gpu_lib, COUNTS[counts], K, 68, trans, True, False, False, False, 14)
+
+
+@pytest.mark.parametrize("N", [1, 2, 5, 16, 33, 64, 129, 260, 515])
+def test_grouped_widths(gpu_lib, N):
+    for counts in ("few", "skewed"):
+        for trans in (False, True):
+            grouped_case(gpu_lib, COUNTS[counts], 40, N, trans, True, True, True, True, 15)
+
+
+@pytest.mark.parametrize("pads,shifts", [((4, 8, 4), (0, 0, 0)), ((1, 3, 5), (0, 0, 0)),
+                                         ((0, 0, 0), (1, 2, 3)), ((2, 0, 1), (0, 3, 0)),
+                                         ((0, 1, 0), (0, 0, 1))])
+def test_grouped_pitches_and_alignment(gpu_lib, pads, shifts):
+    for counts in ("few", "skewed"):
+        for trans in (False, True):
+            grouped_case(gpu_lib, COUNTS[counts], 96, 72, trans, True, True, True, True, 16, pads,
+                         shifts)
+
+
+@pytest.mark.parametrize("K,N", [(512, 384), (1000, 260), (773, 517)])
+@pytest.mark.parametrize("trans", [False, True])
+def test_grouped_larger(gpu_lib, K, N, trans):
+    for counts in ([700, 0, 1300, 90], [5, 9, 0, 2, 16, 16, 15], [1] * 40):
+        grouped_case(gpu_lib, counts, K, N, trans, True, False, False, True, 17)
+        grouped_case(gpu_lib, counts, K, N, trans, False, True, True, False, 18)
+
+
+def test_grouped_shared_weight_and_bias(gpu_lib):
+    """Strides of 0: one weight and one bias for every group."""
+    g = gen(19)
+    A, W, b = (draw(g, *s, integer=True) for s in ((40, 32), (1, 32, 48), (1, 48)))
+    offsets, _ = spans([10, 0, 25])
+    got = gpu_lib.gemm_grouped(A.cuda(), W.cuda().expand(3, 32, 48), offsets.cuda(),
+                               bias=b.cuda().expand(3, 48))
+    assert torch.equal(got.cpu()[:35], (A @ W[0] + b)[:35])
+
+
+def test_grouped_indexes_outside_are_not_followed(gpu_lib):
+    """A row of A whose index is outside counts as zeros (not NaN, not 0 * x); a
+    row of C whose index is outside is not written."""
+    g = gen(20)
+    rows, K, N = 90, 64, 64
+    A, W = draw(g, rows, K, integer=True), draw(g, 2, K, N, integer=True)
+    offsets, _ = spans([50, 40])
+    ia, ic = torch.arange(rows).int(), torch.arange(rows).int()
+    ia[3], ia[60], ia[89] = -1, rows, 2 ** 31 - 1
+    ic[4], ic[49], ic[88] = -2 ** 31, rows, -1
+    C = torch.full((rows, N), 7.0, device="cuda")
+    H.say("grouped indexes outside")
+    gpu_lib.gemm_grouped(A.cuda(), W.cuda(), offsets.cuda(), C, index_a=ia.cuda(),
+                         index_c=ic.cuda())
+    want = torch.cat([A[:50] @ W[0], A[50:] @ W[1]])
+    want[[3, 60, 89]] = 0
+    want[[4, 49, 88]] = 7
+    assert torch.equal(C.cpu(), want)
+
+
+def test_grouped_offsets_outside_or_falling(gpu_lib):
+    """Offsets are taken into [0, rows]; a group that ends before it begins is
+    empty; nothing outside C is written."""
+    g = gen(21)
+    rows, K, N = 70, 32, 40
+    A, W = draw(g, rows, K, integer=True), draw(g, 4, K, N, integer=True)
+    for off, want_groups in [([-5, 20, 20, 70, 1000], [(0, 20, 0), (20, 70, 2)]),
+                             ([0, 30, 10, 10, 10], [(0, 30, 0)]),
+                             ([2 ** 31 - 1, -2 ** 31, 5, 6, 7], [(0, 5, 1), (5, 6, 2), (6, 7, 3)])]:
+        C, flat = H.sentinel_output(rows, N)
+        H.say(f"grouped offsets {off}")
+        gpu_lib.gemm_grouped(A.cuda(), W.cuda(), torch.tensor(off).int().cuda(), C)
+        got = C.cpu()
+        H.check_outside_untouched(flat, rows, N, N)
+        want = torch.full((rows, N), float("nan"))
+        for b, f, e in want_groups:
+            want[b:f] = A[b:f] @ W[e]
+        assert torch.equal(torch.nan_to_num(got, nan=9e9), torch.nan_to_num(want, nan=9e9)), off
+
+
+def test_grouped_non_finite_rows_stay_in_their_row(gpu_lib):
+    """NaN and Inf in one row of A reach that row of C only; NaN in another
+    group's weights and in rows that no place names reach nothing."""
+    g = gen(22)
+    counts = [20, 5, 70]
+    offsets, rows = spans(counts, 6)
+    A, W = draw(g, rows, 100, integer=True), draw(g, 3, 100, 80, integer=True)
+    A[7, 3], A[40, 99] = float("nan"), float("inf")
+    A[95:] = float("nan")
+    W[1] = float("nan")
+    for trans in (False, True):
+        Wd = (W.transpose(1, 2).contiguous() if trans else W).cuda()
+        C = torch.zeros(rows, 80, device="cuda")
+        gpu_lib.gemm_grouped(A.cuda(), Wd, offsets.cuda(), C, trans_b=trans)
+        got = C.cpu()
+        bad = torch.zeros(rows, dtype=torch.bool)
+        bad[7], bad[20:25] = True, True
+        assert bool(torch.isnan(got[bad]).all())
+        assert bool((~torch.isfinite(got[40])).all())
+        bad[40] = True
+        want = torch.cat([A[:20] @ W[0], torch.zeros(5, 80), A[25:95] @ W[2], torch.zeros(6, 80)])
+        assert torch.equal(got[~bad], want[~bad])
+
+
+# ---- the gradient of the weights --------------------------------------------------
+
+def wgrad_case(lib, counts, M, N, gather_a, gather_b, alpha, beta, integer, seed, pads=(0, 0, 0),
+               shifts=(0, 0, 0), spare=3):
+    g = gen(seed)
+    offsets, rows = spans(counts, spare)
+    G = len(counts)
+    rows_a = max(1, rows // 2) if gather_a else rows + 2
+    rows_b = rows + 4
+    A, B = draw(g, rows_a, M, integer=integer), draw(g, rows_b, N, integer=integer)
+    if not gather_a:
+        A[rows - spare:] = float("nan")    # behind the last place: never used
+    ia = torch.randint(0, rows_a, (rows,), generator=g).int() if gather_a else None
+    ib = torch.randperm(rows_b, generator=g)[:rows].int() if gather_b else None
+    C0 = draw(g, G, M, N, integer=integer)
+    Cd = device(C0 if beta else torch.full_like(C0, float("nan")), pads[2], shifts[2])
+    H.say(f"wgrad counts={counts[:8]} M={M} N={N} gather={gather_a},{gather_b} alpha={alpha} "
+          f"beta={beta} int={integer} pads={pads} shifts={shifts}")
+    lib.gemm_grouped_wgrad(device(A, pads[0], shifts[0]), device(B, pads[1], shifts[1]),
+                           offsets.cuda(), Cd, alpha=alpha, beta=beta,
+                           index_a=None if ia is None else ia.cuda(),
+                           index_b=None if ib is None else ib.cuda())
+    torch.cuda.synchronize()
+    want, mag = torch.zeros(G, M, N).double(), torch.zeros(G, M, N).double()
+    for e, (b, f) in enumerate(zip(offsets.tolist(), offsets.tolist()[1:])):
+        at = torch.arange(b, f)
+        a = A[ia[b:f].long() if gather_a else at].double()
+        c = B[ib[b:f].long() if gather_b else at].double()
+        want[e] = alpha * (a.t() @ c)
+        mag[e] = abs(alpha) * (a.abs().t() @ c.abs())
+    if beta:
+        want, mag = want + beta * C0.double(), mag + abs(beta) * C0.double().abs()
+    check(Cd, want, mag, max(counts) + 4, integer, "wgrad")
+
+
+@pytest.mark.parametrize("counts", list(COUNTS))
+@pytest.mark.parametrize("integer", [True, False])
+def test_wgrad_counts(gpu_lib, counts, integer):
+    M, N = (36, 52) if counts in ("many", "most") else (96, 132)
+    wgrad_case(gpu_lib, COUNTS[counts], M, N, True, True, 1.0, 0.0, integer, 31)
+    wgrad_case(gpu_lib, COUNTS[counts], M, N, False, True, 0.5, -2.0, integer, 32)
+
+
+@pytest.mark.parametrize("M,N", [(1, 1), (1, 200), (200, 1), (8, 260), (260, 8), (16, 64),
+                                 (64, 16), (33, 65), (129, 31), (300, 513), (512, 384)])
+def test_wgrad_sizes(gpu_lib, M, N):
+    for counts in ("few", "skewed", "long"):
+        wgrad_case(gpu_lib, COUNTS[counts], M, N, False, False, 1.0, 0.0, True, 33)
+        wgrad_case(gpu_lib, COUNTS[counts], M, N, True, False, 1.0, 1.0, False, 34)
+
+
+@pytest.mark.parametrize("pads,shifts", [((4, 8, 4), (0, 0, 0)), ((1, 3, 5), (0, 0, 0)),
+                                         ((0, 0, 0), (1, 2, 3)), ((2, 0, 1), (0, 3, 0))])
+def test_wgrad_pitches_and_alignment(gpu_lib, pads, shifts):
+    for counts in ("few", "skewed", "long"):
+        for M, N in ((64, 128), (16, 96)):
+            wgrad_case(gpu_lib, COUNTS[counts], M, N, True, True, 1.0, 1.0, True, 35, pads, shifts)
+
+
+def test_wgrad_long_group(gpu_lib):
+    """Few outputs and many rows: 20000 places in one group, both thin shapes."""
+    for M, N in ((8, 512), (512, 8), (4, 4), (1, 300)):
+        wgrad_case(gpu_lib, [20000, 3], M, N, True, False, 1.0, 0.0, True, 36)
+        wgrad_case(gpu_lib, [3000, 0, 17000], M, N, False, True, 1.0, 0.0, False, 37)
+
+
+def test_wgrad_indexes_outside_count_as_zeros(gpu_lib):
+    g = gen(38)
+    rows, M, N = 60, 64, 64
+    A, B = draw(g, rows, M, integer=True), draw(g, rows, N, integer=True)
+    B[5] = float("nan")   # multiplied by a row that counts as zeros elsewhere: named by nothing
+    ia, ib = torch.arange(rows).int(), torch.arange(rows).int()
+    ia[10], ia[59], ib[5], ib[30] = -1, rows, -7, 2 ** 31 - 1
+    offsets, _ = spans([rows])
+    H.say("wgrad indexes outside")
+    got = gpu_lib.gemm_grouped_wgrad(A.cuda(), B.cuda(), offsets.cuda(), index_a=ia.cuda(),
+                                     index_b=ib.cuda())
+    keep = [i for i in range(rows) if i not in (5, 10, 30, 59)]
+    assert torch.equal(got.cpu()[0], A[keep].t() @ B[keep])
+
+
+def test_wgrad_of_ones_is_the_bias_gradient(gpu_lib):
+    g = gen(39)
+    offsets, rows = spans([0, 40, 3])
+    dC = draw(g, rows, 77, integer=True)
+    got = gpu_lib.gemm_grouped_wgrad(torch.ones(rows, 1, device="cuda"), dC.cuda(),
+                                     offsets.cuda())
+    want = torch.stack([torch.zeros(77), dC[:40].sum(0), dC[40:].sum(0)])
+    assert torch.equal(got.cpu()[:, 0], want)
+
+
+# ---- low-rank adapters ------------------------------------------------------------
+
+def adapters_reference(X, W, down, up, scale, bias, offsets, order, trans):
+    """(Y, H, and the sums of magnitudes of both) in 64 bits."""
+    X, W, down, up, scale = (t.double() for t in (X, W, down, up, scale))
+    if trans:
+        W, down, up = W.t(), down.transpose(1, 2), up.transpose(1, 2)
+    Y, MY = X @ W, X.abs() @ W.abs()
+    if bias is not None:
+        Y, MY = Y + bias.double(), MY + bias.double().abs()
+    Hh = torch.full((order.numel(), down.shape[2]), float("nan")).double()
+    MH = torch.ones_like(Hh)
+    for e, (b, f) in enumerate(zip(offsets.tolist(), offsets.tolist()[1:])):
+        r = order[b:f].long()
+        Hh[b:f] = scale[e] * (X[r] @ down[e])
+        MH[b:f] = scale[e].abs() * (X[r].abs() @ down[e].abs())
+        Y[r] += Hh[b:f] @ up[e]
+        MY[r] += MH[b:f] @ up[e].abs()
+    return Y, Hh, MY, MH
+
+
+def adapters_data(M, N, K, R, adapters, trans, integer, seed, none=True):
+    g = gen(seed)
+    index = torch.randint(-1 if none else 0, adapters, (M,), generator=g).int()
+    X = draw(g, M, K, integer=integer)
+    W = draw(g, *((N, K) if trans else (K, N)), integer=integer)
+    down = draw(g, adapters, *((R, K) if trans else (K, R)), integer=integer)
+    up = draw(g, adapters, *((N, R) if trans else (R, N)), integer=integer)
+    scale = torch.tensor([0.5, 2.0, -1.0, 1.0] * adapters)[:adapters]
+    return index, X, W, down, up, scale, draw(g, N, integer=integer), draw(g, M, N, integer=integer)
+
+
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("M,N,K,R,adapters", [
+    (1, 64, 48, 8, 1), (1, 33, 17, 3, 2), (5, 128, 256, 16, 3), (16, 200, 100, 4, 20),
+    (32, 512, 384, 16, 8), (70, 65, 129, 64, 5), (300, 260, 192, 32, 4), (513, 96, 64, 1, 2),
+    (200, 64, 1000, 24, 3), (40, 31, 40, 100, 3), (1000, 384, 256, 8, 3)])
+def test_adapters(gpu_lib, M, N, K, R, adapters, trans):
+    for integer in (True, False):
+        index, X, W, down, up, scale, bias, _ = adapters_data(M, N, K, R, adapters, trans, integer,
+                                                              41)
+        H.say(f"adapters M={M} N={N} K={K} R={R} adapters={adapters} trans={trans} int={integer}")
+        offsets, order, _ = gpu_lib.group_rows(index.cuda(), adapters)
+        Hd = torch.full((M, R), float("nan"), device="cuda")
+        Y, Hd = gpu_lib.gemm_adapters(X.cuda(), W.cuda(), down.cuda(), up.cuda(), offsets, order,
+                                      H=Hd, trans=trans, scale=scale.cuda(), bias=bias.cuda())
+        wy, wh, my, mh = adapters_reference(X, W, down, up, scale, bias, offsets.cpu(),
+                                            order.cpu(), trans)
+        used = int(offsets[-1])
+        assert bool(torch.isnan(Hd[used:]).all()), "H behind the last place was written"
+        check(Hd[:used], wh[:used], mh[:used], K + 2, integer, "H")
+        check(Y, wy, my, K + R + 6, integer, "Y")
+
+
+def test_adapters_without_scale_bias_or_adapters(gpu_lib):
+    index, X, W, down, up, _, _, _ = adapters_data(50, 96, 64, 8, 3, False, True, 42)
+    ones = torch.ones(3)
+    offsets, order, _ = gpu_lib.group_rows(index.cuda(), 3)
+    Y, _ = gpu_lib.gemm_adapters(X.cuda(), W.cuda(), down.cuda(), up.cuda(), offsets, order)
+    want = adapters_reference(X, W, down, up, ones, None, offsets.cpu(), order.cpu(), False)[0]
+    assert torch.equal(Y.cpu().double(), want)
+    # no row has an adapter; no adapters; rank 0
+    none = torch.full((50,), -1, dtype=torch.int32)
+    offsets, order, _ = gpu_lib.group_rows(none.cuda(), 3)
+    Y, _ = gpu_lib.gemm_adapters(X.cuda(), W.cuda(), down.cuda(), up.cuda(), offsets, order)
+    assert torch.equal(Y.cpu(), X @ W)
+    offsets, order, _ = gpu_lib.group_rows(none.cuda(), 0)
+    Y, _ = gpu_lib.gemm_adapters(X.cuda(), W.cuda(), down[:0].cuda(), up[:0].cuda(), offsets,
+                                 order)
+    assert torch.equal(Y.cpu(), X @ W)
+    offsets, order, _ = gpu_lib.group_rows(index.cuda(), 3)
+    Y, _ = gpu_lib.gemm_adapters(X.cuda(), W.cuda(), down[:, :, :0].contiguous().cuda(),
+                                 up[:, :0].contiguous().cuda(), offsets, order)
+    assert torch.equal(Y.cpu(), X @ W)
+
+
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("M,N,K,R,adapters", [(1, 40, 24, 4, 2), (70, 65, 129, 8, 5),
+                                              (300, 260, 192, 16, 4), (900, 96, 128, 32, 3)])
+def test_adapters_gradients_against_the_formulas(gpu_lib, M, N, K, R, adapters, trans):
+    """Whole numbers: exact.  G = s dY op(U)^T, dX = dY op(W)^T + G op(D)^T,
+    dD = X^T G, dU = H^T dY over each adapter's rows."""
+    index, X, W, down, up, scale, _, dY = adapters_data(M, N, K, R, adapters, trans, True, 43)
+    if M * K * R > 10 ** 6:   # keep every sum below 2^24
+        X, dY = X.clamp(-1, 1), dY.clamp(-1, 1)
+        down, up, W = down.clamp(-1, 1), up.clamp(-1, 1), W.clamp(-1, 1)
+    H.say(f"adapter gradients M={M} N={N} K={K} R={R} trans={trans}")
+    offsets, order, _ = gpu_lib.group_rows(index.cuda(), adapters)
+    args = [t.cuda() for t in (X, W, down, up)]
+    _, Hd = gpu_lib.gemm_adapters(*args, offsets, order, trans=trans, scale=scale.cuda())
+    dX, d_down, d_up = gpu_lib.gemm_adapters_grad(dY.cuda(), *args, offsets, order, Hd,
+                                                  trans=trans, scale=scale.cuda())
+    Xd, Wd, Dd, Ud, dYd = (t.double() for t in (X, W, down, up, dY))
+    if trans:
+        Wd, Dd, Ud = Wd.t(), Dd.transpose(1, 2), Ud.transpose(1, 2)
+    wx, wd, wu = dYd @ Wd.t(), torch.zeros_like(Dd), torch.zeros_like(Ud)
+    for e in range(adapters):
+        r = torch.nonzero(index == e)[:, 0]
+        s = float(scale[e])
+        G = s * dYd[r] @ Ud[e].t()
+        wx[r] += G @ Dd[e].t()
+        wd[e] = Xd[r].t() @ G
+        wu[e] = (s * Xd[r] @ Dd[e]).t() @ dYd[r]
+    assert float(max(wd.abs().max(), wu.abs().max(), wx.abs().max())) < 2 ** 23
+    if trans:
+        wd, wu = wd.transpose(1, 2), wu.transpose(1, 2)
+    for got, want, name in ((dX, wx, "dX"), (d_down, wd, "d_down"), (d_up, wu, "d_up")):
+        check(got, want, None, 0, True, name)
+
+
+def test_adapters_gradients_against_differences(gpu_lib):
+    """The loss sum(dY * Y) is linear in X and in each factor alone, so a
+    difference of whole-number losses is the gradient exactly."""
+    index, X, W, down, up, scale, bias, dY = adapters_data(30, 20, 24, 4, 3, False, True, 44)
+    offsets, order, _ = gpu_lib.group_rows(index.cuda(), 3)
+
+    def forward(X, down, up):
+        return gpu_lib.gemm_adapters(X.cuda(), W.cuda(), down.cuda(), up.cuda(), offsets, order,
+                                     scale=scale.cuda(), bias=bias.cuda())
+
+    def loss(X, down, up):
+        return float((forward(X, down, up)[0].cpu().double() * dY.double()).sum())
+
+    Hd = forward(X, down, up)[1]
+    grads = gpu_lib.gemm_adapters_grad(dY.cuda(), X.cuda(), W.cuda(), down.cuda(), up.cuda(),
+                                       offsets, order, Hd, scale=scale.cuda())
+    params = [X, down, up]
+    g = gen(45)
+    for which, grad in enumerate(grads):
+        for _ in range(6):
+            at = tuple(int(torch.randint(0, d, (1,), generator=g)) for d in params[which].shape)
+            up_, dn_ = [t.clone() for t in params], [t.clone() for t in params]
+            up_[which][at] += 1
+            dn_[which][at] -= 1
+            assert (loss(*up_) - loss(*dn_)) / 2 == float(grad[at]), (which, at)
+
+
+# ---- the operators together ---------------------------------------------------------
+
+def test_expert_layer_forward_and_backward(gpu_lib):
+    """A sparse layer as a user runs it: choices ordered by expert, the up
+    product with bias and ReLU on gathered tokens, the down product scattered to
+    the choices' slots, the choices combined by their weights with
+    gemm_batched, and every gradient, against the formulas in 64 bits."""
+    T, top, G, D, F = 75, 3, 9, 40, 56
+    g = gen(50)
+    X = torch.randn(T, D, generator=g)
+    W1, b1 = torch.randn(G, D, F, generator=g) * D ** -0.5, torch.randn(G, F, generator=g)
+    W2 = torch.randn(G, F, D, generator=g) * F ** -0.5
+    choice = torch.stack([torch.randperm(G, generator=g)[:top] for _ in range(T)])
+    choice[torch.rand(T, top, generator=g) < 0.15] = -1
+    weight = torch.rand(T, top, generator=g)
+    dY = torch.randn(T, D, generator=g)
+    Xd, W1d, b1d, W2d, wd, dYd = (t.cuda() for t in (X, W1, b1, W2, weight, dY))
+    offsets, slot, token = gpu_lib.group_rows(choice.reshape(-1).int().cuda(), G, per_row=top)
+    P = T * top
+    h = gpu_lib.gemm_grouped(Xd, W1d, offsets, torch.zeros(P, F, device="cuda"), bias=b1d,
+                             act=gpu_lib.ACT_RELU, index_a=token)
+    y = gpu_lib.gemm_grouped(h, W2d, offsets, torch.zeros(P, D, device="cuda"), index_c=slot)
+    Y = gpu_lib.gemm_batched(wd.view(T, 1, top), y.view(T, top, D)).view(T, D)
+    # backward: to the slots, through the down product, ReLU and the up product
+    dy = gpu_lib.gemm_batched(wd.view(T, top, 1), dYd.view(T, 1, D)).view(P, D)
+    dw = gpu_lib.gemm_batched(y.view(T, top, D), dYd.view(T, D, 1)).view(T, top)
+    dh = gpu_lib.gemm_grouped(dy, W2d, offsets, torch.zeros(P, F, device="cuda"), trans_b=True,
+                              index_a=slot)
+    dh = dh * (h > 0)
+    dW2 = gpu_lib.gemm_grouped_wgrad(h, dy, offsets, index_b=slot)
+    dW1 = gpu_lib.gemm_grouped_wgrad(Xd, dh, offsets, index_a=token)
+    db1 = gpu_lib.gemm_grouped_wgrad(torch.ones(P, 1, device="cuda"), dh, offsets)[:, 0]
+    dx = gpu_lib.gemm_grouped(dh, W1d, offsets, torch.zeros(P, D, device="cuda"), trans_b=True,
+                              index_c=slot)
+    ones = torch.ones(1, 1, top, device="cuda").expand(T, 1, top)
+    dX = gpu_lib.gemm_batched(ones, dx.view(T, top, D)).view(T, D)
+    # the same in 64 bits by autograd
+    leaves = [t.double().requires_grad_() for t in (X, W1, b1, W2, weight)]
+    x, w1, bb, w2, ww = leaves
+    out = []
+    for t in range(T):
+        v = torch.zeros(D).double()
+        for j in range(top):
+            e = int(choice[t, j])
+            if e >= 0:
+                v = v + ww[t, j] * (torch.relu(x[t] @ w1[e] + bb[e]) @ w2[e])
+        out.append(v)
+    want = torch.stack(out)
+    (want * dY.double()).sum().backward()
+    # each path has fewer than 4 products in a row of at most T * top terms of
+    # magnitude a few; (200 + terms) 2^-24 of the largest value covers them
+    for got, ref, name in ((Y, want, "Y"), (dX, x.grad, "dX"), (dW1, w1.grad, "dW1"),
+                           (db1, bb.grad, "db1"), (dW2, w2.grad, "dW2"), (dw, ww.grad, "dw")):
+        ref = ref.detach()
+        err = float((got.cpu().double() - ref).abs().max())
+        assert err <= 425 * U * float(ref.abs().max()), (name, err)
+
+
+# ---- streams, graphs, repeats --------------------------------------------------------
+
+def together(lib, s):
+    """Every operator once, on the state's tensors."""
+    offsets, slot, token = lib.group_rows(s["index"], 6, per_row=2)
+    h = lib.gemm_grouped(s["x"], s["w"], offsets, index_a=token, act=1, C=s["h"])
+    lib.gemm_grouped_wgrad(s["x"], h, offsets, s["dw"], index_a=token)
+    o2, order, _ = lib.group_rows(s["adapter"], 3)
+    y, hh = lib.gemm_adapters(s["x"], s["wp"], s["down"], s["up"], o2, order, s["y"])
+    dx, dd, du = lib.gemm_adapters_grad(s["y0"], s["x"], s["wp"], s["down"], s["up"], o2, order, hh)
+    return [h, s["dw"], y, dx, dd, du]
+
+
+def state(seed, T=60):
+    g = gen(seed)
+    f = lambda *sh: torch.randn(*sh, generator=g).cuda()
+    s = {"x": f(T, 96), "w": f(6, 96, 160), "wp": f(96, 160), "down": f(3, 96, 8),
+         "up": f(3, 8, 160), "y0": f(T, 160),
+         "index": torch.randint(0, 6, (2 * T,), generator=g).int().cuda(),
+         "adapter": torch.randint(0, 3, (T,), generator=g).int().cuda()}
+    s["h"] = torch.zeros(2 * T, 160, device="cuda")
+    s["dw"] = torch.zeros(6, 96, 160, device="cuda")
+    s["y"] = torch.zeros(T, 160, device="cuda")
+    return s
+
+
+@pytest.mark.parametrize("T", [3, 60, 700])
+def test_captured_graphs_replay_as_eager(gpu_lib, T):
+    """Two graphs of all operators captured on one stream, replayed in turn with
+    new inputs and eager work between the replays."""
+    stream = torch.cuda.Stream()
+    states = [state(60, T), state(61, T)]
+    graphs, outs = [], []
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        for s in states:
+            together(gpu_lib, s)
+    torch.cuda.synchronize()
+    H.say(f"capture T={T}")
+    for s in states:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            outs.append(together(gpu_lib, s))
+        graphs.append(graph)
+    torch.cuda.synchronize()
+    for rep in range(3):
+        for i, s in enumerate(states):
+            fresh = state(70 + 2 * rep + i, T)
+            for k in s:
+                s[k].copy_(fresh[k])
+            torch.cuda.synchronize()
+            graphs[i].replay()
+            torch.cuda.synchronize()
+            got = [t.clone() for t in outs[i]]
+            want = together(gpu_lib, fresh)
+            torch.cuda.synchronize()
+            for a, b in zip(got, want):
+                assert torch.equal(a, b), f"replay {rep} of graph {i} differs"
+
+
+def test_two_streams_at_once(gpu_lib):
+    """Calls on two streams overlap without sharing anything."""
+    a, b = state(80, 700), state(81, 700)
+    want = [[t.clone() for t in together(gpu_lib, s)] for s in (a, b)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        got = []
+        for s, st in zip((a, b), streams):
+            with torch.cuda.stream(st):
+                got.append(together(gpu_lib, s))
+        torch.cuda.synchronize()
+        for x, y in zip(got, want):
+            for p, q in zip(x, y):
+                assert torch.equal(p, q)
