@@ -1,0 +1,303 @@
+// One output tile of a grouped product on the CDNA4 matrix cores, its K-tiles
+// copied straight from global memory into LDS (gfx950).
+//
+// The tiles, LDS layouts, swizzles, fragments and the order of copies, reads and
+// MFMAs are those of the extended-operation kernel (kernels_mfma_ex_dma.hip):
+// operand "KC" has k contiguous and lies in LDS as [r][k] with swizzled 16-byte
+// chunks, operand "RC" has its rows r contiguous and lies as [k][r]; two LDS
+// buffers, one barrier for each K-tile.  What differs:
+//
+//   - the rows of a KC operand, or the k of an RC operand, may be gathered
+//     through an index;
+//   - whatever lies outside (a row that is not there, k past the end, an index
+//     outside its matrix) is copied from a block of zeros in global memory, so
+//     K and the edges need no padding and no value outside is ever read;
+//   - a lane copies V floats at once: 4 where both operands allow it, else 1,
+//     which any pitch and alignment does.
+#pragma once
+
+#include <cstdint>
+#include <type_traits>
+
+#include "grouped_internal.h"
+#include "lds_dma.h"
+#include "mfma_common.h"
+
+namespace gemmf32 {
+namespace grouped {
+
+using namespace mfma;
+
+// What copies of absent values read.
+static __device__ __attribute__((aligned(16))) const float kZeros[4] = {0.f, 0.f, 0.f, 0.f};
+
+// Lane l copies V floats from g into LDS at lds_wave + V l.  The address of
+// LDS comes from M0, saved and restored around the copy; written as inline
+// assembly so that the kernel's own waits alone order copies and reads.
+template <int V>
+__device__ __forceinline__ void copy_to_lds(const float* g, float* lds_wave) {
+  if constexpr (V == 4) {
+    load_lds16(g, lds_wave);
+  } else {
+    const uint32_t lds_addr = __builtin_amdgcn_readfirstlane(
+        (uint32_t)(uintptr_t)((__attribute__((address_space(3))) float*)lds_wave));
+    uint32_t saved;
+    asm volatile(
+        "s_mov_b32 %0, m0\n\t"
+        "s_mov_b32 m0, %2\n\t"
+        "global_load_lds_dword %1, off\n\t"
+        "s_mov_b32 m0, %0"
+        : "=&s"(saved)
+        : "v"(g), "s"(lds_addr)
+        : "memory");
+  }
+}
+
+// The rows an operand is gathered by: row i of the operand is row at(i) of the
+// matrix, -1 where there is none.
+struct Gather {
+  const int* index;   // NULL: the identity
+  int limit;          // rows of the matrix
+  __device__ __forceinline__ int at(int i, int end) const {
+    if (i >= end) return -1;
+    const int r = index ? index[i] : i;
+    return r >= 0 && r < limit ? r : -1;
+  }
+};
+
+// One operand's K-tile: R rows by BK, copied by kWaves waves, V floats a lane.
+// kGatherK: k itself is gathered (an RC operand whose k are places).
+template <int R, int BK, int kWaves, bool KC, int V, bool kGatherK = false>
+struct Operand {
+  static_assert(!(KC && kGatherK), "gathered k needs the rows contiguous");
+  static constexpr int kLds = R * BK;
+  static constexpr int kCopies = R * BK / V / (kWaves * 64);   // copies a lane makes
+  static_assert(R * BK % (V * kWaves * 64) == 0, "copies divide evenly over the threads");
+  static_assert(KC || R % 64 == 0, "the [k][r] swizzle needs 64-wide rows");
+
+  const float* src[kCopies];   // this lane's place of each copy at k = 0
+  int k_of[kCopies];           // and its k in the K-tile; a huge value: absent
+  int row[kGatherK ? kCopies : 1];   // gathered k: the matrix row of the next K-tile's copy
+  static constexpr int kAbsent = 0x7fffffff;
+
+  // (r, k) of the first of the V floats at LDS float `f`
+  __device__ __forceinline__ static void logical(int f, int& r, int& k) {
+    if constexpr (KC) {
+      r = f / BK;
+      const int p = f % BK;
+      k = 4 * ((p >> 2) ^ swz_a<BK / 4>(r)) + (p & 3);
+    } else {
+      k = f / R;
+      r = (f % R) ^ swz_b(k);
+    }
+  }
+  // KC with gathered rows: row_at(r) is the matrix row of tile row r, or -1
+  template <class RowAt>
+  __device__ __forceinline__ void init_kc(const float* base, int64_t ld, int wave, int lane,
+                                          RowAt row_at) {
+#pragma unroll
+    for (int v = 0; v < kCopies; ++v) {
+      int r, k;
+      logical(((v * kWaves + wave) * 64 + lane) * V, r, k);
+      const int m = row_at(r);
+      src[v] = m >= 0 ? base + (int64_t)m * ld + k : kZeros;
+      k_of[v] = m >= 0 ? k : kAbsent;
+    }
+  }
+  // RC: columns r0 + r of a matrix with `cols` columns, row k at k * ld
+  __device__ __forceinline__ void init_rc(const float* base, int64_t ld, int r0, int cols,
+                                          int wave, int lane) {
+#pragma unroll
+    for (int v = 0; v < kCopies; ++v) {
+      int r, k;
+      logical(((v * kWaves + wave) * 64 + lane) * V, r, k);
+      const bool in = r < cols - r0;
+      src[v] = in ? base + r0 + r + (kGatherK ? 0 : (int64_t)k * ld) : kZeros;
+      k_of[v] = in ? k : kAbsent;
+    }
+  }
+  // gathered k: fetch the matrix rows of the K-tile at k0 (places first + k)
+  __device__ __forceinline__ void fetch_rows(const Gather& ga, int first, int k0, int k_end) {
+    if constexpr (kGatherK) {
+#pragma unroll
+      for (int v = 0; v < kCopies; ++v)
+        row[v] = k_of[v] < k_end - k0 ? ga.at(first + k0 + k_of[v], first + k_end) : -1;
+    }
+  }
+  __device__ __forceinline__ void copy(int v, float* lds, int64_t ld, int k0, int k_end,
+                                       int wave) const {
+    const float* g;
+    if constexpr (kGatherK) {
+      g = row[v] >= 0 ? src[v] + (int64_t)row[v] * ld : kZeros;
+    } else {
+      const int64_t step = KC ? (int64_t)k0 : (int64_t)k0 * ld;
+      g = k_of[v] < k_end - k0 ? src[v] + step : kZeros;
+    }
+    copy_to_lds<V>(g, lds + (v * kWaves + wave) * (64 * V));
+  }
+
+  // Fragment reads of k group q (8 k), as in the extended-operation kernel.
+  static constexpr int units(int frags) { return KC ? frags : 2 * frags; }
+  template <int kFrag>
+  __device__ __forceinline__ static void read(float (&f)[4][kFrag], const float* lds, int wr,
+                                              int lr, int lk, int q, int unit) {
+    if constexpr (KC) {
+      const int r = wr + 32 * unit + lr;
+      const float4 x =
+          *reinterpret_cast<const float4*>(&lds[r * BK + 4 * ((2 * q + lk) ^ swz_a<BK / 4>(r))]);
+      f[0][unit] = x.x;
+      f[1][unit] = x.y;
+      f[2][unit] = x.z;
+      f[3][unit] = x.w;
+    } else {
+      const int i = unit / 2, s0 = 2 * (unit % 2);
+      const int col = (wr + 32 * i + lr) ^ (lk << 5);
+      f[s0][i] = lds[(8 * q + 4 * lk + s0) * R + col];
+      f[s0 + 1][i] = lds[(8 * q + 4 * lk + s0 + 1) * R + col];
+    }
+  }
+};
+
+// The K loop of a BM x BN tile, wave tiles WM x WN, over k in [0, k_end).
+// pool: 2 (BM + BN) BK floats of LDS.  k_end <= 0 gives zeros.
+template <int BM, int BN, int BK, int WM, int WN, class OpA, class OpB>
+__device__ __forceinline__ void k_loop(float* pool, OpA& opa, OpB& opb, const Gather& ga,
+                                       const Gather& gb, int first, int64_t lda, int64_t ldb,
+                                       int k_end, int wave, int lane,
+                                       floatx16 (&acc)[WM / 32][WN / 32]) {
+  constexpr int kWavesM = BM / WM;
+  constexpr int kFragM = WM / 32, kFragN = WN / 32;
+  static_assert(WM % 32 == 0 && WN % 32 == 0 && BM % WM == 0 && BN % WN == 0, "32x32 blocks");
+  static_assert(BK % 16 == 0, "an even number of 8-k groups in a K-tile");
+  float* const lds_a0 = pool;
+  float* const lds_a1 = lds_a0 + OpA::kLds;
+  float* const lds_b0 = lds_a1 + OpA::kLds;
+  float* const lds_b1 = lds_b0 + OpB::kLds;
+  constexpr int kTileCopies = OpA::kCopies + OpB::kCopies;
+  auto copy_one = [&](float* la, float* lb, int k0, int idx) {
+    if (idx < OpA::kCopies) {
+      opa.copy(idx, la, lda, k0, k_end, wave);
+    } else {
+      opb.copy(idx - OpA::kCopies, lb, ldb, k0, k_end, wave);
+    }
+  };
+  auto fetch_rows = [&](int k0) {
+    opa.fetch_rows(ga, first, k0, k_end);
+    opb.fetch_rows(gb, first, k0, k_end);
+  };
+  const int wr_a = (wave % kWavesM) * WM, wr_b = (wave / kWavesM) * WN;
+  const int lr = lane & 31, lk = lane >> 5;
+  struct Frag {
+    float a[4][kFragM];
+    float b[4][kFragN];
+  };
+  constexpr int kUnitsA = OpA::units(kFragM), kUnitsB = OpB::units(kFragN);
+  constexpr int kReadsPerGroup = kUnitsA + kUnitsB;
+  auto read_one = [&](Frag& f, const float* la, const float* lb, int q, int idx) {
+    if (idx < kUnitsA) {
+      OpA::template read<kFragM>(f.a, la, wr_a, lr, lk, q, idx);
+    } else {
+      OpB::template read<kFragN>(f.b, lb, wr_b, lr, lk, q, idx - kUnitsA);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kFragM; ++i)
+#pragma unroll
+    for (int j = 0; j < kFragN; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+  // one block per wave: odd k-steps go to a second accumulator, added after
+  // the loop (a fixed order: even steps + odd steps)
+  constexpr bool kDual = kFragM * kFragN == 1;
+  floatx16 acc_odd = {};
+  auto mfma_one = [&](const Frag& f, int idx) {
+    const int s = idx / (kFragM * kFragN);
+    const int i = (idx / kFragN) % kFragM, j = idx % kFragN;
+    if constexpr (kDual) {
+      if (s & 1) {
+        acc_odd = __builtin_amdgcn_mfma_f32_32x32x2f32(f.a[s][i], f.b[s][j], acc_odd, 0, 0, 0);
+        return;
+      }
+    }
+    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(f.a[s][i], f.b[s][j], acc[i][j], 0, 0, 0);
+  };
+
+  constexpr int kGroups = BK / 8;
+  constexpr int kMfmaPerGroup = 4 * kFragM * kFragN;
+  constexpr int kHalf = kMfmaPerGroup / 2;
+  constexpr int kReadsPerMfma = (kReadsPerGroup + kMfmaPerGroup - 1) / kMfmaPerGroup;
+  constexpr int kReadsPer = (kReadsPerGroup + kHalf - 1) / kHalf;
+  constexpr int kCopiesPer = (kTileCopies + kHalf - 1) / kHalf;
+
+  // Branch-free steps: the copies of a K-tile past the end re-read the last
+  // one into the buffer no longer needed; the last step reads fragments it does
+  // not use.  One K-tile of zeros where there is no k.
+  const int ktiles = max(1, (k_end + BK - 1) / BK);
+  const int last_k0 = (ktiles - 1) * BK;
+  Frag f0, f1;
+  fetch_rows(0);
+#pragma unroll
+  for (int idx = 0; idx < kTileCopies; ++idx) copy_one(lds_a0, lds_b0, 0, idx);
+  fetch_rows(min(BK, last_k0));
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();
+#pragma unroll
+  for (int idx = 0; idx < kReadsPerGroup; ++idx) read_one(f0, lds_a0, lds_b0, 0, idx);
+#pragma unroll
+  for (int idx = 0; idx < kTileCopies; ++idx) copy_one(lds_a1, lds_b1, min(BK, last_k0), idx);
+
+  auto step = [&](int t, auto cur_tag) {
+    constexpr int kCur = decltype(cur_tag)::value;
+    float* la = kCur ? lds_a1 : lds_a0;
+    float* lb = kCur ? lds_b1 : lds_b0;
+    float* la_next = kCur ? lds_a0 : lds_a1;
+    float* lb_next = kCur ? lds_b0 : lds_b1;
+    const int k_next2 = min((t + 2) * BK, last_k0);
+    fetch_rows(k_next2);
+#pragma unroll
+    for (int q = 0; q < kGroups; ++q) {
+      Frag& fc = (q & 1) ? f1 : f0;
+      Frag& fn = (q & 1) ? f0 : f1;
+      if (q < kGroups - 1) {
+#pragma unroll
+        for (int i = 0; i < kMfmaPerGroup; ++i) {
+          mfma_one(fc, i);
+#pragma unroll
+          for (int r = 0; r < kReadsPerMfma; ++r)
+            if (i * kReadsPerMfma + r < kReadsPerGroup)
+              read_one(fn, la, lb, q + 1, i * kReadsPerMfma + r);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kHalf; ++i) mfma_one(fc, i);
+        __builtin_amdgcn_sched_barrier(0);
+        // the next K-tile is in LDS and every wave is done with this one
+        __builtin_amdgcn_s_waitcnt(0);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kHalf; ++i) {
+          mfma_one(fc, kHalf + i);
+#pragma unroll
+          for (int r = 0; r < kReadsPer; ++r)
+            if (i * kReadsPer + r < kReadsPerGroup)
+              read_one(fn, la_next, lb_next, 0, i * kReadsPer + r);
+#pragma unroll
+          for (int l = 0; l < kCopiesPer; ++l)
+            if (i * kCopiesPer + l < kTileCopies) copy_one(la, lb, k_next2, i * kCopiesPer + l);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+    }
+  };
+  for (int t = 0; t < ktiles; t += 2) {
+    step(t, std::integral_constant<int, 0>{});
+    if (t + 1 < ktiles) step(t + 1, std::integral_constant<int, 1>{});
+  }
+  // no copy into LDS may still be in flight when the pool is used again
+  __builtin_amdgcn_s_waitcnt(0);
+  if constexpr (kDual) acc[0][0] += acc_odd;
+}
+
+}  // namespace grouped
+}  // namespace gemmf32

@@ -1,144 +1,123 @@
 // Products whose rows belong to different weights (gfx950): for every place i
-// of group g, C[ic(i)] = act(alpha s_g A[ia(i)] op(B_g) + beta C[ic(i)] + bias_g),
-// and the gradient of the weights, C_g = alpha sum_i A[ia(i)]^T B[ib(i)] + beta C_g.
+// of group g, C[ic(i)] = act(alpha s_g A[ia(i)] op(B_g) + beta C[ic(i)] + bias_g).
 //
 // The group sizes are known on the device only, so the grid covers the most row
-// tiles that the places can need and each workgroup finds its tile from the
-// offsets.  64 x 64 tiles, 4 waves of one 32 x 32 MFMA block, K-tiles of 16
-// staged through registers into LDS with every element guarded: any size,
-// pitch and alignment.
-#include "grouped_internal.h"
-#include "mfma_common.h"
+// tiles that the places can need; each workgroup finds its tile from the
+// offsets (a scan of 64 groups in a wave) and ends at once if there is none.
+#include "grouped_tile.h"
 
 namespace gemmf32 {
 namespace {
 
-using namespace mfma;
+using namespace grouped;
 
-constexpr int kT = 64, kBK = 16, kPad = 4;
-
-// One K-tile of an operand: 64 rows (of A, or columns of op(B)) by 16 k in LDS
-// as [k][row], fetched by get(row, k).
-template <class Get>
-__device__ __forceinline__ void stage(float (*lds)[kT + kPad], bool row_fast, Get get) {
-  const int tid = threadIdx.x;
+// The update of a wave's blocks, rows of C through row_c (LDS; -1: not
+// written).  The plain product stores the sums themselves.
+template <int KFM, int KFN>
+__device__ __forceinline__ void store_rows(const floatx16 (&acc)[KFM][KFN],
+                                           const GroupedProblem& p, const Epilogue& ep,
+                                           float scale, const int* row_c, int row0, int col0,
+                                           int lane) {
+  const int lr = lane & 31, lk = lane >> 5;
+  const bool direct = scale == 1.f && ep.alpha == 1.f && ep.beta == 0.f && !ep.bias && ep.act == 0;
 #pragma unroll
-  for (int v = 0; v < kT * kBK / 256; ++v) {
-    const int e = v * 256 + tid;
-    const int r = row_fast ? e % kT : e / kBK;
-    const int k = row_fast ? e / kT : e % kBK;
-    lds[k][r] = get(r, k);
+  for (int i = 0; i < KFM; ++i) {
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const int c = row_c[row0 + 32 * i + 4 * lk + 8 * (r >> 2) + (r & 3)];
+      if (c < 0) continue;
+      float* out = p.C + c * p.ldc;
+#pragma unroll
+      for (int j = 0; j < KFN; ++j) {
+        const int col = col0 + 32 * j + lr;
+        if (col < p.N)
+          out[col] = direct ? acc[i][j][r]
+                            : epilogue_apply(ep, scale * acc[i][j][r], out + col, col);
+      }
+    }
   }
 }
 
-__device__ __forceinline__ void multiply(floatx16& acc, const float (*la)[kT + kPad],
-                                         const float (*lb)[kT + kPad], int wave, int lane) {
-  const int wm = (wave & 1) * 32, wn = (wave >> 1) * 32, lr = lane & 31, lk = lane >> 5;
-#pragma unroll
-  for (int k = 0; k < kBK; k += 2)
-    acc = __builtin_amdgcn_mfma_f32_32x32x2f32(la[k + lk][wm + lr], lb[k + lk][wn + lr], acc, 0,
-                                               0, 0);
+template <int BM, int BN, int BK, int WM, int WN, bool kTB, int V>
+__device__ __forceinline__ void grouped_tile(float* pool, const int* row_a, const int* row_c,
+                                             const GroupedProblem& p, const Epilogue& ep, int g,
+                                             int n0, int wave, int lane) {
+  constexpr int kWaves = (BM / WM) * (BN / WN);
+  const float* B = p.B + g * p.sb;
+  Operand<BM, BK, kWaves, true, V> opa;
+  Operand<BN, BK, kWaves, kTB, V> opb;
+  opa.init_kc(p.A, p.lda, wave, lane, [&](int r) { return row_a[r]; });
+  if constexpr (kTB) {
+    opb.init_kc(B, p.ldb, wave, lane, [&](int r) { return r < p.N - n0 ? n0 + r : -1; });
+  } else {
+    opb.init_rc(B, p.ldb, n0, p.N, wave, lane);
+  }
+  floatx16 acc[WM / 32][WN / 32];
+  k_loop<BM, BN, BK, WM, WN>(pool, opa, opb, Gather{}, Gather{}, 0, p.lda, p.ldb, p.K, wave, lane,
+                             acc);
+  const float scale = p.gscale ? p.gscale[g] : 1.f;
+  Epilogue e = ep;
+  if (e.bias) e.bias += g * p.sbias;
+  store_rows(acc, p, e, scale, row_c, (wave % (BM / WM)) * WM, n0 + (wave / (BM / WM)) * WN, lane);
 }
 
-__global__ void __launch_bounds__(256)
+template <int BM, int BN, int BK, int WM, int WN, bool kTB, int V, int kMinWaves>
+__global__ void __launch_bounds__((BM / WM) * (BN / WN) * 64)
+    __attribute__((amdgpu_waves_per_eu(kMinWaves)))
     grouped_kernel(GroupedProblem p, Epilogue ep, int tiles_n, unsigned cap) {
-  __shared__ float la[kBK][kT + kPad], lb[kBK][kT + kPad];
-  __shared__ int row_a[kT], row_c[kT];
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-  RowTiles rt{p.offsets, p.groups, p.rows, kT, lane, cap, 0};
-  const unsigned total = rt.total();
+  __shared__ __attribute__((aligned(16))) float pool[2 * (BM + BN) * BK];
+  __shared__ int row_a[BM], row_c[BM];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  RowTiles rt{p.offsets, p.groups, p.rows, BM, lane, cap, 0};
+  const unsigned total = rt.total(), tiles = total * (unsigned)tiles_n;
+  // each XCD takes a contiguous range of the tiles that there are
   const unsigned id = tile_id();
-  const unsigned t = id / tiles_n;
+  const unsigned x = id % kNumXcd, q = tiles / kNumXcd, rem = tiles % kNumXcd;
+  if (id / kNumXcd >= q + (x < rem ? 1u : 0u)) return;
+  int tm, tn;
+  tile_coords((int)(x * q + min(x, rem) + id / kNumXcd), (int)total, tiles_n, tm, tn);
   int g = 0, begin = 0, end = 0;
   unsigned first = 0;
-  if (t >= total || !rt.find(t, g, begin, end, first)) return;
-  const int m0 = begin + (int)(t - first) * kT, n0 = (int)(id % tiles_n) * kT;
-  if (tid < kT) {
-    const int i = m0 + tid;
-    int a = -1, c = -1;
-    if (i < end) {
-      a = p.ia ? p.ia[i] : i;
-      c = p.ic ? p.ic[i] : i;
-      if (a < 0 || a >= p.rows_a) a = -1;
-      if (c < 0 || c >= p.rows_c) c = -1;
-    }
-    row_a[tid] = a;
-    row_c[tid] = c;
-  }
-  const float* B = p.B + g * p.sb;
-  floatx16 acc = {};
-  for (int k0 = 0; k0 < p.K; k0 += kBK) {
-    __syncthreads();
-    stage(la, false, [&](int r, int k) {
-      const int a = row_a[r];
-      return a >= 0 && k0 + k < p.K ? p.A[a * p.lda + k0 + k] : 0.f;
-    });
-    stage(lb, !p.tb, [&](int r, int k) {
-      if (n0 + r >= p.N || k0 + k >= p.K) return 0.f;
-      return p.tb ? B[(n0 + r) * p.ldb + k0 + k] : B[(k0 + k) * p.ldb + n0 + r];
-    });
-    __syncthreads();
-    multiply(acc, la, lb, wave, lane);
+  if (!rt.find((unsigned)tm, g, begin, end, first)) return;
+  const int m0 = begin + (tm - (int)first) * BM;
+  const Gather ga{p.ia, p.rows_a}, gc{p.ic, p.rows_c};
+  if (tid < BM) {
+    row_a[tid] = ga.at(m0 + tid, end);
+    row_c[tid] = gc.at(m0 + tid, end);
   }
   __syncthreads();
-  const float scale = p.gscale ? p.gscale[g] : 1.f;
-  if (ep.bias) ep.bias += g * p.sbias;
-  const int col = n0 + (wave >> 1) * 32 + (lane & 31);
-  if (col >= p.N) return;
-#pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    const int c = row_c[(wave & 1) * 32 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)];
-    if (c < 0) continue;
-    float* out = p.C + c * p.ldc + col;
-    *out = epilogue_apply(ep, scale * acc[r], out, col);
-  }
+  grouped_tile<BM, BN, BK, WM, WN, kTB, V>(pool, row_a, row_c, p, ep, g, tn * BN, wave, lane);
 }
 
-__global__ void __launch_bounds__(256)
-    grouped_wgrad_kernel(GroupedProblem p, Epilogue ep, int tiles_n) {
-  __shared__ float la[kBK][kT + kPad], lb[kBK][kT + kPad];
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-  const int g = blockIdx.y;
-  int begin, end;
-  group_span(p.offsets, g, p.rows, begin, end);
-  const int m0 = (int)(blockIdx.x / tiles_n) * kT, n0 = (int)(blockIdx.x % tiles_n) * kT;
-  floatx16 acc[1][1] = {};
-  for (int i0 = begin; i0 < end; i0 += kBK) {
-    __syncthreads();
-    stage(la, true, [&](int r, int k) {
-      if (m0 + r >= p.M || k >= end - i0) return 0.f;
-      const int a = p.ia ? p.ia[i0 + k] : i0 + k;
-      return a >= 0 && a < p.rows_a ? p.A[a * p.lda + m0 + r] : 0.f;
-    });
-    stage(lb, true, [&](int r, int k) {
-      if (n0 + r >= p.N || k >= end - i0) return 0.f;
-      const int b = p.ib ? p.ib[i0 + k] : i0 + k;
-      return b >= 0 && b < p.rows_b ? p.B[b * p.ldb + n0 + r] : 0.f;
-    });
-    __syncthreads();
-    multiply(acc[0][0], la, lb, wave, lane);
+template <int BM, int BN, int BK, int WM, int WN, int V, int kMinWaves>
+hipError_t launch(const GroupedProblem& p, const Epilogue& e, hipStream_t s) {
+  const int64_t tiles_n = ((int64_t)p.N + BN - 1) / BN;
+  const int64_t cap = most_row_tiles(p.rows, p.groups, BM);
+  if (cap * tiles_n > 0x7fffffff) return hipErrorInvalidConfiguration;
+  const dim3 grid = tile_grid(cap * tiles_n), block((BM / WM) * (BN / WN) * 64);
+  if (p.tb) {
+    hipLaunchKernelGGL((grouped_kernel<BM, BN, BK, WM, WN, true, V, kMinWaves>), grid, block, 0, s,
+                       p, e, (int)tiles_n, (unsigned)cap);
+  } else {
+    hipLaunchKernelGGL((grouped_kernel<BM, BN, BK, WM, WN, false, V, kMinWaves>), grid, block, 0, s,
+                       p, e, (int)tiles_n, (unsigned)cap);
   }
-  store_blocks<1, 1>(acc, p.C + g * p.sc, p.ldc, p.M, p.N,
-                     m0 + (wave & 1) * 32, n0 + (wave >> 1) * 32, lane, false, ep);
+  return hipGetLastError();
 }
+
+bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
 }  // namespace
 
 hipError_t launch_grouped(const GroupedProblem& p, const Epilogue& e, hipStream_t s) {
-  const int64_t tiles_n = (p.N + kT - 1) / kT;
-  const int64_t cap = most_row_tiles(p.rows, p.groups, kT);
-  if (cap * tiles_n > 0x7fffffff) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL(grouped_kernel, tile_grid(cap * tiles_n), dim3(256), 0, s, p, e,
-                     (int)tiles_n, (unsigned)cap);
-  return hipGetLastError();
-}
-
-hipError_t launch_grouped_wgrad(const GroupedProblem& p, const Epilogue& e, hipStream_t s) {
-  const int64_t tiles_n = (p.N + kT - 1) / kT, tiles_m = (p.M + kT - 1) / kT;
-  if (tiles_m * tiles_n > kGridX) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL(grouped_wgrad_kernel, dim3((unsigned)(tiles_m * tiles_n), (unsigned)p.groups),
-                     dim3(256), 0, s, p, e, (int)tiles_n);
-  return hipGetLastError();
+  // 16-byte copies need whole chunks of both operands inside: bases, pitches
+  // and strides of 16 bytes, and the contiguous sizes multiples of 4
+  const bool wide = aligned16(p.A) && aligned16(p.B) && p.lda % 4 == 0 && p.ldb % 4 == 0 &&
+                    (p.groups == 1 || p.sb % 4 == 0) && p.K % 4 == 0 && (p.tb || p.N % 4 == 0);
+  if (!wide) return launch<64, 64, 16, 32, 32, 1, 4>(p, e, s);
+  if ((int64_t)p.rows * p.N < (INT64_C(1) << 20)) return launch<64, 64, 32, 32, 32, 4, 4>(p, e, s);
+  return launch<128, 128, 32, 64, 32, 4, 2>(p, e, s);
 }
 
 }  // namespace gemmf32

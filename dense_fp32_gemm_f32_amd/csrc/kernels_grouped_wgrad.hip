@@ -1,0 +1,66 @@
+// The gradient of the weights of a grouped product (gfx950): for every group g,
+// over its places i, C_g = alpha sum_i A[ia(i)]^T B[ib(i)] + beta C_g.
+//
+// Both operands have their rows contiguous and are gathered along k (the
+// places), so a K-tile's matrix rows are fetched one K-tile ahead of its copies.
+#include "grouped_tile.h"
+
+namespace gemmf32 {
+namespace {
+
+using namespace grouped;
+
+template <int BM, int BN, int BK, int WM, int WN, int V, int kMinWaves>
+__global__ void __launch_bounds__((BM / WM) * (BN / WN) * 64)
+    __attribute__((amdgpu_waves_per_eu(kMinWaves)))
+    grouped_wgrad_kernel(GroupedProblem p, Epilogue ep, int tiles_m, int tiles_n) {
+  constexpr int kWaves = (BM / WM) * (BN / WN);
+  __shared__ __attribute__((aligned(16))) float pool[2 * (BM + BN) * BK];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int tiles = tiles_m * tiles_n;
+  const int id = xcd_contiguous_id((int)tile_id(), tiles * p.groups);
+  if ((int)tile_id() >= tiles * p.groups) return;
+  const int g = id / tiles;
+  int tm, tn;
+  tile_coords(id - g * tiles, tiles_m, tiles_n, tm, tn);
+  int begin, end;
+  group_span(p.offsets, g, p.rows, begin, end);
+  begin = __builtin_amdgcn_readfirstlane(begin);
+  end = __builtin_amdgcn_readfirstlane(end);
+  Operand<BM, BK, kWaves, false, V, true> opa;
+  Operand<BN, BK, kWaves, false, V, true> opb;
+  opa.init_rc(p.A, p.lda, tm * BM, p.M, wave, lane);
+  opb.init_rc(p.B, p.ldb, tn * BN, p.N, wave, lane);
+  floatx16 acc[WM / 32][WN / 32];
+  k_loop<BM, BN, BK, WM, WN>(pool, opa, opb, Gather{p.ia, p.rows_a}, Gather{p.ib, p.rows_b}, begin,
+                             p.lda, p.ldb, end - begin, wave, lane, acc);
+  store_blocks<WM / 32, WN / 32>(acc, p.C + g * p.sc, p.ldc, p.M, p.N,
+                                 tm * BM + (wave % (BM / WM)) * WM,
+                                 tn * BN + (wave / (BM / WM)) * WN, lane, false, ep);
+}
+
+template <int BM, int BN, int BK, int WM, int WN, int V, int kMinWaves>
+hipError_t launch(const GroupedProblem& p, const Epilogue& e, hipStream_t s) {
+  const int64_t tiles_m = ((int64_t)p.M + BM - 1) / BM, tiles_n = ((int64_t)p.N + BN - 1) / BN;
+  const int64_t n = tiles_m * tiles_n * p.groups;
+  if (n > 0x7fffffff) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL((grouped_wgrad_kernel<BM, BN, BK, WM, WN, V, kMinWaves>), tile_grid(n),
+                     dim3((BM / WM) * (BN / WN) * 64), 0, s, p, e, (int)tiles_m, (int)tiles_n);
+  return hipGetLastError();
+}
+
+bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+
+}  // namespace
+
+hipError_t launch_grouped_wgrad(const GroupedProblem& p, const Epilogue& e, hipStream_t s) {
+  const bool wide = aligned16(p.A) && aligned16(p.B) && p.lda % 4 == 0 && p.ldb % 4 == 0 &&
+                    p.M % 4 == 0 && p.N % 4 == 0;
+  if (!wide) return launch<64, 64, 16, 32, 32, 1, 4>(p, e, s);
+  if ((int64_t)p.M * p.N * p.groups < (INT64_C(1) << 22))
+    return launch<64, 64, 32, 32, 32, 4, 4>(p, e, s);
+  return launch<128, 128, 32, 64, 32, 4, 2>(p, e, s);
+}
+
+}  // namespace gemmf32
