@@ -33,6 +33,8 @@ struct GroupedProblem {
 };
 
 hipError_t launch_grouped(const GroupedProblem& p, const Epilogue& e, hipStream_t s);
+// the same for few rows in a group, or few columns (kernels_grouped_rows.hip)
+hipError_t launch_grouped_rows(const GroupedProblem& p, const Epilogue& e, hipStream_t s);
 hipError_t launch_grouped_wgrad(const GroupedProblem& p, const Epilogue& e, hipStream_t s);
 
 // offsets, order and rows (may be NULL) of gemm_f32_group_rows

@@ -111,6 +111,9 @@ bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 }  // namespace
 
 hipError_t launch_grouped(const GroupedProblem& p, const Epilogue& e, hipStream_t s) {
+  // few rows in a group, or few columns: bound by one read of B or of A
+  if (p.rows <= 24 * (int64_t)p.groups || p.rows <= 64 || p.N <= 64)
+    return launch_grouped_rows(p, e, s);
   // 16-byte copies need whole chunks of both operands inside: bases, pitches
   // and strides of 16 bytes, and the contiguous sizes multiples of 4
   const bool wide = aligned16(p.A) && aligned16(p.B) && p.lda % 4 == 0 && p.ldb % 4 == 0 &&
