@@ -496,44 +496,107 @@ def selected_kernel(A, B, C=None) -> str:
 
 
 # ---- grouped products --------------------------------------------------------
+# (short calls: the checks below read each tensor's sizes and strides once)
+
+def _stream(device):
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
 
 def _index(t, name, device, count=None):
     """Pointer of a contiguous 1-D int32 tensor on ``device`` (0 for None)."""
     import torch
     if t is None:
         return 0
-    if t.dtype != torch.int32 or t.dim() != 1 or (t.numel() > 1 and t.stride(0) != 1):
+    if t.dtype is not torch.int32 or t.dim() != 1 or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous 1-D int32 tensor")
     if t.device != device:
         raise ValueError(f"{name} must be on {device} (got {t.device})")
-    if count is not None and t.numel() != count:
-        raise ValueError(f"{name} must have {count} entries, got {t.numel()}")
+    if count is not None and t.shape[0] != count:
+        raise ValueError(f"{name} must have {count} entries, got {t.shape[0]}")
     return t.data_ptr()
 
 
-def _stack(t, name, device, shape):
-    """(pointer, pitch, stride) of a 3-D float32 tensor: one matrix per group."""
+def _rows(rows, cols, s0, s1, name):
+    """Pitch of a rows x cols matrix with these strides."""
+    if cols > 1 and s1 != 1:
+        raise ValueError(f"{name} rows must be contiguous")
+    if rows <= 1 or cols == 0:
+        return cols if cols > 1 else 1
+    if s0 < cols:
+        raise ValueError(f"{name} rows must not overlap; an expanded tensor needs .contiguous()")
+    return s0
+
+
+def _matrix(t, name, device, rows=None, cols=None):
+    """(pointer, pitch, rows, cols) of a 2-D float32 tensor on ``device``, of
+    the given sizes where they are given."""
     import torch
-    if t.dim() != 3 or t.dtype != torch.float32:
+    if t.dtype is not torch.float32 or t.dim() != 2:
+        raise TypeError(f"{name} must be a 2-D float32 tensor")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device} (got {t.device})")
+    r, c = t.shape
+    if (rows is not None and r != rows) or (cols is not None and c != cols):
+        raise ValueError(f"{name} must be {'?' if rows is None else rows}x"
+                         f"{'?' if cols is None else cols}, got {r}x{c}")
+    s0, s1 = t.stride()
+    return t.data_ptr(), _rows(r, c, s0, s1, name), r, c
+
+
+def _stack(t, name, device, groups, rows=None, cols=None):
+    """(pointer, pitch, stride, rows, cols) of a 3-D float32 tensor on
+    ``device``: one matrix per group, of the given sizes where they are given."""
+    import torch
+    if t.dtype is not torch.float32 or t.dim() != 3:
         raise TypeError(f"{name} must be a 3-D float32 tensor")
     if t.device != device:
         raise ValueError(f"{name} must be on {device} (got {t.device})")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {'x'.join(map(str, shape))}, got {tuple(t.shape)}")
-    pitch = _pitch(t[0], name) if t.shape[0] > 0 else max(t.shape[2], 1)
-    return t.data_ptr(), pitch, t.stride(0)
+    g, r, c = t.shape
+    if g != groups or (rows is not None and r != rows) or (cols is not None and c != cols):
+        raise ValueError(f"{name} must be {groups}x{'?' if rows is None else rows}x"
+                         f"{'?' if cols is None else cols}, got {g}x{r}x{c}")
+    sg, s0, s1 = t.stride()
+    return t.data_ptr(), _rows(r, c, s0, s1, name), sg, r, c
 
 
-def _same_device(first, **others):
-    for name, t in others.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{name} must be on {first.device} (got {t.device})")
+def _vector(t, name, device, count):
+    """Pointer of a contiguous float32 vector on ``device`` (0 for None)."""
+    import torch
+    if t is None:
+        return 0
+    if (t.dtype is not torch.float32 or t.dim() != 1 or t.shape[0] != count
+            or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous vector of {count} floats")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device} (got {t.device})")
+    return t.data_ptr()
+
+
+def _biases(t, device, groups, cols):
+    """(pointer, stride) of one bias row per group; (0, 0) for None."""
+    import torch
+    if t is None:
+        return 0, 0
+    if t.dtype is not torch.float32 or tuple(t.shape) != (groups, cols):
+        raise ValueError(f"bias must be {groups}x{cols} floats, got {tuple(t.shape)}")
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError("bias rows must be contiguous")
+    if t.device != device:
+        raise ValueError(f"bias must be on {device} (got {t.device})")
+    return t.data_ptr(), t.stride(0)
+
+
+def _gpu(t, name):
+    if t.device.type != "cuda":
+        raise TypeError(f"{name} must be on a GPU (got {t.device})")
+    return t.device
 
 
 def _groups_of(offsets):
-    if offsets.dim() != 1 or offsets.numel() < 1:
+    if offsets.dim() != 1 or offsets.shape[0] < 1:
         raise ValueError("offsets must hold one entry more than there are groups")
-    return offsets.numel() - 1
+    return offsets.shape[0] - 1
 
 
 def group_rows(index, groups, *, per_row=1):
@@ -541,18 +604,14 @@ def group_rows(index, groups, *, per_row=1):
     (values outside [0, groups) name none).  Returns int32 tensors ``offsets``
     (groups + 1), ``order`` (the entries by (group, entry)) and ``rows``
     (order // per_row); both hold -1 from offsets[groups] on."""
-    import torch
-    if index.device.type != "cuda":
-        raise TypeError(f"index must be on a GPU (got {index.device})")
-    n, dev = index.numel(), index.device
+    dev = _gpu(index, "index")
     ptr = _index(index, "index", dev)
-    offsets = torch.empty(max(int(groups), 0) + 1, dtype=torch.int32, device=dev)
-    order = torch.empty(n, dtype=torch.int32, device=dev)
-    rows = torch.empty(n, dtype=torch.int32, device=dev)
+    n, groups = index.shape[0], int(groups)
+    offsets = index.new_empty(max(groups, 0) + 1)
+    order, rows = index.new_empty(n), index.new_empty(n)
     with _device(index):
-        rc = gemm_f32_group_rows(n, int(groups), int(per_row), ptr, offsets.data_ptr(),
-                                 order.data_ptr(), rows.data_ptr(),
-                                 torch.cuda.current_stream(dev).cuda_stream)
+        rc = gemm_f32_group_rows(n, groups, int(per_row), ptr, offsets.data_ptr(),
+                                 order.data_ptr(), rows.data_ptr(), _stream(dev))
     if rc != GEMM_F32_OK:
         raise GemmError(rc, "gemm_f32_group_rows")
     return offsets, order, rows
@@ -567,33 +626,21 @@ def gemm_grouped(A, B, offsets, C=None, *, trans_b=False, alpha=1.0, beta=0.0, b
     (A's rows without any).  A new C has one row a place; rows that no place
     names hold nothing in particular there, and keep what they held in a C that
     is given.  Returns C."""
-    import torch
-    lda = _pitch(A, "A")
-    dev, groups = A.device, _groups_of(offsets)
-    K = A.shape[1]
-    N = B.shape[1 if trans_b else 2] if B.dim() == 3 else -1
-    b, ldb, sb = _stack(B, "B", dev, (groups, N, K) if trans_b else (groups, K, N))
-    rows = (index_a.numel() if index_a is not None else
-            index_c.numel() if index_c is not None else A.shape[0])
+    dev, groups = _gpu(A, "A"), _groups_of(offsets)
+    a, lda, rows_a, K = _matrix(A, "A", dev)
+    b, ldb, sb, b_rows, b_cols = _stack(B, "B", dev, groups, *((None, K) if trans_b else (K,)))
+    N = b_rows if trans_b else b_cols
+    rows = (index_a.shape[0] if index_a is not None else
+            index_c.shape[0] if index_c is not None else rows_a)
     ia, ic = _index(index_a, "index_a", dev, rows), _index(index_c, "index_c", dev, rows)
     if C is None:
-        C = torch.empty((rows, N), dtype=torch.float32, device=dev)
-    if C.dim() != 2 or C.shape[1] != N:
-        raise ValueError(f"C must have {N} columns, got {tuple(C.shape)}")
-    ldc = _pitch(C, "C")
-    bptr, sbias = 0, 0
-    if bias is not None:
-        if (bias.dtype != torch.float32 or tuple(bias.shape) != (groups, N)
-                or (N > 1 and bias.stride(1) != 1)):
-            raise ValueError(f"bias must be {groups}x{N} floats with contiguous rows")
-        bptr, sbias = bias.data_ptr(), bias.stride(0)
-    _same_device(A, C=C, bias=bias)
+        C = A.new_empty((rows, N))
+    c, ldc, rows_c, _ = _matrix(C, "C", dev, cols=N)
+    bptr, sbias = _biases(bias, dev, groups, N)
     with _device(A):
-        rc = gemm_f32_grouped(int(bool(trans_b)), rows, N, K, groups,
-                              _index(offsets, "offsets", dev), alpha, A.data_ptr(), lda,
-                              A.shape[0], ia, b, ldb, sb, beta, C.data_ptr(), ldc, C.shape[0],
-                              ic, bptr, sbias, int(act),
-                              torch.cuda.current_stream(dev).cuda_stream)
+        rc = gemm_f32_grouped(1 if trans_b else 0, rows, N, K, groups,
+                              _index(offsets, "offsets", dev), alpha, a, lda, rows_a, ia, b, ldb,
+                              sb, beta, c, ldc, rows_c, ic, bptr, sbias, int(act), _stream(dev))
     if rc != GEMM_F32_OK:
         raise GemmError(rc, "gemm_f32_grouped")
     return C
@@ -604,22 +651,19 @@ def gemm_grouped_wgrad(A, B, offsets, C=None, *, alpha=1.0, beta=0.0, index_a=No
     """C[g] = alpha * sum over the places i of group g of A[index_a[i]]^T
     B[index_b[i]], plus beta * C[g]: the gradient of gemm_grouped's weights.
     Returns C (groups x A's columns x B's columns)."""
-    import torch
-    lda, ldb = _pitch(A, "A"), _pitch(B, "B")
-    dev, groups = A.device, _groups_of(offsets)
-    M, N = A.shape[1], B.shape[1]
-    rows = (index_a.numel() if index_a is not None else
-            index_b.numel() if index_b is not None else A.shape[0])
+    dev, groups = _gpu(A, "A"), _groups_of(offsets)
+    a, lda, rows_a, M = _matrix(A, "A", dev)
+    b, ldb, rows_b, N = _matrix(B, "B", dev)
+    rows = (index_a.shape[0] if index_a is not None else
+            index_b.shape[0] if index_b is not None else rows_a)
     ia, ib = _index(index_a, "index_a", dev, rows), _index(index_b, "index_b", dev, rows)
     if C is None:
-        C = torch.empty((groups, M, N), dtype=torch.float32, device=dev)
-    c, ldc, sc = _stack(C, "C", dev, (groups, M, N))
-    _same_device(A, B=B)
+        C = A.new_empty((groups, M, N))
+    c, ldc, sc, _, _ = _stack(C, "C", dev, groups, M, N)
     with _device(A):
         rc = gemm_f32_grouped_wgrad(rows, M, N, groups, _index(offsets, "offsets", dev), alpha,
-                                    A.data_ptr(), lda, A.shape[0], ia, B.data_ptr(), ldb,
-                                    B.shape[0], ib, beta, c, ldc, sc,
-                                    torch.cuda.current_stream(dev).cuda_stream)
+                                    a, lda, rows_a, ia, b, ldb, rows_b, ib, beta, c, ldc, sc,
+                                    _stream(dev))
     if rc != GEMM_F32_OK:
         raise GemmError(rc, "gemm_f32_grouped_wgrad")
     return C
@@ -633,37 +677,26 @@ def gemm_adapters(X, W, down, up, offsets, order, Y=None, H=None, *, trans=False
     adapters x R x N, or with ``trans`` each matrix stored transposed; ``scale``
     one float per adapter (None: 1), ``bias`` N floats or None.  Returns (Y, H);
     H (one row a place) is what gemm_adapters_grad takes."""
-    import torch
-    ldx, ldw = _pitch(X, "X"), _pitch(W, "W")
-    dev, adapters = X.device, _groups_of(offsets)
-    M, K = X.shape
-    N = W.shape[0] if trans else W.shape[1]
-    if (W.shape[1] if trans else W.shape[0]) != K:
-        raise ValueError(f"inner sizes differ: X is {tuple(X.shape)}, W is {tuple(W.shape)}")
-    R = down.shape[1 if trans else 2] if down.dim() == 3 else -1
-    d, ldd, sd = _stack(down, "down", dev, (adapters, R, K) if trans else (adapters, K, R))
-    u, ldu, su = _stack(up, "up", dev, (adapters, N, R) if trans else (adapters, R, N))
-    places = order.numel()
+    dev, adapters = _gpu(X, "X"), _groups_of(offsets)
+    x, ldx, M, K = _matrix(X, "X", dev)
+    w, ldw, w_rows, w_cols = _matrix(W, "W", dev, *((None, K) if trans else (K,)))
+    d, ldd, sd, d_rows, d_cols = _stack(down, "down", dev, adapters,
+                                        *((None, K) if trans else (K,)))
+    N, R = (w_rows, d_rows) if trans else (w_cols, d_cols)
+    u, ldu, su, _, _ = _stack(up, "up", dev, adapters, *((N, R) if trans else (R, N)))
+    places = order.shape[0]
     if Y is None:
-        Y = torch.empty((M, N), dtype=torch.float32, device=dev)
+        Y = X.new_empty((M, N))
     if H is None:
-        H = torch.empty((places, R), dtype=torch.float32, device=dev)
-    if tuple(Y.shape) != (M, N) or tuple(H.shape) != (places, R):
-        raise ValueError(f"Y must be {M}x{N} and H {places}x{R}, got {tuple(Y.shape)} and "
-                         f"{tuple(H.shape)}")
-    ldy, ldh = _pitch(Y, "Y"), _pitch(H, "H")
-    for t, name, count in ((scale, "scale", adapters), (bias, "bias", N)):
-        if t is not None and (t.dtype != torch.float32 or t.dim() != 1 or t.numel() != count
-                              or (count > 1 and t.stride(0) != 1)):
-            raise ValueError(f"{name} must be a contiguous vector of {count} floats")
-    _same_device(X, W=W, Y=Y, H=H, scale=scale, bias=bias)
+        H = X.new_empty((places, R))
+    y, ldy, _, _ = _matrix(Y, "Y", dev, M, N)
+    h, ldh, _, _ = _matrix(H, "H", dev, places, R)
     with _device(X):
-        rc = gemm_f32_adapters(int(bool(trans)), M, N, K, R, adapters, places,
+        rc = gemm_f32_adapters(1 if trans else 0, M, N, K, R, adapters, places,
                                _index(offsets, "offsets", dev), _index(order, "order", dev),
-                               0 if scale is None else scale.data_ptr(), X.data_ptr(), ldx,
-                               W.data_ptr(), ldw, d, ldd, sd, u, ldu, su,
-                               0 if bias is None else bias.data_ptr(), H.data_ptr(), ldh,
-                               Y.data_ptr(), ldy, torch.cuda.current_stream(dev).cuda_stream)
+                               _vector(scale, "scale", dev, adapters), x, ldx, w, ldw, d, ldd, sd,
+                               u, ldu, su, _vector(bias, "bias", dev, N), h, ldh, y, ldy,
+                               _stream(dev))
     if rc != GEMM_F32_OK:
         raise GemmError(rc, "gemm_f32_adapters")
     return Y, H

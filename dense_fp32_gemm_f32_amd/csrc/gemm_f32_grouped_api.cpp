@@ -111,7 +111,7 @@ int gemm_f32_grouped(int transB, int64_t rows, int64_t N, int64_t K, int64_t gro
   if (bad_pitch(lda, K) || bad_pitch(ldb, b_cols) || bad_pitch(ldc, N) || strideB < 0 ||
       strideBias < 0)
     return GEMM_F32_ERR_INVALID_LD;
-  const bool none = rows == 0 || N == 0 || groups == 0;
+  const bool none = rows == 0 || N == 0 || groups == 0 || rowsC == 0;
   const int64_t ea = extent(rowsA, K, lda), eb = extent(b_rows, b_cols, ldb, groups, strideB),
                 ec = extent(rowsC, N, ldc), ebias = extent(1, N, N, groups, strideBias);
   if (ea < 0 || eb < 0 || ec < 0 || ebias < 0) return GEMM_F32_ERR_INVALID_LD;

@@ -12,7 +12,10 @@ namespace {
 using namespace grouped;
 
 // The update of a wave's blocks, rows of C through row_c (LDS; -1: not
-// written).  The plain product stores the sums themselves.
+// written).  One path for the plain product, one that does not read C, one
+// that does: a wait for a load also waits for the stores before it, so C's old
+// values are loaded a block at a time, and not at all where beta is 0 (the same
+// loop with the load under a condition took 27 us more at 8192 x 1024 x 2048).
 template <int KFM, int KFN>
 __device__ __forceinline__ void store_rows(const floatx16 (&acc)[KFM][KFN],
                                            const GroupedProblem& p, const Epilogue& ep,
@@ -20,21 +23,59 @@ __device__ __forceinline__ void store_rows(const floatx16 (&acc)[KFM][KFN],
                                            int lane) {
   const int lr = lane & 31, lk = lane >> 5;
   const bool direct = scale == 1.f && ep.alpha == 1.f && ep.beta == 0.f && !ep.bias && ep.act == 0;
+  float bias[KFN];
 #pragma unroll
-  for (int i = 0; i < KFM; ++i) {
+  for (int j = 0; j < KFN; ++j) {
+    const int col = col0 + 32 * j + lr;
+    bias[j] = ep.bias && col < p.N ? ep.bias[col] : 0.f;
+  }
+  // every element: f(its column's bias, its sum, a pointer to it)
+  auto each = [&](auto f) {
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const int c = row_c[row0 + 32 * i + 4 * lk + 8 * (r >> 2) + (r & 3)];
-      if (c < 0) continue;
-      float* out = p.C + c * p.ldc;
+    for (int i = 0; i < KFM; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int c = row_c[row0 + 32 * i + 4 * lk + 8 * (r >> 2) + (r & 3)];
+        if (c < 0) continue;
+        float* const out = p.C + c * p.ldc + col0 + lr;
+#pragma unroll
+        for (int j = 0; j < KFN; ++j)
+          if (col0 + 32 * j + lr < p.N) f(j, acc[i][j][r], out + 32 * j);
+      }
+  };
+  if (direct) {
+    each([&](int, float s, float* out) { *out = s; });
+  } else if (ep.beta == 0.f) {
+    const float alpha = ep.alpha;
+    const bool relu = ep.act == 1;
+    each([&](int j, float s, float* out) {
+      float v = alpha * (scale * s);
+      if (ep.bias) v = v + bias[j];
+      *out = relu && v < 0.f ? 0.f : v;
+    });
+  } else {
+#pragma unroll
+    for (int i = 0; i < KFM; ++i)
 #pragma unroll
       for (int j = 0; j < KFN; ++j) {
         const int col = col0 + 32 * j + lr;
-        if (col < p.N)
-          out[col] = direct ? acc[i][j][r]
-                            : epilogue_apply(ep, scale * acc[i][j][r], out + col, col);
+        if (col >= p.N) continue;
+        float old[16];
+        int row[16];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          row[r] = row_c[row0 + 32 * i + 4 * lk + 8 * (r >> 2) + (r & 3)];
+          // an absent row reads the first element of C, which is there
+          old[r] = p.C[max(row[r], 0) * p.ldc + col];
+        }
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          float v = ep.alpha * (scale * acc[i][j][r]) + ep.beta * old[r];
+          if (ep.bias) v = v + bias[j];
+          if (ep.act == 1 && v < 0.f) v = 0.f;
+          if (row[r] >= 0) p.C[row[r] * p.ldc + col] = v;
+        }
       }
-    }
   }
 }
 
@@ -90,6 +131,75 @@ __global__ void __launch_bounds__((BM / WM) * (BN / WN) * 64)
   grouped_tile<BM, BN, BK, WM, WN, kTB, V>(pool, row_a, row_c, p, ep, g, tn * BN, wave, lane);
 }
 
+// The same with tiles of 128 x 128 for whole rounds of the CUs, and what is
+// left over, if it fills at most three quarters of a round, as 64 x 64 quarters of
+// its tiles; a group's last row tile of at most 64 places is 64 x 128.
+// (8192 x 1024 x 2048 in 8 uneven groups: 287 us, against 334 us with 128 x 128
+// tiles only, whose fifth round of the CUs is a quarter full, and 319 us with
+// 64 x 64 tiles only; in even groups, four whole rounds, 267, 263 and 296 us.)
+constexpr unsigned kCus = 256;
+constexpr unsigned kMostSplit = kCus / 4 * 3;
+
+template <bool kTB>
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
+    grouped_mixed_kernel(GroupedProblem p, Epilogue ep, int tiles_n, unsigned cap) {
+  constexpr int BM = 128, BN = 128, BK = 32;
+  __shared__ __attribute__((aligned(16))) float pool[2 * (BM + BN) * BK];
+  __shared__ int row_a[BM], row_c[BM];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  RowTiles rt{p.offsets, p.groups, p.rows, BM, lane, cap, 0};
+  const unsigned total = rt.total(), tiles = total * (unsigned)tiles_n;
+  const unsigned split = tiles % kCus <= kMostSplit ? tiles % kCus : 0, whole = tiles - split;
+  const unsigned id = tile_id();
+  const bool quarter = id >= whole;
+  // each XCD takes a contiguous range of the whole tiles, and one of the quarters
+  // (whole is a multiple of the CUs wherever there are quarters)
+  const unsigned n = quarter ? 4 * split : whole, at = quarter ? id - whole : id;
+  const unsigned x = at % kNumXcd, q = n / kNumXcd, rem = n % kNumXcd;
+  if (at / kNumXcd >= q + (x < rem ? 1u : 0u)) return;
+  const unsigned pos = x * q + min(x, rem) + at / kNumXcd;
+  int tm, tn;
+  tile_coords((int)(quarter ? whole + pos / 4 : pos), (int)total, tiles_n, tm, tn);
+  int g = 0, begin = 0, end = 0;
+  unsigned first = 0;
+  if (!rt.find((unsigned)tm, g, begin, end, first)) return;
+  int m0 = begin + (tm - (int)first) * BM, n0 = tn * BN;
+  if (quarter) {
+    m0 += (pos & 1) * 64;
+    n0 += ((pos >> 1) & 1) * 64;
+    if (m0 >= end || n0 >= p.N) return;
+  }
+  const Gather ga{p.ia, p.rows_a}, gc{p.ic, p.rows_c};
+  if (tid < BM) {
+    row_a[tid] = ga.at(m0 + tid, end);
+    row_c[tid] = gc.at(m0 + tid, end);
+  }
+  __syncthreads();
+  if (quarter) {
+    grouped_tile<64, 64, BK, 32, 32, kTB, 4>(pool, row_a, row_c, p, ep, g, n0, wave, lane);
+  } else if (end - m0 <= 64) {
+    grouped_tile<64, 128, BK, 32, 64, kTB, 4>(pool, row_a, row_c, p, ep, g, n0, wave, lane);
+  } else {
+    grouped_tile<128, 128, BK, 64, 64, kTB, 4>(pool, row_a, row_c, p, ep, g, n0, wave, lane);
+  }
+}
+
+hipError_t launch_mixed(const GroupedProblem& p, const Epilogue& e, hipStream_t s) {
+  const int64_t tiles_n = ((int64_t)p.N + 127) / 128;
+  const int64_t cap = most_row_tiles(p.rows, p.groups, 128);
+  if (cap * tiles_n + 3 * kMostSplit > 0x7fffffff) return hipErrorInvalidConfiguration;
+  const dim3 grid = tile_grid(cap * tiles_n + 3 * kMostSplit);
+  if (p.tb) {
+    hipLaunchKernelGGL((grouped_mixed_kernel<true>), grid, dim3(256), 0, s, p, e, (int)tiles_n,
+                       (unsigned)cap);
+  } else {
+    hipLaunchKernelGGL((grouped_mixed_kernel<false>), grid, dim3(256), 0, s, p, e, (int)tiles_n,
+                       (unsigned)cap);
+  }
+  return hipGetLastError();
+}
+
 template <int BM, int BN, int BK, int WM, int WN, int V, int kMinWaves>
 hipError_t launch(const GroupedProblem& p, const Epilogue& e, hipStream_t s) {
   const int64_t tiles_n = ((int64_t)p.N + BN - 1) / BN;
@@ -119,8 +229,7 @@ hipError_t launch_grouped(const GroupedProblem& p, const Epilogue& e, hipStream_
   const bool wide = aligned16(p.A) && aligned16(p.B) && p.lda % 4 == 0 && p.ldb % 4 == 0 &&
                     (p.groups == 1 || p.sb % 4 == 0) && p.K % 4 == 0 && (p.tb || p.N % 4 == 0);
   if (!wide) return launch<64, 64, 16, 32, 32, 1, 4>(p, e, s);
-  if ((int64_t)p.rows * p.N < (INT64_C(1) << 20)) return launch<64, 64, 32, 32, 32, 4, 4>(p, e, s);
-  return launch<128, 128, 32, 64, 32, 4, 2>(p, e, s);
+  return launch_mixed(p, e, s);
 }
 
 }  // namespace gemmf32

@@ -10,6 +10,25 @@ namespace {
 
 using namespace grouped;
 
+// The n-th largest of at most 64 groups (equal ones by number), found by each
+// wave.  A tile takes as long as its group has places, so the longest start
+// first and the shortest fill the end.
+__device__ __forceinline__ int nth_largest(const int* offsets, int groups, int rows, int n,
+                                           int lane) {
+  int mine = -1;
+  if (lane < groups) {
+    int b, e;
+    group_span(offsets, lane, rows, b, e);
+    mine = e - b;
+  }
+  int rank = 0;
+  for (int j = 0; j < groups; ++j) {
+    const int other = __builtin_amdgcn_readlane(mine, j);
+    rank += other > mine || (other == mine && j < lane) ? 1 : 0;
+  }
+  return __builtin_ctzll(__ballot(lane < groups && rank == n));
+}
+
 template <int BM, int BN, int BK, int WM, int WN, int V, int kMinWaves>
 __global__ void __launch_bounds__((BM / WM) * (BN / WN) * 64)
     __attribute__((amdgpu_waves_per_eu(kMinWaves)))
@@ -18,12 +37,15 @@ __global__ void __launch_bounds__((BM / WM) * (BN / WN) * 64)
   __shared__ __attribute__((aligned(16))) float pool[2 * (BM + BN) * BK];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  // the groups' tiles in order of the groups' sizes, each group's spread over
+  // the XCDs in contiguous ranges
   const int tiles = tiles_m * tiles_n;
-  const int id = xcd_contiguous_id((int)tile_id(), tiles * p.groups);
-  if ((int)tile_id() >= tiles * p.groups) return;
-  const int g = id / tiles;
+  const unsigned id = tile_id();
+  if (id >= (unsigned)tiles * p.groups) return;
+  const int g = p.groups <= 64 ? nth_largest(p.offsets, p.groups, p.rows, (int)(id / tiles), lane)
+                               : (int)(id / tiles);
   int tm, tn;
-  tile_coords(id - g * tiles, tiles_m, tiles_n, tm, tn);
+  tile_coords(xcd_contiguous_id((int)(id % tiles), tiles), tiles_m, tiles_n, tm, tn);
   int begin, end;
   group_span(p.offsets, g, p.rows, begin, end);
   begin = __builtin_amdgcn_readfirstlane(begin);

@@ -142,6 +142,46 @@ def test_binding_refuses_tensors_it_cannot_pass():
     with pytest.raises(ValueError, match="3 entries"):
         binding._index(torch.zeros(4, dtype=torch.int32), "index", x.device, 3)
     with pytest.raises(ValueError, match="2x8x8"):
-        binding._stack(torch.zeros(2, 8, 9), "B", x.device, (2, 8, 8))
+        binding._stack(torch.zeros(2, 8, 9), "B", x.device, 2, 8, 8)
+    with pytest.raises(TypeError, match="3-D"):
+        binding._stack(x, "B", x.device, 2)
+    with pytest.raises(TypeError, match="float32"):
+        binding._matrix(x.double(), "A", x.device)
+    with pytest.raises(ValueError, match="contiguous"):
+        binding._matrix(torch.zeros(8, 4).t(), "A", x.device)
+    with pytest.raises(ValueError, match="overlap"):
+        binding._matrix(torch.zeros(1, 8).expand(4, 8), "A", x.device)
+    with pytest.raises(ValueError, match="overlap"):
+        binding._matrix(torch.zeros(20).as_strided((4, 8), (3, 1)), "A", x.device)
+    with pytest.raises(ValueError, match="must be 4x9"):
+        binding._matrix(x, "A", x.device, 4, 9)
+    with pytest.raises(ValueError, match="on cuda"):
+        binding._matrix(x, "A", torch.device("cuda", 0))
+    with pytest.raises(ValueError, match="vector of 4"):
+        binding._vector(torch.zeros(5), "scale", x.device, 4)
+    with pytest.raises(ValueError, match="bias must be"):
+        binding._biases(torch.zeros(3, 4), x.device, 3, 5)
+    assert binding._matrix(x[:, 2:5], "A", x.device)[1:] == (8, 4, 3)
+    assert binding._matrix(x[:1, :].expand(1, 8), "A", x.device)[1:] == (8, 1, 8)
+    assert binding._matrix(torch.zeros(4, 0), "A", x.device)[1:] == (1, 4, 0)
+    assert binding._stack(torch.zeros(1, 8, 4).expand(3, 8, 4), "B", x.device, 3)[1:] == \
+        (4, 0, 8, 4)
+
+
+def test_products_refuse_tensors_whose_rows_overlap():
+    """An expanded matrix has no pitch: it would be read past its end."""
+    class Gpu:   # what _pitch looks at, with the device a GPU tensor reports
+        dtype, shape = torch.float32, (4, 8)
+        device = torch.device("cuda", 0)
+        def __init__(self, *strides):
+            self.strides = strides
+        def dim(self):
+            return 2
+        def stride(self, d):
+            return self.strides[d]
+    assert binding._pitch(Gpu(8, 1), "A") == 8 and binding._pitch(Gpu(11, 1), "A") == 11
+    for s0 in (0, 1, 7):
+        with pytest.raises(ValueError, match="overlap"):
+            binding._pitch(Gpu(s0, 1), "A")
     with pytest.raises(ValueError, match="offsets"):
         binding._groups_of(torch.zeros(0, dtype=torch.int32))
