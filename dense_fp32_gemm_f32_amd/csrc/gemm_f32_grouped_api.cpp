@@ -11,6 +11,7 @@
 #include "gemm_f32_internal.h"
 #include "grouped_internal.h"
 
+using gemmf32::AdapterProblem;
 using gemmf32::Epilogue;
 using gemmf32::GroupedProblem;
 
@@ -242,10 +243,43 @@ int gemm_f32_adapters(int trans, int64_t M, int64_t N, int64_t K, int64_t R, int
   int dev = -1;
   if (rc == GEMM_F32_OK) rc = check_reach(r, &dev);
   if (rc != GEMM_F32_OK) return rc;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (some) {
+    AdapterProblem a{};
+    a.X = X;
+    a.W = W;
+    a.D = D;
+    a.U = U;
+    a.scale = scale;
+    a.bias = bias;
+    a.offsets = offsets;
+    a.order = order;
+    a.H = H;
+    a.Y = Y;
+    a.ldx = ldx;
+    a.ldw = ldw;
+    a.ldd = ldd;
+    a.sd = strideD;
+    a.ldu = ldu;
+    a.su = strideU;
+    a.ldh = ldh;
+    a.ldy = ldy;
+    a.M = (int)M;
+    a.N = (int)N;
+    a.K = (int)K;
+    a.R = (int)R;
+    a.groups = (int)groups;
+    a.places = (int)places;
+    a.trans = t;
+    if (gemmf32::adapters_few(a)) {
+      float* part = nullptr;
+      rc = gemmf32::host_partials(dev, s, gemmf32::adapters_few_floats(a), &part);
+      return rc != GEMM_F32_OK ? rc : launched(gemmf32::launch_adapters_few(a, part, s));
+    }
+  }
   rc = gemm_f32_fused(0, trans, M, N, K, 1.f, X, ldx, W, ldw, 0.f, Y, ldy, bias,
                       GEMM_F32_ACT_NONE, stream);
   if (rc != GEMM_F32_OK || !some) return rc;
-  hipStream_t s = static_cast<hipStream_t>(stream);
   GroupedProblem p;   // H = s_g X[order] op(D_g)
   p.A = X;
   p.lda = ldx;

@@ -37,6 +37,21 @@ hipError_t launch_grouped(const GroupedProblem& p, const Epilogue& e, hipStream_
 hipError_t launch_grouped_rows(const GroupedProblem& p, const Epilogue& e, hipStream_t s);
 hipError_t launch_grouped_wgrad(const GroupedProblem& p, const Epilogue& e, hipStream_t s);
 
+// gemm_f32_adapters after its checks: matrices as stored (trans: each transposed).
+struct AdapterProblem {
+  const float *X, *W, *D, *U, *scale, *bias;
+  const int *offsets, *order;
+  float *H, *Y;
+  int64_t ldx, ldw, ldd, sd, ldu, su, ldh, ldy;
+  int M, N, K, R, groups, places;
+  bool trans;
+};
+// few rows: one launch of partial sums and one that joins them
+// (kernels_adapters.hip); the floats of workspace it takes
+bool adapters_few(const AdapterProblem& p);
+size_t adapters_few_floats(const AdapterProblem& p);
+hipError_t launch_adapters_few(const AdapterProblem& p, float* part, hipStream_t s);
+
 // offsets, order and rows (may be NULL) of gemm_f32_group_rows
 hipError_t launch_group_rows(int n, int groups, int per_row, const int* index, int* offsets,
                              int* order, int* rows, hipStream_t s);
