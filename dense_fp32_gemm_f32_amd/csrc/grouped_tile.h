@@ -77,7 +77,7 @@ struct Operand {
 
   const float* src[kCopies];   // this lane's place of each copy at k = 0
   int k_of[kCopies];           // and its k in the K-tile; a huge value: absent
-  int row[kGatherK ? kCopies : 1];   // gathered k: the matrix row of the next K-tile's copy
+  int row[kGatherK ? kCopies : 1];   // gathered k: the index entry of the next K-tile's copy
   static constexpr int kAbsent = 0x7fffffff;
 
   // (r, k) of the first of the V floats at LDS float `f`
@@ -116,19 +116,27 @@ struct Operand {
       k_of[v] = in ? k : kAbsent;
     }
   }
-  // gathered k: fetch the matrix rows of the K-tile at k0 (places first + k)
+  // gathered k: fetch the index entries of the K-tile at k0 (places first + k;
+  // past the end, the last place's).  They are looked at by copy() only: a use
+  // here would wait for them, and so for the copies in flight.
   __device__ __forceinline__ void fetch_rows(const Gather& ga, int first, int k0, int k_end) {
     if constexpr (kGatherK) {
+      if (ga.index) {
 #pragma unroll
-      for (int v = 0; v < kCopies; ++v)
-        row[v] = k_of[v] < k_end - k0 ? ga.at(first + k0 + k_of[v], first + k_end) : -1;
+        for (int v = 0; v < kCopies; ++v)
+          row[v] = ga.index[first + max(0, min(k0 + min(k_of[v], BK), k_end - 1))];
+      } else {
+#pragma unroll
+        for (int v = 0; v < kCopies; ++v) row[v] = first + k0 + k_of[v];
+      }
     }
   }
-  __device__ __forceinline__ void copy(int v, float* lds, int64_t ld, int k0, int k_end,
+  __device__ __forceinline__ void copy(int v, float* lds, int64_t ld, int k0, int k_end, int limit,
                                        int wave) const {
     const float* g;
     if constexpr (kGatherK) {
-      g = row[v] >= 0 ? src[v] + (int64_t)row[v] * ld : kZeros;
+      const bool in = k_of[v] < k_end - k0 && (unsigned)row[v] < (unsigned)limit;
+      g = in ? src[v] + (int64_t)row[v] * ld : kZeros;
     } else {
       const int64_t step = KC ? (int64_t)k0 : (int64_t)k0 * ld;
       g = k_of[v] < k_end - k0 ? src[v] + step : kZeros;
@@ -159,7 +167,8 @@ struct Operand {
 };
 
 // The K loop of a BM x BN tile, wave tiles WM x WN, over k in [0, k_end).
-// pool: 2 (BM + BN) BK floats of LDS.  k_end <= 0 gives zeros.
+// pool: 2 (BM + BN) BK floats of LDS.  k_end <= 0 gives zeros; where k is gathered
+// the index still has an entry at `first` then.
 template <int BM, int BN, int BK, int WM, int WN, class OpA, class OpB>
 __device__ __forceinline__ void k_loop(float* pool, OpA& opa, OpB& opb, const Gather& ga,
                                        const Gather& gb, int first, int64_t lda, int64_t ldb,
@@ -176,9 +185,9 @@ __device__ __forceinline__ void k_loop(float* pool, OpA& opa, OpB& opb, const Ga
   constexpr int kTileCopies = OpA::kCopies + OpB::kCopies;
   auto copy_one = [&](float* la, float* lb, int k0, int idx) {
     if (idx < OpA::kCopies) {
-      opa.copy(idx, la, lda, k0, k_end, wave);
+      opa.copy(idx, la, lda, k0, k_end, ga.limit, wave);
     } else {
-      opb.copy(idx - OpA::kCopies, lb, ldb, k0, k_end, wave);
+      opb.copy(idx - OpA::kCopies, lb, ldb, k0, k_end, gb.limit, wave);
     }
   };
   auto fetch_rows = [&](int k0) {

@@ -10,17 +10,20 @@ namespace {
 
 using namespace grouped;
 
+// A group's size in its lane, -1 past the last group.
+__device__ __forceinline__ int group_size(const int* offsets, int groups, int rows, int lane) {
+  if (lane >= groups) return -1;
+  int b, e;
+  group_span(offsets, lane, rows, b, e);
+  return e - b;
+}
+
 // The n-th largest of at most 64 groups (equal ones by number), found by each
 // wave.  A tile takes as long as its group has places, so the longest start
 // first and the shortest fill the end.
 __device__ __forceinline__ int nth_largest(const int* offsets, int groups, int rows, int n,
                                            int lane) {
-  int mine = -1;
-  if (lane < groups) {
-    int b, e;
-    group_span(offsets, lane, rows, b, e);
-    mine = e - b;
-  }
+  const int mine = group_size(offsets, groups, rows, lane);
   int rank = 0;
   for (int j = 0; j < groups; ++j) {
     const int other = __builtin_amdgcn_readlane(mine, j);
@@ -39,24 +42,26 @@ __global__ void __launch_bounds__((BM / WM) * (BN / WN) * 64)
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   // the groups' tiles in order of the groups' sizes, each group's spread over
   // the XCDs in contiguous ranges
-  const int tiles = tiles_m * tiles_n;
-  const unsigned id = tile_id();
-  if (id >= (unsigned)tiles * p.groups) return;
+  const unsigned id = tile_id(), tiles = (unsigned)tiles_m * tiles_n;
+  if (id >= tiles * p.groups) return;
   const int g = p.groups <= 64 ? nth_largest(p.offsets, p.groups, p.rows, (int)(id / tiles), lane)
                                : (int)(id / tiles);
   int tm, tn;
-  tile_coords(xcd_contiguous_id((int)(id % tiles), tiles), tiles_m, tiles_n, tm, tn);
+  tile_coords(xcd_contiguous_id((int)(id % tiles), (int)tiles), tiles_m, tiles_n, tm, tn);
   int begin, end;
   group_span(p.offsets, g, p.rows, begin, end);
   begin = __builtin_amdgcn_readfirstlane(begin);
   end = __builtin_amdgcn_readfirstlane(end);
+  // an empty group may begin behind the last place: no index entry to look at
+  const bool none = begin == end;
   Operand<BM, BK, kWaves, false, V, true> opa;
   Operand<BN, BK, kWaves, false, V, true> opb;
   opa.init_rc(p.A, p.lda, tm * BM, p.M, wave, lane);
   opb.init_rc(p.B, p.ldb, tn * BN, p.N, wave, lane);
   floatx16 acc[WM / 32][WN / 32];
-  k_loop<BM, BN, BK, WM, WN>(pool, opa, opb, Gather{p.ia, p.rows_a}, Gather{p.ib, p.rows_b}, begin,
-                             p.lda, p.ldb, end - begin, wave, lane, acc);
+  k_loop<BM, BN, BK, WM, WN>(pool, opa, opb, Gather{none ? nullptr : p.ia, p.rows_a},
+                             Gather{none ? nullptr : p.ib, p.rows_b}, begin, p.lda, p.ldb,
+                             end - begin, wave, lane, acc);
   store_blocks<WM / 32, WN / 32>(acc, p.C + g * p.sc, p.ldc, p.M, p.N,
                                  tm * BM + (wave % (BM / WM)) * WM,
                                  tn * BN + (wave / (BM / WM)) * WN, lane, false, ep);
@@ -80,8 +85,12 @@ hipError_t launch_grouped_wgrad(const GroupedProblem& p, const Epilogue& e, hipS
   const bool wide = aligned16(p.A) && aligned16(p.B) && p.lda % 4 == 0 && p.ldb % 4 == 0 &&
                     p.M % 4 == 0 && p.N % 4 == 0;
   if (!wide) return launch<64, 64, 16, 32, 32, 1, 4>(p, e, s);
-  if ((int64_t)p.M * p.N * p.groups < (INT64_C(1) << 22))
-    return launch<64, 64, 32, 32, 32, 4, 4>(p, e, s);
+  // 128 x 128 tiles, two a CU, where they make two rounds or more (16 groups of
+  // 512, 1024 x 1024: 148 us against 168 us for 64 x 64; 1024 x 2048 in 8 uneven
+  // groups of 8192 places in all: 289 against 328 us); below that a tile of a
+  // long group would run alone (3000 + 1000, 1024 x 1024: 219 against 108 us)
+  const int64_t tiles = ((int64_t)p.M + 127) / 128 * (((int64_t)p.N + 127) / 128) * p.groups;
+  if (tiles < 512) return launch<64, 64, 32, 32, 32, 4, 4>(p, e, s);
   return launch<128, 128, 32, 64, 32, 4, 2>(p, e, s);
 }
 
