@@ -9,9 +9,11 @@
 //
 //   - the rows of a KC operand, or the k of an RC operand, may be gathered
 //     through an index;
-//   - whatever lies outside (a row that is not there, k past the end, an index
-//     outside its matrix) is copied from a block of zeros in global memory, so
-//     K and the edges need no padding and no value outside is ever read;
+//   - k past the end, and gathered k whose index is outside the matrix, are
+//     copied from a block of zeros in global memory, so K needs no padding and no
+//     value outside is ever read.  Rows that are not there read row 0 and columns
+//     past the last read column 0: they reach only sums that are not stored, or,
+//     for a row whose index is outside, are stored as the zeros they count as;
 //   - a lane copies V floats at once: 4 where both operands allow it, else 1,
 //     which any pitch and alignment does.
 #pragma once
@@ -76,9 +78,7 @@ struct Operand {
   static_assert(KC || R % 64 == 0, "the [k][r] swizzle needs 64-wide rows");
 
   const float* src[kCopies];   // this lane's place of each copy at k = 0
-  int k_of[kCopies];           // and its k in the K-tile; a huge value: absent
   int row[kGatherK ? kCopies : 1];   // gathered k: the index entry of the next K-tile's copy
-  static constexpr int kAbsent = 0x7fffffff;
 
   // (r, k) of the first of the V floats at LDS float `f`
   __device__ __forceinline__ static void logical(int f, int& r, int& k) {
@@ -91,7 +91,12 @@ struct Operand {
       r = (f % R) ^ swz_b(k);
     }
   }
-  // KC with gathered rows: row_at(r) is the matrix row of tile row r, or -1
+  __device__ __forceinline__ static int k_of(int v, int wave, int lane) {
+    int r, k;
+    logical(((v * kWaves + wave) * 64 + lane) * V, r, k);
+    return k;
+  }
+  // KC with gathered rows: row_at(r) is the matrix row of tile row r
   template <class RowAt>
   __device__ __forceinline__ void init_kc(const float* base, int64_t ld, int wave, int lane,
                                           RowAt row_at) {
@@ -99,9 +104,7 @@ struct Operand {
     for (int v = 0; v < kCopies; ++v) {
       int r, k;
       logical(((v * kWaves + wave) * 64 + lane) * V, r, k);
-      const int m = row_at(r);
-      src[v] = m >= 0 ? base + (int64_t)m * ld + k : kZeros;
-      k_of[v] = m >= 0 ? k : kAbsent;
+      src[v] = base + (int64_t)row_at(r) * ld + k;
     }
   }
   // RC: columns r0 + r of a matrix with `cols` columns, row k at k * ld
@@ -111,35 +114,35 @@ struct Operand {
     for (int v = 0; v < kCopies; ++v) {
       int r, k;
       logical(((v * kWaves + wave) * 64 + lane) * V, r, k);
-      const bool in = r < cols - r0;
-      src[v] = in ? base + r0 + r + (kGatherK ? 0 : (int64_t)k * ld) : kZeros;
-      k_of[v] = in ? k : kAbsent;
+      src[v] = base + (r < cols - r0 ? r0 + r : 0) + (kGatherK ? 0 : (int64_t)k * ld);
     }
   }
   // gathered k: fetch the index entries of the K-tile at k0 (places first + k;
   // past the end, the last place's).  They are looked at by copy() only: a use
   // here would wait for them, and so for the copies in flight.
-  __device__ __forceinline__ void fetch_rows(const Gather& ga, int first, int k0, int k_end) {
+  __device__ __forceinline__ void fetch_rows(const Gather& ga, int first, int k0, int k_end,
+                                             int wave, int lane) {
     if constexpr (kGatherK) {
       if (ga.index) {
 #pragma unroll
         for (int v = 0; v < kCopies; ++v)
-          row[v] = ga.index[first + max(0, min(k0 + min(k_of[v], BK), k_end - 1))];
+          row[v] = ga.index[first + max(0, min(k0 + k_of(v, wave, lane), k_end - 1))];
       } else {
 #pragma unroll
-        for (int v = 0; v < kCopies; ++v) row[v] = first + k0 + k_of[v];
+        for (int v = 0; v < kCopies; ++v) row[v] = first + k0 + k_of(v, wave, lane);
       }
     }
   }
   __device__ __forceinline__ void copy(int v, float* lds, int64_t ld, int k0, int k_end, int limit,
-                                       int wave) const {
+                                       int wave, int lane) const {
     const float* g;
     if constexpr (kGatherK) {
-      const bool in = k_of[v] < k_end - k0 && (unsigned)row[v] < (unsigned)limit;
+      const bool in = k_of(v, wave, lane) < k_end - k0 && (unsigned)row[v] < (unsigned)limit;
       g = in ? src[v] + (int64_t)row[v] * ld : kZeros;
     } else {
-      const int64_t step = KC ? (int64_t)k0 : (int64_t)k0 * ld;
-      g = k_of[v] < k_end - k0 ? src[v] + step : kZeros;
+      g = src[v] + (KC ? (int64_t)k0 : (int64_t)k0 * ld);
+      // only the last K-tile can be part full
+      if (k0 + BK > k_end) g = k_of(v, wave, lane) < k_end - k0 ? g : kZeros;
     }
     copy_to_lds<V>(g, lds + (v * kWaves + wave) * (64 * V));
   }
@@ -185,14 +188,14 @@ __device__ __forceinline__ void k_loop(float* pool, OpA& opa, OpB& opb, const Ga
   constexpr int kTileCopies = OpA::kCopies + OpB::kCopies;
   auto copy_one = [&](float* la, float* lb, int k0, int idx) {
     if (idx < OpA::kCopies) {
-      opa.copy(idx, la, lda, k0, k_end, ga.limit, wave);
+      opa.copy(idx, la, lda, k0, k_end, ga.limit, wave, lane);
     } else {
-      opb.copy(idx - OpA::kCopies, lb, ldb, k0, k_end, gb.limit, wave);
+      opb.copy(idx - OpA::kCopies, lb, ldb, k0, k_end, gb.limit, wave, lane);
     }
   };
   auto fetch_rows = [&](int k0) {
-    opa.fetch_rows(ga, first, k0, k_end);
-    opb.fetch_rows(gb, first, k0, k_end);
+    opa.fetch_rows(ga, first, k0, k_end, wave, lane);
+    opb.fetch_rows(gb, first, k0, k_end, wave, lane);
   };
   const int wr_a = (wave % kWavesM) * WM, wr_b = (wave / kWavesM) * WN;
   const int lr = lane & 31, lk = lane >> 5;

@@ -81,64 +81,74 @@ __device__ __forceinline__ void store_rows(const floatx16 (&acc)[KFM][KFN],
 
 template <int BM, int BN, int BK, int WM, int WN, bool kTB, int V>
 __device__ __forceinline__ void grouped_tile(float* pool, const int* row_a, const int* row_c,
-                                             const GroupedProblem& p, const Epilogue& ep, int g,
-                                             int n0, int wave, int lane) {
+                                             bool absent, const GroupedProblem& p,
+                                             const Epilogue& ep, int g, int n0, int wave,
+                                             int lane) {
   constexpr int kWaves = (BM / WM) * (BN / WN);
   const float* B = p.B + g * p.sb;
   Operand<BM, BK, kWaves, true, V> opa;
   Operand<BN, BK, kWaves, kTB, V> opb;
-  opa.init_kc(p.A, p.lda, wave, lane, [&](int r) { return row_a[r]; });
+  opa.init_kc(p.A, p.lda, wave, lane, [&](int r) { return max(row_a[r], 0); });
   if constexpr (kTB) {
-    opb.init_kc(B, p.ldb, wave, lane, [&](int r) { return r < p.N - n0 ? n0 + r : -1; });
+    opb.init_kc(B, p.ldb, wave, lane, [&](int r) { return r < p.N - n0 ? n0 + r : 0; });
   } else {
     opb.init_rc(B, p.ldb, n0, p.N, wave, lane);
   }
   floatx16 acc[WM / 32][WN / 32];
   k_loop<BM, BN, BK, WM, WN>(pool, opa, opb, Gather{}, Gather{}, 0, p.lda, p.ldb, p.K, wave, lane,
                              acc);
+  const int row0 = (wave % (BM / WM)) * WM;
+  if (absent) {   // rows whose index is outside count as zeros
+#pragma unroll
+    for (int i = 0; i < WM / 32; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        if (row_a[row0 + 32 * i + 4 * (lane >> 5) + 8 * (r >> 2) + (r & 3)] < 0)
+#pragma unroll
+          for (int j = 0; j < WN / 32; ++j) acc[i][j][r] = 0.f;
+  }
   const float scale = p.gscale ? p.gscale[g] : 1.f;
   Epilogue e = ep;
   if (e.bias) e.bias += g * p.sbias;
-  store_rows(acc, p, e, scale, row_c, (wave % (BM / WM)) * WM, n0 + (wave / (BM / WM)) * WN, lane);
+  store_rows(acc, p, e, scale, row_c, row0, n0 + (wave / (BM / WM)) * WN, lane);
 }
 
-template <int BM, int BN, int BK, int WM, int WN, bool kTB, int V, int kMinWaves>
-__global__ void __launch_bounds__((BM / WM) * (BN / WN) * 64)
-    __attribute__((amdgpu_waves_per_eu(kMinWaves)))
-    grouped_kernel(GroupedProblem p, Epilogue ep, int tiles_n, unsigned cap) {
-  __shared__ __attribute__((aligned(16))) float pool[2 * (BM + BN) * BK];
-  __shared__ int row_a[BM], row_c[BM];
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  RowTiles rt{p.offsets, p.groups, p.rows, BM, lane, cap, 0};
-  const unsigned total = rt.total(), tiles = total * (unsigned)tiles_n;
-  // each XCD takes a contiguous range of the tiles that there are
-  const unsigned id = tile_id();
-  const unsigned x = id % kNumXcd, q = tiles / kNumXcd, rem = tiles % kNumXcd;
-  if (id / kNumXcd >= q + (x < rem ? 1u : 0u)) return;
-  int tm, tn;
-  tile_coords((int)(x * q + min(x, rem) + id / kNumXcd), (int)total, tiles_n, tm, tn);
-  int g = 0, begin = 0, end = 0;
-  unsigned first = 0;
-  if (!rt.find((unsigned)tm, g, begin, end, first)) return;
-  const int m0 = begin + (tm - (int)first) * BM;
+// A workgroup's tile and its rows: what both kernels do before their tiles.
+struct Place {
+  int g, m0, n0, end;   // group, first place and column, end of the group
+  bool absent;          // some row of A is outside its matrix
+};
+
+// The rows of A and C of the places m0 .. m0 + BM - 1, into LDS.
+template <int BM>
+__device__ __forceinline__ void find_rows(const GroupedProblem& p, Place& at, int* row_a,
+                                          int* row_c) {
   const Gather ga{p.ia, p.rows_a}, gc{p.ic, p.rows_c};
-  if (tid < BM) {
-    row_a[tid] = ga.at(m0 + tid, end);
-    row_c[tid] = gc.at(m0 + tid, end);
+  int outside = 0;
+  if ((int)threadIdx.x < BM) {
+    const int a = ga.at(at.m0 + threadIdx.x, at.end), c = gc.at(at.m0 + threadIdx.x, at.end);
+    row_a[threadIdx.x] = a;
+    row_c[threadIdx.x] = c;
+    outside = a < 0 && c >= 0;
   }
-  __syncthreads();
-  grouped_tile<BM, BN, BK, WM, WN, kTB, V>(pool, row_a, row_c, p, ep, g, tn * BN, wave, lane);
+  at.absent = __syncthreads_or(outside);
 }
 
-// The same with tiles of 128 x 128 for whole rounds of the CUs, and what is
-// left over, if it fills at most three quarters of a round, as 64 x 64 quarters of
-// its tiles; a group's last row tile of at most 64 places is 64 x 128.
-// (8192 x 1024 x 2048 in 8 uneven groups: 287 us, against 334 us with 128 x 128
-// tiles only, whose fifth round of the CUs is a quarter full, and 319 us with
-// 64 x 64 tiles only; in even groups, four whole rounds, 267, 263 and 296 us.)
+// Position `at` of n positions dealt to the XCDs round robin by workgroup id, so
+// that each XCD has a contiguous range; -1 past the end.
+__device__ __forceinline__ int xcd_position(unsigned at, unsigned n) {
+  const unsigned x = at % kNumXcd, q = n / kNumXcd, rem = n % kNumXcd;
+  if (at / kNumXcd >= q + (x < rem ? 1u : 0u)) return -1;
+  return (int)(x * q + min(x, rem) + at / kNumXcd);
+}
+
+// 16-byte copies: tiles of 128 x 128 for whole rounds of the CUs; what is left
+// over, if it fills at most three quarters of a round or there is no whole round,
+// as 64 x 64 quarters of its tiles; a group's last row tile of at most 64 places is
+// 64 x 128.  (8192 x 1024 x 2048 in 8 uneven groups: 287 us, against 334 us with
+// 128 x 128 tiles only, whose fifth round of the CUs is a quarter full, and 319 us
+// with 64 x 64 tiles only; in even groups, four whole rounds, 264, 263 and 296 us.)
 constexpr unsigned kCus = 256;
-constexpr unsigned kMostSplit = kCus / 4 * 3;
 
 template <bool kTB>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
@@ -146,50 +156,74 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
   constexpr int BM = 128, BN = 128, BK = 32;
   __shared__ __attribute__((aligned(16))) float pool[2 * (BM + BN) * BK];
   __shared__ int row_a[BM], row_c[BM];
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   RowTiles rt{p.offsets, p.groups, p.rows, BM, lane, cap, 0};
-  const unsigned total = rt.total(), tiles = total * (unsigned)tiles_n;
-  const unsigned split = tiles % kCus <= kMostSplit ? tiles % kCus : 0, whole = tiles - split;
+  const unsigned total = rt.total(), tiles = total * (unsigned)tiles_n, over = tiles % kCus;
+  const unsigned split = tiles < kCus || over <= kCus / 4 * 3 ? over : 0, whole = tiles - split;
+  // (whole is a multiple of the XCDs wherever there are quarters)
   const unsigned id = tile_id();
   const bool quarter = id >= whole;
-  // each XCD takes a contiguous range of the whole tiles, and one of the quarters
-  // (whole is a multiple of the CUs wherever there are quarters)
-  const unsigned n = quarter ? 4 * split : whole, at = quarter ? id - whole : id;
-  const unsigned x = at % kNumXcd, q = n / kNumXcd, rem = n % kNumXcd;
-  if (at / kNumXcd >= q + (x < rem ? 1u : 0u)) return;
-  const unsigned pos = x * q + min(x, rem) + at / kNumXcd;
-  int tm, tn;
-  tile_coords((int)(quarter ? whole + pos / 4 : pos), (int)total, tiles_n, tm, tn);
-  int g = 0, begin = 0, end = 0;
+  const int pos = quarter ? xcd_position(id - whole, 4 * split) : xcd_position(id, whole);
+  if (pos < 0) return;
+  int tm, tn, begin = 0;
+  tile_coords(quarter ? (int)whole + pos / 4 : pos, (int)total, tiles_n, tm, tn);
+  Place at{};
   unsigned first = 0;
-  if (!rt.find((unsigned)tm, g, begin, end, first)) return;
-  int m0 = begin + (tm - (int)first) * BM, n0 = tn * BN;
+  if (!rt.find((unsigned)tm, at.g, begin, at.end, first)) return;
+  at.m0 = begin + (tm - (int)first) * BM;
+  at.n0 = tn * BN;
   if (quarter) {
-    m0 += (pos & 1) * 64;
-    n0 += ((pos >> 1) & 1) * 64;
-    if (m0 >= end || n0 >= p.N) return;
+    at.m0 += (pos & 1) * 64;
+    at.n0 += ((pos >> 1) & 1) * 64;
+    if (at.m0 >= at.end || at.n0 >= p.N) return;
   }
-  const Gather ga{p.ia, p.rows_a}, gc{p.ic, p.rows_c};
-  if (tid < BM) {
-    row_a[tid] = ga.at(m0 + tid, end);
-    row_c[tid] = gc.at(m0 + tid, end);
-  }
-  __syncthreads();
+  find_rows<BM>(p, at, row_a, row_c);
   if (quarter) {
-    grouped_tile<64, 64, BK, 32, 32, kTB, 4>(pool, row_a, row_c, p, ep, g, n0, wave, lane);
-  } else if (end - m0 <= 64) {
-    grouped_tile<64, 128, BK, 32, 64, kTB, 4>(pool, row_a, row_c, p, ep, g, n0, wave, lane);
+    grouped_tile<64, 64, BK, 32, 32, kTB, 4>(pool, row_a, row_c, at.absent, p, ep, at.g, at.n0,
+                                             wave, lane);
+  } else if (at.end - at.m0 <= 64) {
+    grouped_tile<64, 128, BK, 32, 64, kTB, 4>(pool, row_a, row_c, at.absent, p, ep, at.g, at.n0,
+                                              wave, lane);
   } else {
-    grouped_tile<128, 128, BK, 64, 64, kTB, 4>(pool, row_a, row_c, p, ep, g, n0, wave, lane);
+    grouped_tile<128, 128, BK, 64, 64, kTB, 4>(pool, row_a, row_c, at.absent, p, ep, at.g, at.n0,
+                                               wave, lane);
   }
+}
+
+// Copies of single floats, for any pitch and alignment: BM x BN tiles, in waves
+// of WM x WN.
+template <int BM, int BN, int WM, int WN, bool kTB, int kMinWaves>
+__global__ void __launch_bounds__((BM / WM) * (BN / WN) * 64)
+    __attribute__((amdgpu_waves_per_eu(kMinWaves)))
+    grouped_any_kernel(GroupedProblem p, Epilogue ep, int tiles_n, unsigned cap) {
+  constexpr int BK = 16;
+  __shared__ __attribute__((aligned(16))) float pool[2 * (BM + BN) * BK];
+  __shared__ int row_a[BM], row_c[BM];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  RowTiles rt{p.offsets, p.groups, p.rows, BM, lane, cap, 0};
+  const unsigned total = rt.total();
+  const int pos = xcd_position(tile_id(), total * (unsigned)tiles_n);
+  if (pos < 0) return;
+  int tm, tn, begin = 0;
+  tile_coords(pos, (int)total, tiles_n, tm, tn);
+  Place at{};
+  unsigned first = 0;
+  if (!rt.find((unsigned)tm, at.g, begin, at.end, first)) return;
+  at.m0 = begin + (tm - (int)first) * BM;
+  at.n0 = tn * BN;
+  find_rows<BM>(p, at, row_a, row_c);
+  grouped_tile<BM, BN, BK, WM, WN, kTB, 1>(pool, row_a, row_c, at.absent, p, ep, at.g, at.n0, wave,
+                                           lane);
 }
 
 hipError_t launch_mixed(const GroupedProblem& p, const Epilogue& e, hipStream_t s) {
   const int64_t tiles_n = ((int64_t)p.N + 127) / 128;
   const int64_t cap = most_row_tiles(p.rows, p.groups, 128);
-  if (cap * tiles_n + 3 * kMostSplit > 0x7fffffff) return hipErrorInvalidConfiguration;
-  const dim3 grid = tile_grid(cap * tiles_n + 3 * kMostSplit);
+  // the quarters of less than one round take at most three more workgroups a CU
+  if (cap * tiles_n + 3 * kCus > 0x7fffffff) return hipErrorInvalidConfiguration;
+  const dim3 grid = tile_grid(cap * tiles_n + 3 * kCus);
   if (p.tb) {
     hipLaunchKernelGGL((grouped_mixed_kernel<true>), grid, dim3(256), 0, s, p, e, (int)tiles_n,
                        (unsigned)cap);
@@ -200,17 +234,17 @@ hipError_t launch_mixed(const GroupedProblem& p, const Epilogue& e, hipStream_t 
   return hipGetLastError();
 }
 
-template <int BM, int BN, int BK, int WM, int WN, int V, int kMinWaves>
-hipError_t launch(const GroupedProblem& p, const Epilogue& e, hipStream_t s) {
+template <int BM, int BN, int WM, int WN, int kMinWaves>
+hipError_t launch_any(const GroupedProblem& p, const Epilogue& e, hipStream_t s) {
   const int64_t tiles_n = ((int64_t)p.N + BN - 1) / BN;
   const int64_t cap = most_row_tiles(p.rows, p.groups, BM);
   if (cap * tiles_n > 0x7fffffff) return hipErrorInvalidConfiguration;
   const dim3 grid = tile_grid(cap * tiles_n), block((BM / WM) * (BN / WN) * 64);
   if (p.tb) {
-    hipLaunchKernelGGL((grouped_kernel<BM, BN, BK, WM, WN, true, V, kMinWaves>), grid, block, 0, s,
-                       p, e, (int)tiles_n, (unsigned)cap);
+    hipLaunchKernelGGL((grouped_any_kernel<BM, BN, WM, WN, true, kMinWaves>), grid, block, 0, s, p,
+                       e, (int)tiles_n, (unsigned)cap);
   } else {
-    hipLaunchKernelGGL((grouped_kernel<BM, BN, BK, WM, WN, false, V, kMinWaves>), grid, block, 0, s,
+    hipLaunchKernelGGL((grouped_any_kernel<BM, BN, WM, WN, false, kMinWaves>), grid, block, 0, s,
                        p, e, (int)tiles_n, (unsigned)cap);
   }
   return hipGetLastError();
@@ -220,7 +254,9 @@ bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
 }  // namespace
 
-hipError_t launch_grouped(const GroupedProblem& p, const Epilogue& e, hipStream_t s) {
+hipError_t launch_grouped(const GroupedProblem& call, const Epilogue& e, hipStream_t s) {
+  GroupedProblem p = call;
+  if (p.rows_a == 0) p.K = 0;   // every row of A is outside: empty sums
   // few rows in a group, or few columns: bound by one read of B or of A
   if (p.rows <= 24 * (int64_t)p.groups || p.rows <= 64 || p.N <= 64)
     return launch_grouped_rows(p, e, s);
@@ -228,8 +264,13 @@ hipError_t launch_grouped(const GroupedProblem& p, const Epilogue& e, hipStream_
   // and strides of 16 bytes, and the contiguous sizes multiples of 4
   const bool wide = aligned16(p.A) && aligned16(p.B) && p.lda % 4 == 0 && p.ldb % 4 == 0 &&
                     (p.groups == 1 || p.sb % 4 == 0) && p.K % 4 == 0 && (p.tb || p.N % 4 == 0);
-  if (!wide) return launch<64, 64, 16, 32, 32, 1, 4>(p, e, s);
-  return launch_mixed(p, e, s);
+  if (wide) return launch_mixed(p, e, s);
+  // 128 x 128 tiles where they make two rounds of the CUs (8 x 1000 x 1023 x 2047:
+  // 336 us against 452 us), 64 x 64 below (16 x 200 x 511 x 1025: 88 against 74 us)
+  const int64_t row_tiles = (int64_t)p.rows / 128 + p.groups / 2;
+  if (row_tiles * (((int64_t)p.N + 127) / 128) >= 2 * (int64_t)kCus)
+    return launch_any<128, 128, 64, 32, 2>(p, e, s);
+  return launch_any<64, 64, 32, 32, 4>(p, e, s);
 }
 
 }  // namespace gemmf32

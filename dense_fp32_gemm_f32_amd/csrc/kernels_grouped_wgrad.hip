@@ -84,14 +84,18 @@ bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 hipError_t launch_grouped_wgrad(const GroupedProblem& p, const Epilogue& e, hipStream_t s) {
   const bool wide = aligned16(p.A) && aligned16(p.B) && p.lda % 4 == 0 && p.ldb % 4 == 0 &&
                     p.M % 4 == 0 && p.N % 4 == 0;
-  if (!wide) return launch<64, 64, 16, 32, 32, 1, 4>(p, e, s);
   // 128 x 128 tiles, two a CU, where they make two rounds or more (16 groups of
   // 512, 1024 x 1024: 148 us against 168 us for 64 x 64; 1024 x 2048 in 8 uneven
-  // groups of 8192 places in all: 289 against 328 us); below that a tile of a
-  // long group would run alone (3000 + 1000, 1024 x 1024: 219 against 108 us)
+  // groups of 8192 places in all: 289 against 328 us; 1023 x 2047 with single-float
+  // copies, 8000 places: 362 against 459 us); below that a tile of a long group
+  // would run alone (3000 + 1000, 1024 x 1024: 219 against 108 us)
   const int64_t tiles = ((int64_t)p.M + 127) / 128 * (((int64_t)p.N + 127) / 128) * p.groups;
-  if (tiles < 512) return launch<64, 64, 32, 32, 32, 4, 4>(p, e, s);
-  return launch<128, 128, 32, 64, 32, 4, 2>(p, e, s);
+  const bool many = tiles >= 512;
+  if (!wide)
+    return many ? launch<128, 128, 16, 64, 32, 1, 2>(p, e, s)
+                : launch<64, 64, 16, 32, 32, 1, 4>(p, e, s);
+  return many ? launch<128, 128, 32, 64, 32, 4, 2>(p, e, s)
+              : launch<64, 64, 32, 32, 32, 4, 4>(p, e, s);
 }
 
 }  // namespace gemmf32
