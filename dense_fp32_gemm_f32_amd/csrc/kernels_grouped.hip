@@ -257,8 +257,12 @@ bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 hipError_t launch_grouped(const GroupedProblem& call, const Epilogue& e, hipStream_t s) {
   GroupedProblem p = call;
   if (p.rows_a == 0) p.K = 0;   // every row of A is outside: empty sums
-  // few rows in a group, or few columns: bound by one read of B or of A
-  if (p.rows <= 24 * (int64_t)p.groups || p.rows <= 64 || p.N <= 64)
+  // few rows in a group, few columns, or few sums: bound by one read of B or of A,
+  // or by the latency of a tile (16 groups of 32, 1024 x 1024: 27 us against 43 us
+  // for the tiles; of 64: 34 against 43; of 96: 49 against 43; 64 groups of 48: 130
+  // against 77)
+  const int64_t busy = p.rows < p.groups ? p.rows : p.groups, sums = (int64_t)p.rows * p.N;
+  if (p.N <= 64 || p.rows <= 32 * busy || (p.rows <= 64 * busy && sums <= 1 << 20) || sums <= 1 << 18)
     return launch_grouped_rows(p, e, s);
   // 16-byte copies need whole chunks of both operands inside: bases, pitches
   // and strides of 16 bytes, and the contiguous sizes multiples of 4

@@ -646,3 +646,42 @@ def test_two_streams_at_once(gpu_lib):
         for x, y in zip(got, want):
             for p, q in zip(x, y):
                 assert torch.equal(p, q)
+
+
+# ---- sizes that take the larger tiles -----------------------------------------------
+
+@pytest.mark.parametrize("K,N,pads", [(64, 1280, (0, 0, 0)), (35, 1301, (0, 0, 0)),
+                                      (36, 1284, (0, 0, 1)), (33, 1280, (3, 0, 0))])
+@pytest.mark.parametrize("trans", [False, True])
+def test_grouped_many_tiles(gpu_lib, K, N, pads, trans):
+    """Whole rounds of 128 x 128 tiles, the part-full round after them, and
+    groups that end in a short tile; 16-byte and single-float copies."""
+    counts = [3000, 0, 2500, 64, 1500, 129]
+    grouped_case(gpu_lib, counts, K, N, trans, True, True, True, True, 51, pads)
+    grouped_case(gpu_lib, counts, K, N, trans, False, False, False, False, 52, pads)
+
+
+@pytest.mark.parametrize("M,N", [(512, 1024), (513, 1029)])
+def test_wgrad_many_tiles(gpu_lib, M, N):
+    counts = [300, 0, 17, 500, 64, 1, 90, 33, 0, 128, 40, 7, 256]
+    wgrad_case(gpu_lib, counts, M, N, True, True, 1.0, 0.0, True, 53)
+    wgrad_case(gpu_lib, counts, M, N, False, False, 0.5, -2.0, False, 54)
+
+
+def test_wgrad_more_groups_than_a_wave(gpu_lib):
+    """Groups beyond 64 are not ordered by size."""
+    counts = [(11 * i) % 40 for i in range(100)]
+    wgrad_case(gpu_lib, counts, 200, 260, True, False, 1.0, 0.0, True, 55)
+
+
+def test_grouped_no_row_of_a_at_all(gpu_lib):
+    """A without rows: every index is outside, every sum empty."""
+    offsets, rows = spans([100, 50])
+    index = torch.zeros(rows, dtype=torch.int32).cuda()
+    b = torch.arange(300.).reshape(2, 150).cuda()
+    for n in (150, 40):   # the tiles, and the kernel for few columns
+        C = gpu_lib.gemm_grouped(torch.empty(0, 64, device="cuda"),
+                                 torch.ones(2, 64, n, device="cuda"), offsets.cuda(),
+                                 bias=b[:, :n], index_a=index)
+        want = torch.cat([b[0, :n].expand(100, n), b[1, :n].expand(50, n)])
+        assert torch.equal(C, want)
