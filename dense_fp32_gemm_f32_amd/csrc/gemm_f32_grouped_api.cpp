@@ -203,7 +203,12 @@ int gemm_f32_grouped_wgrad(int64_t rows, int64_t M, int64_t N, int64_t groups,
   Epilogue e;
   e.alpha = alpha;
   e.beta = beta;
-  return launched(gemmf32::launch_grouped_wgrad(p, e, static_cast<hipStream_t>(stream)));
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (!gemmf32::wgrad_thin(p)) return launched(gemmf32::launch_grouped_wgrad(p, e, s));
+  float* part = nullptr;
+  const size_t floats = gemmf32::wgrad_thin_floats(p);
+  if (floats > 0) rc = gemmf32::host_partials(dev, s, floats, &part);
+  return rc != GEMM_F32_OK ? rc : launched(gemmf32::launch_wgrad_thin(p, e, part, s));
 }
 
 int gemm_f32_adapters(int trans, int64_t M, int64_t N, int64_t K, int64_t R, int64_t groups,
@@ -244,42 +249,46 @@ int gemm_f32_adapters(int trans, int64_t M, int64_t N, int64_t K, int64_t R, int
   if (rc == GEMM_F32_OK) rc = check_reach(r, &dev);
   if (rc != GEMM_F32_OK) return rc;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (some) {
-    AdapterProblem a{};
-    a.X = X;
-    a.W = W;
-    a.D = D;
-    a.U = U;
-    a.scale = scale;
-    a.bias = bias;
-    a.offsets = offsets;
-    a.order = order;
-    a.H = H;
-    a.Y = Y;
-    a.ldx = ldx;
-    a.ldw = ldw;
-    a.ldd = ldd;
-    a.sd = strideD;
-    a.ldu = ldu;
-    a.su = strideU;
-    a.ldh = ldh;
-    a.ldy = ldy;
-    a.M = (int)M;
-    a.N = (int)N;
-    a.K = (int)K;
-    a.R = (int)R;
-    a.groups = (int)groups;
-    a.places = (int)places;
-    a.trans = t;
-    if (gemmf32::adapters_few(a)) {
-      float* part = nullptr;
-      rc = gemmf32::host_partials(dev, s, gemmf32::adapters_few_floats(a), &part);
-      return rc != GEMM_F32_OK ? rc : launched(gemmf32::launch_adapters_few(a, part, s));
-    }
+  if (!some)
+    return gemm_f32_fused(0, trans, M, N, K, 1.f, X, ldx, W, ldw, 0.f, Y, ldy, bias,
+                          GEMM_F32_ACT_NONE, stream);
+  AdapterProblem a{};
+  a.X = X;
+  a.W = W;
+  a.D = D;
+  a.U = U;
+  a.scale = scale;
+  a.bias = bias;
+  a.offsets = offsets;
+  a.order = order;
+  a.H = H;
+  a.Y = Y;
+  a.ldx = ldx;
+  a.ldw = ldw;
+  a.ldd = ldd;
+  a.sd = strideD;
+  a.ldu = ldu;
+  a.su = strideU;
+  a.ldh = ldh;
+  a.ldy = ldy;
+  a.M = (int)M;
+  a.N = (int)N;
+  a.K = (int)K;
+  a.R = (int)R;
+  a.groups = (int)groups;
+  a.places = (int)places;
+  a.trans = t;
+  float* work = nullptr;   // partial sums, or the map of rows
+  if (gemmf32::adapters_few(a)) {
+    rc = gemmf32::host_partials(dev, s, gemmf32::adapters_few_floats(a), &work);
+    return rc != GEMM_F32_OK ? rc : launched(gemmf32::launch_adapters_few(a, work, s));
   }
-  rc = gemm_f32_fused(0, trans, M, N, K, 1.f, X, ldx, W, ldw, 0.f, Y, ldy, bias,
-                      GEMM_F32_ACT_NONE, stream);
-  if (rc != GEMM_F32_OK || !some) return rc;
+  const bool tiles = gemmf32::adapters_tiles(a);
+  if (tiles) rc = gemmf32::host_partials(dev, s, 2 * (size_t)M, &work);
+  if (rc == GEMM_F32_OK && !tiles)
+    rc = gemm_f32_fused(0, trans, M, N, K, 1.f, X, ldx, W, ldw, 0.f, Y, ldy, bias,
+                        GEMM_F32_ACT_NONE, stream);
+  if (rc != GEMM_F32_OK) return rc;
   GroupedProblem p;   // H = s_g X[order] op(D_g)
   p.A = X;
   p.lda = ldx;
@@ -298,6 +307,11 @@ int gemm_f32_adapters(int trans, int64_t M, int64_t N, int64_t K, int64_t R, int
   p.N = (int)R;
   p.K = (int)K;
   p.tb = t;
+  if (tiles) {
+    p.map = reinterpret_cast<int*>(work);
+    rc = launched(gemmf32::launch_grouped_rows(p, Epilogue{}, s));
+    return rc != GEMM_F32_OK ? rc : launched(gemmf32::launch_adapters_tiles(a, p.map, s));
+  }
   rc = launched(gemmf32::launch_grouped(p, Epilogue{}, s));
   if (rc != GEMM_F32_OK) return rc;
   GroupedProblem q = p;   // Y[order] += H op(U_g)

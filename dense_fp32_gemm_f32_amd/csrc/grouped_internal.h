@@ -24,6 +24,8 @@ struct GroupedProblem {
   const int* ib = nullptr;   // gradient only
   const int* ic = nullptr;   // product only
   const float* gscale = nullptr;
+  int* map = nullptr;        // product by launch_grouped_rows only: where not NULL,
+                             // map[2 r] = i and map[2 r + 1] = g for A's row r = ia(i)
   int64_t lda = 0, ldb = 0, ldc = 0;
   int64_t sb = 0, sc = 0, sbias = 0;   // strides of B_g, C_g and bias_g
   int rows = 0, groups = 0;
@@ -36,6 +38,12 @@ hipError_t launch_grouped(const GroupedProblem& p, const Epilogue& e, hipStream_
 // the same for few rows in a group, or few columns (kernels_grouped_rows.hip)
 hipError_t launch_grouped_rows(const GroupedProblem& p, const Epilogue& e, hipStream_t s);
 hipError_t launch_grouped_wgrad(const GroupedProblem& p, const Epilogue& e, hipStream_t s);
+// the same for M or N of at most 64 (kernels_grouped_wgrad_thin.hip), and the
+// floats of workspace it takes
+bool wgrad_thin(const GroupedProblem& p);
+size_t wgrad_thin_floats(const GroupedProblem& p);
+hipError_t launch_wgrad_thin(const GroupedProblem& p, const Epilogue& e, float* part,
+                             hipStream_t s);
 
 // gemm_f32_adapters after its checks: matrices as stored (trans: each transposed).
 struct AdapterProblem {
@@ -46,6 +54,11 @@ struct AdapterProblem {
   int M, N, K, R, groups, places;
   bool trans;
 };
+// more rows and few adapters: H first (with the map of launch_grouped_rows, 2 M
+// ints), then the projection with H's products added to its tiles
+// (kernels_adapters_tile.hip)
+bool adapters_tiles(const AdapterProblem& p);
+hipError_t launch_adapters_tiles(const AdapterProblem& p, const int* map, hipStream_t s);
 // few rows: one launch of partial sums and one that joins them
 // (kernels_adapters.hip); the floats of workspace it takes
 bool adapters_few(const AdapterProblem& p);

@@ -107,6 +107,16 @@ struct Operand {
       src[v] = base + (int64_t)row_at(r) * ld + k;
     }
   }
+  // KC, any place for each row: at(r, k) points to the copy's first float at k
+  template <class At>
+  __device__ __forceinline__ void init_rows(int wave, int lane, At at) {
+#pragma unroll
+    for (int v = 0; v < kCopies; ++v) {
+      int r, k;
+      logical(((v * kWaves + wave) * 64 + lane) * V, r, k);
+      src[v] = at(r, k);
+    }
+  }
   // RC: columns r0 + r of a matrix with `cols` columns, row k at k * ld
   __device__ __forceinline__ void init_rc(const float* base, int64_t ld, int r0, int cols,
                                           int wave, int lane) {
@@ -169,14 +179,46 @@ struct Operand {
   }
 };
 
-// The K loop of a BM x BN tile, wave tiles WM x WN, over k in [0, k_end).
-// pool: 2 (BM + BN) BK floats of LDS.  k_end <= 0 gives zeros; where k is gathered
-// the index still has an entry at `first` then.
-template <int BM, int BN, int BK, int WM, int WN, class OpA, class OpB>
-__device__ __forceinline__ void k_loop(float* pool, OpA& opa, OpB& opb, const Gather& ga,
-                                       const Gather& gb, int first, int64_t lda, int64_t ldb,
-                                       int k_end, int wave, int lane,
+// Where the K loop's copies come from: two operands over k in [0, k_end), whole
+// K-tiles but for the last; one K-tile of zeros where k_end is 0.  seek(t) points
+// the copies at K-tile t, or at the last one, for t = 0, 1, 2, ... in turn.
+// Where k is gathered the index has an entry at `first`.
+template <int BK, class OpA_, class OpB_>
+struct Source {
+  using OpA = OpA_;
+  using OpB = OpB_;
+  OpA a;
+  OpB b;
+  int64_t lda, ldb;
+  int k_end, wave, lane;
+  Gather ga{nullptr, 0}, gb{nullptr, 0};
+  int first = 0;
+  int k0 = 0;
+
+  __device__ __forceinline__ Source(int64_t lda_, int64_t ldb_, int k_end_, int wave_, int lane_)
+      : lda(lda_), ldb(ldb_), k_end(k_end_), wave(wave_), lane(lane_) {}
+  __device__ __forceinline__ int tiles() const { return max(1, (k_end + BK - 1) / BK); }
+  __device__ __forceinline__ void seek(int t) {
+    k0 = min(t, tiles() - 1) * BK;
+    a.fetch_rows(ga, first, k0, k_end, wave, lane);
+    b.fetch_rows(gb, first, k0, k_end, wave, lane);
+  }
+  __device__ __forceinline__ void copy(float* la, float* lb, int idx) const {
+    if (idx < OpA::kCopies) {
+      a.copy(idx, la, lda, k0, k_end, ga.limit, wave, lane);
+    } else {
+      b.copy(idx - OpA::kCopies, lb, ldb, k0, k_end, gb.limit, wave, lane);
+    }
+  }
+};
+
+// The K loop of a BM x BN tile, wave tiles WM x WN, over src's K-tiles.
+// pool: 2 (BM + BN) BK floats of LDS, read by no wave any more.
+template <int BM, int BN, int BK, int WM, int WN, class Src>
+__device__ __forceinline__ void k_loop(float* pool, Src& src, int wave, int lane,
                                        floatx16 (&acc)[WM / 32][WN / 32]) {
+  using OpA = typename Src::OpA;
+  using OpB = typename Src::OpB;
   constexpr int kWavesM = BM / WM;
   constexpr int kFragM = WM / 32, kFragN = WN / 32;
   static_assert(WM % 32 == 0 && WN % 32 == 0 && BM % WM == 0 && BN % WN == 0, "32x32 blocks");
@@ -186,17 +228,6 @@ __device__ __forceinline__ void k_loop(float* pool, OpA& opa, OpB& opb, const Ga
   float* const lds_b0 = lds_a1 + OpA::kLds;
   float* const lds_b1 = lds_b0 + OpB::kLds;
   constexpr int kTileCopies = OpA::kCopies + OpB::kCopies;
-  auto copy_one = [&](float* la, float* lb, int k0, int idx) {
-    if (idx < OpA::kCopies) {
-      opa.copy(idx, la, lda, k0, k_end, ga.limit, wave, lane);
-    } else {
-      opb.copy(idx - OpA::kCopies, lb, ldb, k0, k_end, gb.limit, wave, lane);
-    }
-  };
-  auto fetch_rows = [&](int k0) {
-    opa.fetch_rows(ga, first, k0, k_end, wave, lane);
-    opb.fetch_rows(gb, first, k0, k_end, wave, lane);
-  };
   const int wr_a = (wave % kWavesM) * WM, wr_b = (wave / kWavesM) * WN;
   const int lr = lane & 31, lk = lane >> 5;
   struct Frag {
@@ -243,20 +274,19 @@ __device__ __forceinline__ void k_loop(float* pool, OpA& opa, OpB& opb, const Ga
 
   // Branch-free steps: the copies of a K-tile past the end re-read the last
   // one into the buffer no longer needed; the last step reads fragments it does
-  // not use.  One K-tile of zeros where there is no k.
-  const int ktiles = max(1, (k_end + BK - 1) / BK);
-  const int last_k0 = (ktiles - 1) * BK;
+  // not use.
+  const int ktiles = src.tiles();
   Frag f0, f1;
-  fetch_rows(0);
+  src.seek(0);
 #pragma unroll
-  for (int idx = 0; idx < kTileCopies; ++idx) copy_one(lds_a0, lds_b0, 0, idx);
-  fetch_rows(min(BK, last_k0));
+  for (int idx = 0; idx < kTileCopies; ++idx) src.copy(lds_a0, lds_b0, idx);
+  src.seek(1);
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
 #pragma unroll
   for (int idx = 0; idx < kReadsPerGroup; ++idx) read_one(f0, lds_a0, lds_b0, 0, idx);
 #pragma unroll
-  for (int idx = 0; idx < kTileCopies; ++idx) copy_one(lds_a1, lds_b1, min(BK, last_k0), idx);
+  for (int idx = 0; idx < kTileCopies; ++idx) src.copy(lds_a1, lds_b1, idx);
 
   auto step = [&](int t, auto cur_tag) {
     constexpr int kCur = decltype(cur_tag)::value;
@@ -264,8 +294,7 @@ __device__ __forceinline__ void k_loop(float* pool, OpA& opa, OpB& opb, const Ga
     float* lb = kCur ? lds_b1 : lds_b0;
     float* la_next = kCur ? lds_a0 : lds_a1;
     float* lb_next = kCur ? lds_b0 : lds_b1;
-    const int k_next2 = min((t + 2) * BK, last_k0);
-    fetch_rows(k_next2);
+    src.seek(t + 2);
 #pragma unroll
     for (int q = 0; q < kGroups; ++q) {
       Frag& fc = (q & 1) ? f1 : f0;
@@ -296,7 +325,7 @@ __device__ __forceinline__ void k_loop(float* pool, OpA& opa, OpB& opb, const Ga
               read_one(fn, la_next, lb_next, 0, i * kReadsPer + r);
 #pragma unroll
           for (int l = 0; l < kCopiesPer; ++l)
-            if (i * kCopiesPer + l < kTileCopies) copy_one(la, lb, k_next2, i * kCopiesPer + l);
+            if (i * kCopiesPer + l < kTileCopies) src.copy(la, lb, i * kCopiesPer + l);
           __builtin_amdgcn_sched_barrier(0);
         }
       }
@@ -309,6 +338,112 @@ __device__ __forceinline__ void k_loop(float* pool, OpA& opa, OpB& opb, const Ga
   // no copy into LDS may still be in flight when the pool is used again
   __builtin_amdgcn_s_waitcnt(0);
   if constexpr (kDual) acc[0][0] += acc_odd;
+}
+
+// Position `at` of n positions dealt to the XCDs round robin by workgroup id, so
+// that each XCD has a contiguous range; -1 past the end.
+__device__ __forceinline__ int xcd_position(unsigned at, unsigned n) {
+  const unsigned x = at % kNumXcd, q = n / kNumXcd, rem = n % kNumXcd;
+  if (at / kNumXcd >= q + (x < rem ? 1u : 0u)) return -1;
+  return (int)(x * q + min(x, rem) + at / kNumXcd);
+}
+
+// Mixed tiles: 128 x 128 for whole rounds of the CUs; what is left over, if it
+// fills at most three quarters of a round or there is no whole round, as 64 x 64
+// quarters of its tiles.  (Grouped product of 8192 x 1024 x 2048 in 8 uneven groups:
+// 287 us, against 334 us with 128 x 128 tiles only, whose fifth round of the CUs is a
+// quarter full, and 319 us with 64 x 64 tiles only; in even groups, four whole
+// rounds, 264, 263 and 296 us.)  The grid has a workgroup for every tile and 3 kCus
+// more.
+constexpr unsigned kCus = 256;
+
+struct MixedTile {
+  bool any, quarter;
+  int tm, tn, m_off, n_off;   // the 128 x 128 tile, and the quarter's place in it
+};
+__device__ __forceinline__ MixedTile mixed_tile(unsigned tiles_m, int tiles_n) {
+  const unsigned tiles = tiles_m * (unsigned)tiles_n, over = tiles % kCus;
+  const unsigned split = tiles < kCus || over <= kCus / 4 * 3 ? over : 0, whole = tiles - split;
+  // (whole is a multiple of the XCDs wherever there are quarters)
+  const unsigned id = tile_id();
+  MixedTile t{};
+  t.quarter = id >= whole;
+  const int pos = t.quarter ? xcd_position(id - whole, 4 * split) : xcd_position(id, whole);
+  t.any = pos >= 0;
+  if (!t.any) return t;
+  tile_coords(t.quarter ? (int)whole + pos / 4 : pos, (int)tiles_m, tiles_n, t.tm, t.tn);
+  if (t.quarter) {
+    t.m_off = (pos & 1) * 64;
+    t.n_off = ((pos >> 1) & 1) * 64;
+  }
+  return t;
+}
+
+// The update of a wave's blocks, rows of C through row_c (LDS; -1: not
+// written).  One path for the plain product, one that does not read C, one
+// that does: a wait for a load also waits for the stores before it, so C's old
+// values are loaded a block at a time, and not at all where beta is 0 (the same
+// loop with the load under a condition took 27 us more at 8192 x 1024 x 2048).
+template <int KFM, int KFN>
+__device__ __forceinline__ void store_rows(const floatx16 (&acc)[KFM][KFN], float* C, int64_t ldc,
+                                           int N, const Epilogue& ep, float scale,
+                                           const int* row_c, int row0, int col0, int lane) {
+  const int lr = lane & 31, lk = lane >> 5;
+  const bool direct = scale == 1.f && ep.alpha == 1.f && ep.beta == 0.f && !ep.bias && ep.act == 0;
+  float bias[KFN];
+#pragma unroll
+  for (int j = 0; j < KFN; ++j) {
+    const int col = col0 + 32 * j + lr;
+    bias[j] = ep.bias && col < N ? ep.bias[col] : 0.f;
+  }
+  // every element: f(its column's bias, its sum, a pointer to it)
+  auto each = [&](auto f) {
+#pragma unroll
+    for (int i = 0; i < KFM; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int c = row_c[row0 + 32 * i + 4 * lk + 8 * (r >> 2) + (r & 3)];
+        if (c < 0) continue;
+        float* const out = C + c * ldc + col0 + lr;
+#pragma unroll
+        for (int j = 0; j < KFN; ++j)
+          if (col0 + 32 * j + lr < N) f(j, acc[i][j][r], out + 32 * j);
+      }
+  };
+  if (direct) {
+    each([&](int, float s, float* out) { *out = s; });
+  } else if (ep.beta == 0.f) {
+    const float alpha = ep.alpha;
+    const bool relu = ep.act == 1;
+    each([&](int j, float s, float* out) {
+      float v = alpha * (scale * s);
+      if (ep.bias) v = v + bias[j];
+      *out = relu && v < 0.f ? 0.f : v;
+    });
+  } else {
+#pragma unroll
+    for (int i = 0; i < KFM; ++i)
+#pragma unroll
+      for (int j = 0; j < KFN; ++j) {
+        const int col = col0 + 32 * j + lr;
+        if (col >= N) continue;
+        float old[16];
+        int row[16];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          row[r] = row_c[row0 + 32 * i + 4 * lk + 8 * (r >> 2) + (r & 3)];
+          // an absent row reads the first element of C, which is there
+          old[r] = C[max(row[r], 0) * ldc + col];
+        }
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          float v = ep.alpha * (scale * acc[i][j][r]) + ep.beta * old[r];
+          if (ep.bias) v = v + bias[j];
+          if (ep.act == 1 && v < 0.f) v = 0.f;
+          if (row[r] >= 0) C[row[r] * ldc + col] = v;
+        }
+      }
+  }
 }
 
 }  // namespace grouped

@@ -11,74 +11,6 @@ namespace {
 
 using namespace grouped;
 
-// The update of a wave's blocks, rows of C through row_c (LDS; -1: not
-// written).  One path for the plain product, one that does not read C, one
-// that does: a wait for a load also waits for the stores before it, so C's old
-// values are loaded a block at a time, and not at all where beta is 0 (the same
-// loop with the load under a condition took 27 us more at 8192 x 1024 x 2048).
-template <int KFM, int KFN>
-__device__ __forceinline__ void store_rows(const floatx16 (&acc)[KFM][KFN],
-                                           const GroupedProblem& p, const Epilogue& ep,
-                                           float scale, const int* row_c, int row0, int col0,
-                                           int lane) {
-  const int lr = lane & 31, lk = lane >> 5;
-  const bool direct = scale == 1.f && ep.alpha == 1.f && ep.beta == 0.f && !ep.bias && ep.act == 0;
-  float bias[KFN];
-#pragma unroll
-  for (int j = 0; j < KFN; ++j) {
-    const int col = col0 + 32 * j + lr;
-    bias[j] = ep.bias && col < p.N ? ep.bias[col] : 0.f;
-  }
-  // every element: f(its column's bias, its sum, a pointer to it)
-  auto each = [&](auto f) {
-#pragma unroll
-    for (int i = 0; i < KFM; ++i)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int c = row_c[row0 + 32 * i + 4 * lk + 8 * (r >> 2) + (r & 3)];
-        if (c < 0) continue;
-        float* const out = p.C + c * p.ldc + col0 + lr;
-#pragma unroll
-        for (int j = 0; j < KFN; ++j)
-          if (col0 + 32 * j + lr < p.N) f(j, acc[i][j][r], out + 32 * j);
-      }
-  };
-  if (direct) {
-    each([&](int, float s, float* out) { *out = s; });
-  } else if (ep.beta == 0.f) {
-    const float alpha = ep.alpha;
-    const bool relu = ep.act == 1;
-    each([&](int j, float s, float* out) {
-      float v = alpha * (scale * s);
-      if (ep.bias) v = v + bias[j];
-      *out = relu && v < 0.f ? 0.f : v;
-    });
-  } else {
-#pragma unroll
-    for (int i = 0; i < KFM; ++i)
-#pragma unroll
-      for (int j = 0; j < KFN; ++j) {
-        const int col = col0 + 32 * j + lr;
-        if (col >= p.N) continue;
-        float old[16];
-        int row[16];
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          row[r] = row_c[row0 + 32 * i + 4 * lk + 8 * (r >> 2) + (r & 3)];
-          // an absent row reads the first element of C, which is there
-          old[r] = p.C[max(row[r], 0) * p.ldc + col];
-        }
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          float v = ep.alpha * (scale * acc[i][j][r]) + ep.beta * old[r];
-          if (ep.bias) v = v + bias[j];
-          if (ep.act == 1 && v < 0.f) v = 0.f;
-          if (row[r] >= 0) p.C[row[r] * p.ldc + col] = v;
-        }
-      }
-  }
-}
-
 template <int BM, int BN, int BK, int WM, int WN, bool kTB, int V>
 __device__ __forceinline__ void grouped_tile(float* pool, const int* row_a, const int* row_c,
                                              bool absent, const GroupedProblem& p,
@@ -86,17 +18,16 @@ __device__ __forceinline__ void grouped_tile(float* pool, const int* row_a, cons
                                              int lane) {
   constexpr int kWaves = (BM / WM) * (BN / WN);
   const float* B = p.B + g * p.sb;
-  Operand<BM, BK, kWaves, true, V> opa;
-  Operand<BN, BK, kWaves, kTB, V> opb;
-  opa.init_kc(p.A, p.lda, wave, lane, [&](int r) { return max(row_a[r], 0); });
+  Source<BK, Operand<BM, BK, kWaves, true, V>, Operand<BN, BK, kWaves, kTB, V>> src(
+      p.lda, p.ldb, p.K, wave, lane);
+  src.a.init_kc(p.A, p.lda, wave, lane, [&](int r) { return max(row_a[r], 0); });
   if constexpr (kTB) {
-    opb.init_kc(B, p.ldb, wave, lane, [&](int r) { return r < p.N - n0 ? n0 + r : 0; });
+    src.b.init_kc(B, p.ldb, wave, lane, [&](int r) { return r < p.N - n0 ? n0 + r : 0; });
   } else {
-    opb.init_rc(B, p.ldb, n0, p.N, wave, lane);
+    src.b.init_rc(B, p.ldb, n0, p.N, wave, lane);
   }
   floatx16 acc[WM / 32][WN / 32];
-  k_loop<BM, BN, BK, WM, WN>(pool, opa, opb, Gather{}, Gather{}, 0, p.lda, p.ldb, p.K, wave, lane,
-                             acc);
+  k_loop<BM, BN, BK, WM, WN>(pool, src, wave, lane, acc);
   const int row0 = (wave % (BM / WM)) * WM;
   if (absent) {   // rows whose index is outside count as zeros
 #pragma unroll
@@ -110,7 +41,7 @@ __device__ __forceinline__ void grouped_tile(float* pool, const int* row_a, cons
   const float scale = p.gscale ? p.gscale[g] : 1.f;
   Epilogue e = ep;
   if (e.bias) e.bias += g * p.sbias;
-  store_rows(acc, p, e, scale, row_c, row0, n0 + (wave / (BM / WM)) * WN, lane);
+  store_rows(acc, p.C, p.ldc, p.N, e, scale, row_c, row0, n0 + (wave / (BM / WM)) * WN, lane);
 }
 
 // A workgroup's tile and its rows: what both kernels do before their tiles.
@@ -134,22 +65,8 @@ __device__ __forceinline__ void find_rows(const GroupedProblem& p, Place& at, in
   at.absent = __syncthreads_or(outside);
 }
 
-// Position `at` of n positions dealt to the XCDs round robin by workgroup id, so
-// that each XCD has a contiguous range; -1 past the end.
-__device__ __forceinline__ int xcd_position(unsigned at, unsigned n) {
-  const unsigned x = at % kNumXcd, q = n / kNumXcd, rem = n % kNumXcd;
-  if (at / kNumXcd >= q + (x < rem ? 1u : 0u)) return -1;
-  return (int)(x * q + min(x, rem) + at / kNumXcd);
-}
-
-// 16-byte copies: tiles of 128 x 128 for whole rounds of the CUs; what is left
-// over, if it fills at most three quarters of a round or there is no whole round,
-// as 64 x 64 quarters of its tiles; a group's last row tile of at most 64 places is
-// 64 x 128.  (8192 x 1024 x 2048 in 8 uneven groups: 287 us, against 334 us with
-// 128 x 128 tiles only, whose fifth round of the CUs is a quarter full, and 319 us
-// with 64 x 64 tiles only; in even groups, four whole rounds, 264, 263 and 296 us.)
-constexpr unsigned kCus = 256;
-
+// 16-byte copies, in mixed tiles; a group's last row tile of at most 64 places is
+// 64 x 128.
 template <bool kTB>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
     grouped_mixed_kernel(GroupedProblem p, Epilogue ep, int tiles_n, unsigned cap) {
@@ -159,27 +76,17 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   RowTiles rt{p.offsets, p.groups, p.rows, BM, lane, cap, 0};
-  const unsigned total = rt.total(), tiles = total * (unsigned)tiles_n, over = tiles % kCus;
-  const unsigned split = tiles < kCus || over <= kCus / 4 * 3 ? over : 0, whole = tiles - split;
-  // (whole is a multiple of the XCDs wherever there are quarters)
-  const unsigned id = tile_id();
-  const bool quarter = id >= whole;
-  const int pos = quarter ? xcd_position(id - whole, 4 * split) : xcd_position(id, whole);
-  if (pos < 0) return;
-  int tm, tn, begin = 0;
-  tile_coords(quarter ? (int)whole + pos / 4 : pos, (int)total, tiles_n, tm, tn);
+  const MixedTile mt = mixed_tile(rt.total(), tiles_n);
+  if (!mt.any) return;
   Place at{};
+  int begin = 0;
   unsigned first = 0;
-  if (!rt.find((unsigned)tm, at.g, begin, at.end, first)) return;
-  at.m0 = begin + (tm - (int)first) * BM;
-  at.n0 = tn * BN;
-  if (quarter) {
-    at.m0 += (pos & 1) * 64;
-    at.n0 += ((pos >> 1) & 1) * 64;
-    if (at.m0 >= at.end || at.n0 >= p.N) return;
-  }
+  if (!rt.find((unsigned)mt.tm, at.g, begin, at.end, first)) return;
+  at.m0 = begin + (mt.tm - (int)first) * BM + mt.m_off;
+  at.n0 = mt.tn * BN + mt.n_off;
+  if (at.m0 >= at.end || at.n0 >= p.N) return;
   find_rows<BM>(p, at, row_a, row_c);
-  if (quarter) {
+  if (mt.quarter) {
     grouped_tile<64, 64, BK, 32, 32, kTB, 4>(pool, row_a, row_c, at.absent, p, ep, at.g, at.n0,
                                              wave, lane);
   } else if (at.end - at.m0 <= 64) {
@@ -191,13 +98,12 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
   }
 }
 
-// Copies of single floats, for any pitch and alignment: BM x BN tiles, in waves
-// of WM x WN.
-template <int BM, int BN, int WM, int WN, bool kTB, int kMinWaves>
+// Tiles of one size, BM x BN in waves of WM x WN; copies of V floats (1: for any
+// pitch and alignment).
+template <int BM, int BN, int BK, int WM, int WN, bool kTB, int V, int kMinWaves>
 __global__ void __launch_bounds__((BM / WM) * (BN / WN) * 64)
     __attribute__((amdgpu_waves_per_eu(kMinWaves)))
-    grouped_any_kernel(GroupedProblem p, Epilogue ep, int tiles_n, unsigned cap) {
-  constexpr int BK = 16;
+    grouped_even_kernel(GroupedProblem p, Epilogue ep, int tiles_n, unsigned cap) {
   __shared__ __attribute__((aligned(16))) float pool[2 * (BM + BN) * BK];
   __shared__ int row_a[BM], row_c[BM];
   const int lane = threadIdx.x & 63;
@@ -214,14 +120,13 @@ __global__ void __launch_bounds__((BM / WM) * (BN / WN) * 64)
   at.m0 = begin + (tm - (int)first) * BM;
   at.n0 = tn * BN;
   find_rows<BM>(p, at, row_a, row_c);
-  grouped_tile<BM, BN, BK, WM, WN, kTB, 1>(pool, row_a, row_c, at.absent, p, ep, at.g, at.n0, wave,
+  grouped_tile<BM, BN, BK, WM, WN, kTB, V>(pool, row_a, row_c, at.absent, p, ep, at.g, at.n0, wave,
                                            lane);
 }
 
 hipError_t launch_mixed(const GroupedProblem& p, const Epilogue& e, hipStream_t s) {
   const int64_t tiles_n = ((int64_t)p.N + 127) / 128;
   const int64_t cap = most_row_tiles(p.rows, p.groups, 128);
-  // the quarters of less than one round take at most three more workgroups a CU
   if (cap * tiles_n + 3 * kCus > 0x7fffffff) return hipErrorInvalidConfiguration;
   const dim3 grid = tile_grid(cap * tiles_n + 3 * kCus);
   if (p.tb) {
@@ -234,18 +139,18 @@ hipError_t launch_mixed(const GroupedProblem& p, const Epilogue& e, hipStream_t 
   return hipGetLastError();
 }
 
-template <int BM, int BN, int WM, int WN, int kMinWaves>
-hipError_t launch_any(const GroupedProblem& p, const Epilogue& e, hipStream_t s) {
+template <int BM, int BN, int BK, int WM, int WN, int V, int kMinWaves>
+hipError_t launch_even(const GroupedProblem& p, const Epilogue& e, hipStream_t s) {
   const int64_t tiles_n = ((int64_t)p.N + BN - 1) / BN;
   const int64_t cap = most_row_tiles(p.rows, p.groups, BM);
   if (cap * tiles_n > 0x7fffffff) return hipErrorInvalidConfiguration;
   const dim3 grid = tile_grid(cap * tiles_n), block((BM / WM) * (BN / WN) * 64);
   if (p.tb) {
-    hipLaunchKernelGGL((grouped_any_kernel<BM, BN, WM, WN, true, kMinWaves>), grid, block, 0, s, p,
-                       e, (int)tiles_n, (unsigned)cap);
+    hipLaunchKernelGGL((grouped_even_kernel<BM, BN, BK, WM, WN, true, V, kMinWaves>), grid, block,
+                       0, s, p, e, (int)tiles_n, (unsigned)cap);
   } else {
-    hipLaunchKernelGGL((grouped_any_kernel<BM, BN, WM, WN, false, kMinWaves>), grid, block, 0, s,
-                       p, e, (int)tiles_n, (unsigned)cap);
+    hipLaunchKernelGGL((grouped_even_kernel<BM, BN, BK, WM, WN, false, V, kMinWaves>), grid, block,
+                       0, s, p, e, (int)tiles_n, (unsigned)cap);
   }
   return hipGetLastError();
 }
@@ -268,13 +173,18 @@ hipError_t launch_grouped(const GroupedProblem& call, const Epilogue& e, hipStre
   // and strides of 16 bytes, and the contiguous sizes multiples of 4
   const bool wide = aligned16(p.A) && aligned16(p.B) && p.lda % 4 == 0 && p.ldb % 4 == 0 &&
                     (p.groups == 1 || p.sb % 4 == 0) && p.K % 4 == 0 && (p.tb || p.N % 4 == 0);
-  if (wide) return launch_mixed(p, e, s);
-  // 128 x 128 tiles where they make two rounds of the CUs (8 x 1000 x 1023 x 2047:
-  // 336 us against 452 us), 64 x 64 below (16 x 200 x 511 x 1025: 88 against 74 us)
-  const int64_t row_tiles = (int64_t)p.rows / 128 + p.groups / 2;
-  if (row_tiles * (((int64_t)p.N + 127) / 128) >= 2 * (int64_t)kCus)
-    return launch_any<128, 128, 64, 32, 2>(p, e, s);
-  return launch_any<64, 64, 32, 32, 4>(p, e, s);
+  // about how many 128 x 128 tiles
+  const int64_t tiles =
+      ((int64_t)p.rows / 128 + p.groups / 2) * (((int64_t)p.N + 127) / 128);
+  // below a round of the CUs 64 x 64 tiles, four workgroups a CU
+  if (wide)
+    return tiles < (int64_t)kCus ? launch_even<64, 64, 32, 32, 32, 4, 4>(p, e, s)
+                                 : launch_mixed(p, e, s);
+  // single floats: 128 x 128 tiles where they make two rounds of the CUs (8 x 1000 x
+  // 1023 x 2047: 336 us against 452 us), 64 x 64 below (16 x 200 x 511 x 1025: 88
+  // against 74 us)
+  if (tiles >= 2 * (int64_t)kCus) return launch_even<128, 128, 16, 64, 32, 1, 2>(p, e, s);
+  return launch_even<64, 64, 16, 32, 32, 1, 4>(p, e, s);
 }
 
 }  // namespace gemmf32

@@ -54,14 +54,15 @@ __global__ void __launch_bounds__((BM / WM) * (BN / WN) * 64)
   end = __builtin_amdgcn_readfirstlane(end);
   // an empty group may begin behind the last place: no index entry to look at
   const bool none = begin == end;
-  Operand<BM, BK, kWaves, false, V, true> opa;
-  Operand<BN, BK, kWaves, false, V, true> opb;
-  opa.init_rc(p.A, p.lda, tm * BM, p.M, wave, lane);
-  opb.init_rc(p.B, p.ldb, tn * BN, p.N, wave, lane);
+  Source<BK, Operand<BM, BK, kWaves, false, V, true>, Operand<BN, BK, kWaves, false, V, true>> src(
+      p.lda, p.ldb, end - begin, wave, lane);
+  src.a.init_rc(p.A, p.lda, tm * BM, p.M, wave, lane);
+  src.b.init_rc(p.B, p.ldb, tn * BN, p.N, wave, lane);
+  src.ga = Gather{none ? nullptr : p.ia, p.rows_a};
+  src.gb = Gather{none ? nullptr : p.ib, p.rows_b};
+  src.first = begin;
   floatx16 acc[WM / 32][WN / 32];
-  k_loop<BM, BN, BK, WM, WN>(pool, opa, opb, Gather{none ? nullptr : p.ia, p.rows_a},
-                             Gather{none ? nullptr : p.ib, p.rows_b}, begin, p.lda, p.ldb,
-                             end - begin, wave, lane, acc);
+  k_loop<BM, BN, BK, WM, WN>(pool, src, wave, lane, acc);
   store_blocks<WM / 32, WN / 32>(acc, p.C + g * p.sc, p.ldc, p.M, p.N,
                                  tm * BM + (wave % (BM / WM)) * WM,
                                  tn * BN + (wave / (BM / WM)) * WN, lane, false, ep);
