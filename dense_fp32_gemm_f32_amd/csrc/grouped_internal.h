@@ -80,7 +80,16 @@ inline dim3 tile_grid(int64_t n) {
 }
 
 #if defined(__HIP__)
+constexpr unsigned kXcds = 8;
 __device__ __forceinline__ unsigned tile_id() { return blockIdx.y * gridDim.x + blockIdx.x; }
+
+// Position `at` of n positions dealt to the XCDs round robin by workgroup id, so
+// that each XCD has a contiguous range; -1 past the end.
+__device__ __forceinline__ int xcd_position(unsigned at, unsigned n) {
+  const unsigned x = at % kXcds, q = n / kXcds, rem = n % kXcds;
+  if (at / kXcds >= q + (x < rem ? 1u : 0u)) return -1;
+  return (int)(x * q + min(x, rem) + at / kXcds);
+}
 
 // Group g's places, taken into [0, rows]; a group that ends before it begins
 // is empty.

@@ -1,7 +1,7 @@
 // The product of few rows of A with a strip of B's columns, K split over the
-// 8 waves of a workgroup (gfx950): bound by reading the weights, or A, once.
+// waves of a workgroup (gfx950): bound by reading the weights, or A, once.
 //
-// Wave w takes the chunks of 16 U k numbered w, w + 8, ... and multiplies them
+// Wave w takes the chunks of 16 U k numbered w, w + kWaves, ... and multiplies them
 // from registers with v_mfma_f32_16x16x4_f32, whose operand layout needs no
 // LDS: lane (h = l / 16, c = l % 16) holds A[row c][k slot h] and B[k slot h][column
 // c].  One 16-byte load gives a lane four consecutive k of its row of A (k =
@@ -24,13 +24,38 @@ using namespace mfma;
 
 typedef float floatx4 __attribute__((ext_vector_type(4)));
 
-constexpr int kWaves = 8;
 static __device__ __attribute__((aligned(16))) const float kZeroRow[4] = {0.f, 0.f, 0.f, 0.f};
 
+typedef float floatx4_a4 __attribute__((ext_vector_type(4), aligned(4)));
+typedef float floatx2_a4 __attribute__((ext_vector_type(2), aligned(4)));
+// B's loads: non-temporal where B is read once (kOnce)
+template <bool kOnce>
+__device__ __forceinline__ float4 load_b4(const float* p) {
+  if constexpr (!kOnce) return load4(p);
+  const floatx4 v = __builtin_nontemporal_load(reinterpret_cast<const floatx4_a4*>(p));
+  return make_float4(v.x, v.y, v.z, v.w);
+}
+template <bool kOnce>
+__device__ __forceinline__ float2 load_b2(const float* p) {
+  float2 v;
+  if constexpr (kOnce) {
+    const floatx2_a4 x = __builtin_nontemporal_load(reinterpret_cast<const floatx2_a4*>(p));
+    v = make_float2(x.x, x.y);
+  } else {
+    __builtin_memcpy(&v, p, sizeof(v));
+  }
+  return v;
+}
+template <bool kOnce>
+__device__ __forceinline__ float load_b1(const float* p) {
+  return kOnce ? __builtin_nontemporal_load(p) : *p;
+}
+
 // The tile of 16 RM rows by 16 NB columns n0 .. of A B, each wave's share of K
-// left in red (8 * 16 RM * 16 NB floats of LDS) behind a barrier.  row_at(i): the
-// row of A of tile row i, -1 for none.  kTB: B stored N x K.
-template <int RM, int NB, bool kTB, int U, class RowAt>
+// left in red (kWaves * 16 RM * 16 NB floats of LDS) behind a barrier.  row_at(i): the
+// row of A of tile row i, -1 for none.  kTB: B stored N x K; kOnce: its loads are
+// non-temporal.
+template <int kWaves, int RM, int NB, bool kTB, int U, bool kOnce, class RowAt>
 __device__ __forceinline__ void rows_product(float* red, const float* A, int64_t lda, RowAt row_at,
                                              const float* B, int64_t ldb, int N, int n0, int K,
                                              int wave, int lane) {
@@ -66,20 +91,19 @@ __device__ __forceinline__ void rows_product(float* red, const float* A, int64_t
     for (int i = 0; i < RM; ++i) x.a[i] = load4(a_in[i] ? a_row[i] + k : kZeroRow);
     if constexpr (kTB) {
 #pragma unroll
-      for (int j = 0; j < NB; ++j) x.b[j] = load4(b_row[j] + k);
+      for (int j = 0; j < NB; ++j) x.b[j] = load_b4<kOnce>(b_row[j] + k);
     } else {
       const float* b = b_row[0] + (int64_t)k * ldb;
       if (cols == NB) {
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
           if constexpr (NB == 4) {
-            x.b[s] = load4(b + s * ldb);
+            x.b[s] = load_b4<kOnce>(b + s * ldb);
           } else if constexpr (NB == 2) {
-            float2 v;
-            __builtin_memcpy(&v, b + s * ldb, sizeof(v));
+            const float2 v = load_b2<kOnce>(b + s * ldb);
             x.b[s] = make_float4(v.x, v.y, 0.f, 0.f);
           } else {
-            x.b[s] = make_float4(b[s * ldb], 0.f, 0.f, 0.f);
+            x.b[s] = make_float4(load_b1<kOnce>(b + s * ldb), 0.f, 0.f, 0.f);
           }
         }
       } else {
@@ -189,7 +213,7 @@ __device__ __forceinline__ void rows_product(float* red, const float* A, int64_t
 
 // Element x (row x / BN, column x % BN) of the tile that rows_product left in
 // red: the waves' tiles added in wave order.
-template <int RM, int NB>
+template <int kWaves, int RM, int NB>
 __device__ __forceinline__ float rows_sum(const float* red, int x) {
   float sum = red[x];
 #pragma unroll

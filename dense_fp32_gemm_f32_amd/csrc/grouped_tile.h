@@ -340,14 +340,6 @@ __device__ __forceinline__ void k_loop(float* pool, Src& src, int wave, int lane
   if constexpr (kDual) acc[0][0] += acc_odd;
 }
 
-// Position `at` of n positions dealt to the XCDs round robin by workgroup id, so
-// that each XCD has a contiguous range; -1 past the end.
-__device__ __forceinline__ int xcd_position(unsigned at, unsigned n) {
-  const unsigned x = at % kNumXcd, q = n / kNumXcd, rem = n % kNumXcd;
-  if (at / kNumXcd >= q + (x < rem ? 1u : 0u)) return -1;
-  return (int)(x * q + min(x, rem) + at / kNumXcd);
-}
-
 // Mixed tiles: 128 x 128 for whole rounds of the CUs; what is left over, if it
 // fills at most three quarters of a round or there is no whole round, as 64 x 64
 // quarters of its tiles.  (Grouped product of 8192 x 1024 x 2048 in 8 uneven groups:

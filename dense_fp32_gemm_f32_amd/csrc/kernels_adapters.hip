@@ -19,6 +19,7 @@ namespace {
 
 using namespace grouped;
 
+constexpr int kWaves = 8;
 constexpr int kMaxRows = 64, kMaxRank = 128;
 constexpr int kMaxSlices = 16;
 
@@ -34,13 +35,13 @@ __device__ __forceinline__ void partial_tile(float* red, const AdapterProblem& p
                                              int k_len, float* out, int rows) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  rows_product<RM, NB, kTB, 2>(red, p.X + k0, p.ldx, row_at,
+  rows_product<kWaves, RM, NB, kTB, 2, false>(red, p.X + k0, p.ldx, row_at,
                                B + (kTB ? (int64_t)k0 : (int64_t)k0 * ldb), ldb, N, n0, k_len, wave,
                                lane);
   constexpr int BN = 16 * NB;
   for (int x = threadIdx.x; x < 16 * RM * BN; x += kWaves * 64) {
     const int r = x / BN, col = n0 + x % BN;
-    if (r < rows && col < N) out[(int64_t)r * N + col] = rows_sum<RM, NB>(red, x);
+    if (r < rows && col < N) out[(int64_t)r * N + col] = rows_sum<kWaves, RM, NB>(red, x);
   }
 }
 

@@ -8,10 +8,10 @@ namespace {
 
 using namespace grouped;
 
-template <int RM, int NB, bool kTB, int U>
+template <int kWaves, int RM, int NB, bool kTB, int U, bool kOnce>
 __device__ __forceinline__ void rows_tile(float* red, const GroupedProblem& p, const Epilogue& ep,
                                           int g, int m0, int end, int n0, int wave, int lane) {
-  rows_product<RM, NB, kTB, U>(
+  rows_product<kWaves, RM, NB, kTB, U, kOnce>(
       red, p.A, p.lda,
       [&](int i) {
         if (m0 + i >= end) return -1;
@@ -36,11 +36,11 @@ __device__ __forceinline__ void rows_tile(float* red, const GroupedProblem& p, c
     const int r = p.ic ? p.ic[at] : at;
     if (r < 0 || r >= p.rows_c) continue;
     float* out = p.C + (int64_t)r * p.ldc + col;
-    *out = epilogue_apply(e, scale * rows_sum<RM, NB>(red, x), out, col);
+    *out = epilogue_apply(e, scale * rows_sum<kWaves, RM, NB>(red, x), out, col);
   }
 }
 
-template <int RM, int NB, bool kTB, int U>
+template <int kWaves, int RM, int NB, bool kTB, int U, bool kOnce>
 __global__ void __launch_bounds__(kWaves * 64)
     grouped_rows_kernel(GroupedProblem p, Epilogue ep, int strips, unsigned cap) {
   constexpr int BM = 16 * RM;
@@ -49,58 +49,78 @@ __global__ void __launch_bounds__(kWaves * 64)
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   RowTiles rt{p.offsets, p.groups, p.rows, BM, lane, cap, 0};
   const unsigned total = rt.total();
-  const unsigned id = tile_id(), t = id / strips;
-  if (t >= total) return;
+  // each XCD takes a contiguous range of the tiles, strips of a group together
+  const int id = xcd_position(tile_id(), total * (unsigned)strips);
+  if (id < 0) return;
+  const unsigned t = (unsigned)id / strips;
   int g = 0, begin = 0, end = 0;
   unsigned first = 0;
   if (!rt.find(t, g, begin, end, first)) return;
   const int m0 = begin + (int)(t - first) * BM, n0 = (int)(id % strips) * 16 * NB;
   if (RM == 1 || end - m0 <= 16) {
-    rows_tile<1, NB, kTB, U>(red, p, ep, g, m0, min(end, m0 + 16), n0, wave, lane);
+    rows_tile<kWaves, 1, NB, kTB, U, kOnce>(red, p, ep, g, m0, min(end, m0 + 16), n0, wave, lane);
   } else {
-    rows_tile<RM, NB, kTB, U>(red, p, ep, g, m0, min(end, m0 + BM), n0, wave, lane);
+    rows_tile<kWaves, RM, NB, kTB, U, kOnce>(red, p, ep, g, m0, min(end, m0 + BM), n0, wave, lane);
   }
 }
 
-template <int RM, int NB>
+// kWaves waves, chunks of 16 kU k; with B stored K x N a strip's runs of whole lines
+// are read once and non-temporally (64 groups of 1024 x 1024, weights not in a
+// cache: 51 against 56 us; stored N x K a load reads half lines, which a
+// non-temporal load fetches twice: 56 against 54 us).
+template <int kWaves, int RM, int NB, bool kTB, int kU>
 hipError_t launch(const GroupedProblem& p, const Epilogue& e, hipStream_t s) {
   const int64_t strips = ((int64_t)p.N + 16 * NB - 1) / (16 * NB);
   const int64_t cap = most_row_tiles(p.rows, p.groups, 16 * RM);
   if (cap * strips > 0x7fffffff) return hipErrorInvalidConfiguration;
-  const dim3 grid = tile_grid(cap * strips), block(kWaves * 64);
-  if (p.tb) {
-    hipLaunchKernelGGL((grouped_rows_kernel<RM, NB, true, 4>), grid, block, 0, s, p, e, (int)strips,
-                       (unsigned)cap);
-  } else {
-    hipLaunchKernelGGL((grouped_rows_kernel<RM, NB, false, NB == 4 ? 2 : 4>), grid, block, 0, s, p,
-                       e, (int)strips, (unsigned)cap);
-  }
+  constexpr bool kOnce = !kTB && (kWaves == 4 || (kWaves == 16 && NB == 2));
+  hipLaunchKernelGGL((grouped_rows_kernel<kWaves, RM, NB, kTB, kU, kOnce>), tile_grid(cap * strips),
+                     dim3(kWaves * 64), 0, s, p, e, (int)strips, (unsigned)cap);
   return hipGetLastError();
 }
 
+// Many workgroups: 64 columns each; B stored K x N in 4 waves that look one step
+// ahead, so that four workgroups share a CU (32 x 1024 x 2048 with 6 places a
+// group: 49 us against 52 us for 8 waves that look two steps ahead).
 template <int RM>
-hipError_t launch_strips(const GroupedProblem& p, int nb, const Epilogue& e, hipStream_t s) {
-  return nb == 1 ? launch<RM, 1>(p, e, s) : nb == 2 ? launch<RM, 2>(p, e, s)
-                                                    : launch<RM, 4>(p, e, s);
+hipError_t launch_many(const GroupedProblem& p, const Epilogue& e, hipStream_t s) {
+  return p.tb ? launch<8, RM, 4, true, 4>(p, e, s) : launch<4, RM, 4, false, 1>(p, e, s);
+}
+
+// Few workgroups: 16 waves each, 32 or 16 columns.
+template <int RM, bool kTB>
+hipError_t launch_few(const GroupedProblem& p, int nb, const Epilogue& e, hipStream_t s) {
+  return nb == 1 ? launch<16, RM, 1, kTB, 1>(p, e, s) : launch<16, RM, 2, kTB, 1>(p, e, s);
+}
+
+// Few columns: 16 places a workgroup, 8 waves, all columns in one strip.
+template <bool kTB>
+hipError_t launch_thin(const GroupedProblem& p, const Epilogue& e, hipStream_t s) {
+  if (p.N <= 16) return launch<8, 1, 1, kTB, 4>(p, e, s);
+  if (p.N <= 32) return launch<8, 1, 2, kTB, 4>(p, e, s);
+  return launch<8, 1, 4, kTB, kTB ? 4 : 2>(p, e, s);
 }
 
 }  // namespace
 
 hipError_t launch_grouped_rows(const GroupedProblem& p, const Epilogue& e, hipStream_t s) {
-  // few columns: 16 places a workgroup, all columns in one strip up to 64 (4096
-  // places of 2048, 32 columns: 14 us against 20 us for 32 places)
-  if (p.N <= 64) return launch_strips<1>(p, p.N <= 16 ? 1 : p.N <= 32 ? 2 : 4, e, s);
-  // few rows in a group: 32 places where groups have more than 10 on average (16
-  // groups of 19, 1024 x 1024: 19 against 24 us), else 16 (less LDS: 6 places,
-  // 32 x 1024 x 2048: 47 against 51 us); strips as wide as leaves two workgroups a
-  // CU (64 groups of one place: 64 columns 43 us, 32 columns 51, 16 columns 59; 8 of
-  // 2048 x 1024: 21, 18 and 16 us)
+  // few columns (4096 places of 2048, 32 columns: 14 us against 20 us for 32 places
+  // a workgroup)
+  if (p.N <= 64) return p.tb ? launch_thin<true>(p, e, s) : launch_thin<false>(p, e, s);
+  // few rows in a group: 32 places a workgroup where groups have more than 10 on
+  // average (16 groups of 19, 1024 x 1024: 19 against 24 us), else 16 (less LDS: 6
+  // places, 32 x 1024 x 2048: 47 against 51 us)
   const int64_t busy = p.rows < p.groups ? p.rows : p.groups;
   const bool two = p.rows > 10 * busy;
   const int64_t tiles = busy * ((p.rows / busy + (two ? 31 : 15)) / (two ? 32 : 16));
-  int nb = 4;
-  while (nb > 1 && tiles * (((int64_t)p.N + 16 * nb - 1) / (16 * nb)) < 512) nb /= 2;
-  return two ? launch_strips<2>(p, nb, e, s) : launch_strips<1>(p, nb, e, s);
+  // strips of 64 columns where they leave two workgroups a CU, of 32 where those
+  // leave one (8 groups of one place, 2048 x 1024: 15 us against 22 and 18 us for 64
+  // and 16 columns; one of 4096 x 4096: 16 us for 16 columns against 21 for 32)
+  if (tiles * (((int64_t)p.N + 63) / 64) >= 512)
+    return two ? launch_many<2>(p, e, s) : launch_many<1>(p, e, s);
+  const int nb = tiles * (((int64_t)p.N + 31) / 32) >= 256 ? 2 : 1;
+  if (p.tb) return two ? launch_few<2, true>(p, nb, e, s) : launch_few<1, true>(p, nb, e, s);
+  return two ? launch_few<2, false>(p, nb, e, s) : launch_few<1, false>(p, nb, e, s);
 }
 
 }  // namespace gemmf32
