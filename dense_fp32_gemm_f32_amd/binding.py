@@ -498,9 +498,15 @@ def selected_kernel(A, B, C=None) -> str:
 # ---- grouped products --------------------------------------------------------
 # (short calls: the checks below read each tensor's sizes and strides once)
 
-def _stream(device):
+def _on(t, call, *args):
+    """call(*args, stream) with t's device current, on torch's current stream of it."""
     import torch
-    return torch._C._cuda_getCurrentRawStream(device.index)
+    index = t.device.index
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if torch._C._cuda_getDevice() == index:
+        return call(*args, stream)
+    with _device(t):
+        return call(*args, stream)
 
 
 def _index(t, name, device, count=None):
@@ -603,15 +609,15 @@ def group_rows(index, groups, *, per_row=1):
     """The entries of a 1-D int32 GPU tensor ordered by the group they name
     (values outside [0, groups) name none).  Returns int32 tensors ``offsets``
     (groups + 1), ``order`` (the entries by (group, entry)) and ``rows``
-    (order // per_row); both hold -1 from offsets[groups] on."""
+    (order // per_row); both hold -1 from offsets[groups] on.  (The three are
+    parts of one allocation.)"""
     dev = _gpu(index, "index")
     ptr = _index(index, "index", dev)
     n, groups = index.shape[0], int(groups)
-    offsets = index.new_empty(max(groups, 0) + 1)
-    order, rows = index.new_empty(n), index.new_empty(n)
-    with _device(index):
-        rc = gemm_f32_group_rows(n, groups, int(per_row), ptr, offsets.data_ptr(),
-                                 order.data_ptr(), rows.data_ptr(), _stream(dev))
+    places = max(groups, 0) + 1
+    offsets, order, rows = index.new_empty(places + 2 * n).split_with_sizes((places, n, n))
+    rc = _on(index, gemm_f32_group_rows, n, groups, int(per_row), ptr, offsets.data_ptr(),
+             order.data_ptr(), rows.data_ptr())
     if rc != GEMM_F32_OK:
         raise GemmError(rc, "gemm_f32_group_rows")
     return offsets, order, rows
@@ -637,10 +643,9 @@ def gemm_grouped(A, B, offsets, C=None, *, trans_b=False, alpha=1.0, beta=0.0, b
         C = A.new_empty((rows, N))
     c, ldc, rows_c, _ = _matrix(C, "C", dev, cols=N)
     bptr, sbias = _biases(bias, dev, groups, N)
-    with _device(A):
-        rc = gemm_f32_grouped(1 if trans_b else 0, rows, N, K, groups,
-                              _index(offsets, "offsets", dev), alpha, a, lda, rows_a, ia, b, ldb,
-                              sb, beta, c, ldc, rows_c, ic, bptr, sbias, int(act), _stream(dev))
+    rc = _on(A, gemm_f32_grouped, 1 if trans_b else 0, rows, N, K, groups,
+             _index(offsets, "offsets", dev), alpha, a, lda, rows_a, ia, b, ldb, sb, beta, c, ldc,
+             rows_c, ic, bptr, sbias, int(act))
     if rc != GEMM_F32_OK:
         raise GemmError(rc, "gemm_f32_grouped")
     return C
@@ -660,10 +665,8 @@ def gemm_grouped_wgrad(A, B, offsets, C=None, *, alpha=1.0, beta=0.0, index_a=No
     if C is None:
         C = A.new_empty((groups, M, N))
     c, ldc, sc, _, _ = _stack(C, "C", dev, groups, M, N)
-    with _device(A):
-        rc = gemm_f32_grouped_wgrad(rows, M, N, groups, _index(offsets, "offsets", dev), alpha,
-                                    a, lda, rows_a, ia, b, ldb, rows_b, ib, beta, c, ldc, sc,
-                                    _stream(dev))
+    rc = _on(A, gemm_f32_grouped_wgrad, rows, M, N, groups, _index(offsets, "offsets", dev), alpha,
+             a, lda, rows_a, ia, b, ldb, rows_b, ib, beta, c, ldc, sc)
     if rc != GEMM_F32_OK:
         raise GemmError(rc, "gemm_f32_grouped_wgrad")
     return C
@@ -691,12 +694,10 @@ def gemm_adapters(X, W, down, up, offsets, order, Y=None, H=None, *, trans=False
         H = X.new_empty((places, R))
     y, ldy, _, _ = _matrix(Y, "Y", dev, M, N)
     h, ldh, _, _ = _matrix(H, "H", dev, places, R)
-    with _device(X):
-        rc = gemm_f32_adapters(1 if trans else 0, M, N, K, R, adapters, places,
-                               _index(offsets, "offsets", dev), _index(order, "order", dev),
-                               _vector(scale, "scale", dev, adapters), x, ldx, w, ldw, d, ldd, sd,
-                               u, ldu, su, _vector(bias, "bias", dev, N), h, ldh, y, ldy,
-                               _stream(dev))
+    rc = _on(X, gemm_f32_adapters, 1 if trans else 0, M, N, K, R, adapters, places,
+             _index(offsets, "offsets", dev), _index(order, "order", dev),
+             _vector(scale, "scale", dev, adapters), x, ldx, w, ldw, d, ldd, sd, u, ldu, su,
+             _vector(bias, "bias", dev, N), h, ldh, y, ldy)
     if rc != GEMM_F32_OK:
         raise GemmError(rc, "gemm_f32_adapters")
     return Y, H
