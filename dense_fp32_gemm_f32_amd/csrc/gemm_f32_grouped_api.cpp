@@ -76,6 +76,12 @@ int launched(hipError_t e) {
   return GEMM_F32_ERR_LAUNCH;
 }
 
+// 16-byte copies fit both operands of X op(W).
+bool wide(const float* X, int64_t ldx, const float* W, int64_t ldw, int64_t N, int64_t K, bool t) {
+  return (((uintptr_t)X | (uintptr_t)W) & 15u) == 0 && ldx % 4 == 0 && ldw % 4 == 0 && K % 4 == 0 &&
+         (t || N % 4 == 0);
+}
+
 template <class T>
 Range used(const T* p, int64_t count) {
   return Range{p, p ? count : 0};
@@ -278,16 +284,37 @@ int gemm_f32_adapters(int trans, int64_t M, int64_t N, int64_t K, int64_t R, int
   a.groups = (int)groups;
   a.places = (int)places;
   a.trans = t;
-  float* work = nullptr;   // partial sums, or the map of rows
   if (gemmf32::adapters_few(a)) {
-    rc = gemmf32::host_partials(dev, s, gemmf32::adapters_few_floats(a), &work);
-    return rc != GEMM_F32_OK ? rc : launched(gemmf32::launch_adapters_few(a, work, s));
+    float* part = nullptr;
+    rc = gemmf32::host_partials(dev, s, gemmf32::adapters_few_floats(a), &part);
+    return rc != GEMM_F32_OK ? rc : launched(gemmf32::launch_adapters_few(a, part, s));
   }
-  const bool tiles = gemmf32::adapters_tiles(a);
-  if (tiles) rc = gemmf32::host_partials(dev, s, 2 * (size_t)M, &work);
-  if (rc == GEMM_F32_OK && !tiles)
+  // the projection: gemm_f32_fused, or the grouped product's kernels with one group
+  // where they are faster: 192 to 255 tiles of 128 x 128 (2048 x 1536 x 1024: 59 us
+  // against 67; 3000 x 1024 x 2048: 111 against 127), and few rows with W stored
+  // transposed (100 x 2048 x 2048: 19 against 37 us)
+  const int64_t tiles = (M + 127) / 128 * ((N + 127) / 128);
+  if ((tiles >= 192 && tiles < 256 && wide(X, ldx, W, ldw, N, K, t)) ||
+      (t && M <= 128 && M * N <= 1 << 18)) {
+    GroupedProblem b;
+    b.A = X;
+    b.lda = ldx;
+    b.rows_a = b.rows_c = b.rows = (int)M;
+    b.B = W;
+    b.ldb = ldw;
+    b.C = Y;
+    b.ldc = ldy;
+    b.groups = 1;
+    b.N = (int)N;
+    b.K = (int)K;
+    b.tb = t;
+    Epilogue e;
+    e.bias = bias;
+    rc = launched(gemmf32::launch_grouped(b, e, s));
+  } else {
     rc = gemm_f32_fused(0, trans, M, N, K, 1.f, X, ldx, W, ldw, 0.f, Y, ldy, bias,
                         GEMM_F32_ACT_NONE, stream);
+  }
   if (rc != GEMM_F32_OK) return rc;
   GroupedProblem p;   // H = s_g X[order] op(D_g)
   p.A = X;
@@ -307,31 +334,8 @@ int gemm_f32_adapters(int trans, int64_t M, int64_t N, int64_t K, int64_t R, int
   p.N = (int)R;
   p.K = (int)K;
   p.tb = t;
-  if (tiles) {
-    p.map = reinterpret_cast<int*>(work);
-    rc = launched(gemmf32::launch_grouped_rows(p, Epilogue{}, s));
-    return rc != GEMM_F32_OK ? rc : launched(gemmf32::launch_adapters_tiles(a, p.map, s));
-  }
   rc = launched(gemmf32::launch_grouped(p, Epilogue{}, s));
-  if (rc != GEMM_F32_OK) return rc;
-  GroupedProblem q = p;   // Y[order] += H op(U_g)
-  q.A = H;
-  q.lda = ldh;
-  q.rows_a = (int)places;
-  q.ia = nullptr;
-  q.B = U;
-  q.ldb = ldu;
-  q.sb = strideU;
-  q.C = Y;
-  q.ldc = ldy;
-  q.rows_c = (int)M;
-  q.ic = order;
-  q.gscale = nullptr;
-  q.N = (int)N;
-  q.K = (int)R;
-  Epilogue add;
-  add.beta = 1.f;
-  return launched(gemmf32::launch_grouped(q, add, s));
+  return rc != GEMM_F32_OK ? rc : launched(gemmf32::launch_adapters_add(a, s));
 }
 
 }  // extern "C"

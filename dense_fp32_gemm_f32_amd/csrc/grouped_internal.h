@@ -14,6 +14,7 @@ namespace gemmf32 {
 // Place i (0 <= i < rows) belongs to group g when offsets[g] <= i < offsets[g+1].
 // Product (launch_grouped):   C[ic(i)] = act(alpha s_g A[ia(i)] op(B_g) + beta C[ic(i)] + bias_g)
 // Gradient (launch_grouped_wgrad): C_g = alpha sum_i A[ia(i)]^T B[ib(i)] + beta C_g
+// Without offsets (product only) all places are of group 0.
 // An index array that is NULL is the identity.  s_g = gscale[g], 1 when NULL.
 struct GroupedProblem {
   const float* A = nullptr;
@@ -24,8 +25,6 @@ struct GroupedProblem {
   const int* ib = nullptr;   // gradient only
   const int* ic = nullptr;   // product only
   const float* gscale = nullptr;
-  int* map = nullptr;        // product by launch_grouped_rows only: where not NULL,
-                             // map[2 r] = i and map[2 r + 1] = g for A's row r = ia(i)
   int64_t lda = 0, ldb = 0, ldc = 0;
   int64_t sb = 0, sc = 0, sbias = 0;   // strides of B_g, C_g and bias_g
   int rows = 0, groups = 0;
@@ -54,13 +53,10 @@ struct AdapterProblem {
   int M, N, K, R, groups, places;
   bool trans;
 };
-// more rows and few adapters: H first (with the map of launch_grouped_rows, 2 M
-// ints), then the projection with H's products added to its tiles
-// (kernels_adapters_tile.hip)
-bool adapters_tiles(const AdapterProblem& p);
-hipError_t launch_adapters_tiles(const AdapterProblem& p, const int* map, hipStream_t s);
+// Y[order[i]] += H[i] op(U_g) (kernels_adapters.hip)
+hipError_t launch_adapters_add(const AdapterProblem& p, hipStream_t s);
 // few rows: one launch of partial sums and one that joins them
-// (kernels_adapters.hip); the floats of workspace it takes
+// (kernels_adapters_few.hip); the floats of workspace it takes
 bool adapters_few(const AdapterProblem& p);
 size_t adapters_few_floats(const AdapterProblem& p);
 hipError_t launch_adapters_few(const AdapterProblem& p, float* part, hipStream_t s);
@@ -92,11 +88,11 @@ __device__ __forceinline__ int xcd_position(unsigned at, unsigned n) {
 }
 
 // Group g's places, taken into [0, rows]; a group that ends before it begins
-// is empty.
+// is empty.  Without offsets there is one group, of all places.
 __device__ __forceinline__ void group_span(const int* offsets, int g, int rows, int& begin,
                                            int& end) {
-  begin = min(max(offsets[g], 0), rows);
-  end = max(begin, min(offsets[g + 1], rows));
+  begin = offsets ? min(max(offsets[g], 0), rows) : 0;
+  end = offsets ? max(begin, min(offsets[g + 1], rows)) : rows;
 }
 
 // Inclusive sum over the lanes of a wave, held below `cap`.

@@ -107,16 +107,6 @@ struct Operand {
       src[v] = base + (int64_t)row_at(r) * ld + k;
     }
   }
-  // KC, any place for each row: at(r, k) points to the copy's first float at k
-  template <class At>
-  __device__ __forceinline__ void init_rows(int wave, int lane, At at) {
-#pragma unroll
-    for (int v = 0; v < kCopies; ++v) {
-      int r, k;
-      logical(((v * kWaves + wave) * 64 + lane) * V, r, k);
-      src[v] = at(r, k);
-    }
-  }
   // RC: columns r0 + r of a matrix with `cols` columns, row k at k * ld
   __device__ __forceinline__ void init_rc(const float* base, int64_t ld, int r0, int cols,
                                           int wave, int lane) {

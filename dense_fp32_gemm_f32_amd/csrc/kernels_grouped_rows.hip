@@ -20,13 +20,6 @@ __device__ __forceinline__ void rows_tile(float* red, const GroupedProblem& p, c
       },
       p.B + g * p.sb, p.ldb, p.N, n0, p.K, wave, lane);
   constexpr int BM = 16 * RM, BN = 16 * NB;
-  if (p.map && n0 == 0 && (int)threadIdx.x < min(BM, end - m0)) {
-    const int i = m0 + threadIdx.x, r = p.ia ? p.ia[i] : i;
-    if (r >= 0 && r < p.rows_a) {
-      p.map[2 * (int64_t)r] = i;
-      p.map[2 * (int64_t)r + 1] = g;
-    }
-  }
   const float scale = p.gscale ? p.gscale[g] : 1.f;
   Epilogue e = ep;
   if (e.bias) e.bias += g * p.sbias;

@@ -685,3 +685,24 @@ def test_grouped_no_row_of_a_at_all(gpu_lib):
                                  bias=b[:, :n], index_a=index)
         want = torch.cat([b[0, :n].expand(100, n), b[1, :n].expand(50, n)])
         assert torch.equal(C, want)
+
+
+@pytest.mark.parametrize("M,N,K,R", [(30, 96, 64, 8), (200, 260, 256, 16), (700, 1280, 512, 32),
+                                     (4000, 1300, 512, 32), (300, 96, 129, 5)])
+@pytest.mark.parametrize("trans", [False, True])
+def test_adapters_non_finite_factors_stay_with_their_rows(gpu_lib, M, N, K, R, trans):
+    """An infinite or NaN factor of one adapter reaches the rows of that adapter
+    only, though rows of others share their tiles."""
+    index, X, W, down, up, scale, bias, _ = adapters_data(M, N, K, R, 3, trans, True, 46)
+    good = adapters_data(M, N, K, R, 3, trans, True, 46)[3:5]
+    up[1] = float("nan")
+    up[2].view(-1)[5] = float("inf")
+    down[2].view(-1)[3] = float("nan")
+    H.say(f"adapters non-finite M={M} N={N} K={K} R={R} trans={trans}")
+    offsets, order, _ = gpu_lib.group_rows(index.cuda(), 3)
+    Y, _ = gpu_lib.gemm_adapters(X.cuda(), W.cuda(), down.cuda(), up.cuda(), offsets, order,
+                                 trans=trans, scale=scale.cuda(), bias=bias.cuda())
+    want = adapters_reference(X, W, *good, scale, bias, offsets.cpu(), order.cpu(), trans)[0]
+    rows = index < 1
+    assert torch.equal(Y.cpu()[rows].double(), want[rows])
+    assert bool(torch.isnan(Y.cpu()[index == 1]).all())
