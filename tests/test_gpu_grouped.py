@@ -706,3 +706,89 @@ def test_adapters_non_finite_factors_stay_with_their_rows(gpu_lib, M, N, K, R, t
     rows = index < 1
     assert torch.equal(Y.cpu()[rows].double(), want[rows])
     assert bool(torch.isnan(Y.cpu()[index == 1]).all())
+
+
+@pytest.mark.parametrize("M,K,N,R", [(20, 64, 96, 8), (300, 128, 160, 16)])
+@pytest.mark.parametrize("trans", [False, True])
+def test_adapters_places_without_rows(gpu_lib, M, K, N, R, trans):
+    """More places than rows, places of adapters whose row is outside X (their H
+    is that of a row of zeros, no row of Y takes it), places before the first
+    adapter and behind the last."""
+    index, X, W, down, up, _, _, _ = adapters_data(M, N, K, R, 3, trans, True, 47)
+    places = min(64, 2 * M) if M <= 64 else 2 * M
+    order = torch.full((places,), -1, dtype=torch.int32)
+    used = torch.randperm(M, generator=gen(48))[:M - 5].int()
+    order[4:4 + len(used)] = used
+    order[7], order[9], order[11] = M, -3, 2 ** 31 - 1
+    order[1] = used[0]          # in no adapter: before the first place
+    offsets = torch.tensor([4, 10, 10, 4 + len(used)]).int()
+    H.say(f"adapters places without rows M={M} trans={trans}")
+    Hd = torch.full((places, R), float("nan"), device="cuda")
+    Y, Hd = gpu_lib.gemm_adapters(X.cuda(), W.cuda(), down.cuda(), up.cuda(), offsets.cuda(),
+                                  order.cuda(), H=Hd, trans=trans)
+    Wf, D, Uf = (W.t(), down.transpose(1, 2), up.transpose(1, 2)) if trans else (W, down, up)
+    wy, wh = X @ Wf, torch.full((places, R), float("nan"))
+    for g, (b, e) in enumerate(zip(offsets.tolist(), offsets.tolist()[1:])):
+        for i in range(b, e):
+            r = int(order[i])
+            wh[i] = X[r] @ D[g] if 0 <= r < M else 0
+            if 0 <= r < M:
+                wy[r] += wh[i] @ Uf[g]
+    assert torch.equal(Y.cpu(), wy)
+    assert torch.equal(torch.nan_to_num(Hd.cpu(), nan=9e9), torch.nan_to_num(wh, nan=9e9))
+
+
+# the refused call enqueues nothing, so the captured graph is empty by design
+@pytest.mark.filterwarnings("ignore:The CUDA Graph is empty")
+def test_capture_without_workspace_is_refused(gpu_lib):
+    """Adapters of few rows and thin gradients of long groups take the stream's
+    workspace: without one a capturing stream cannot get it."""
+    index, X, W, down, up, _, _, _ = [t.cuda() for t in
+                                      adapters_data(8, 512, 2048, 8, 2, False, True, 49)]
+    offsets, order, _ = gpu_lib.group_rows(index, 2)
+    long, _ = spans([20000])
+    A, B = torch.zeros(20000, 8, device="cuda"), torch.zeros(20000, 64, device="cuda")
+    C = torch.empty(1, 8, 64, device="cuda")
+    Y, Hh = torch.empty(8, 512, device="cuda"), torch.empty(8, 8, device="cuda")
+    long = long.cuda()
+    torch.cuda.synchronize()
+    for call in (lambda: gpu_lib.gemm_adapters(X, W, down, up, offsets, order, Y, Hh),
+                 lambda: gpu_lib.gemm_grouped_wgrad(A, B, long, C)):
+        assert gpu_lib.gemm_f32_release_workspaces() == 0
+        s, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            with pytest.raises(gpu_lib.GemmError) as err:
+                call()
+        assert err.value.status == 6
+    torch.cuda.synchronize()
+
+
+def test_offsets_beyond_32_bits(gpu_lib):
+    """Weights, rows of A and rows of C further apart than 2^31 floats."""
+    g = gen(56)
+    far = 2 ** 31 + 64
+    flat, out = (torch.empty(far + (1 << 20), device="cuda") for _ in range(2))
+    for rows, K, N, trans in ((40, 64, 48, False), (40, 64, 48, True), (300, 64, 256, False),
+                              (300, 64, 256, True), (300, 61, 131, False)):
+        A, W = draw(g, 2, K, integer=True), draw(g, 2, *((N, K) if trans else (K, N)), integer=True)
+        Wd = torch.as_strided(flat, W.shape, (far, W.shape[2], 1))
+        Ad = torch.as_strided(flat, (2, K), (far, 1), 1 << 18)
+        Wd.copy_(W)
+        Ad.copy_(A)
+        offsets, _ = spans([rows // 2, rows - rows // 2])
+        index = torch.randint(0, 2, (rows,), generator=g).int()
+        H.say(f"far operands rows={rows} K={K} N={N} trans={trans}")
+        got = gpu_lib.gemm_grouped(Ad, Wd, offsets.cuda(), trans_b=trans, index_a=index.cuda())
+        Wf = W.transpose(1, 2) if trans else W
+        want = torch.cat([A[index[:rows // 2].long()] @ Wf[0], A[index[rows // 2:].long()] @ Wf[1]])
+        assert torch.equal(got.cpu(), want)
+        # the same rows as the operand of a gradient, and a far C
+        B = draw(g, rows, N, integer=True)
+        Cd = torch.as_strided(out, (2, K, N), (far, N, 1))
+        gpu_lib.gemm_grouped_wgrad(Ad, B.cuda(), offsets.cuda(), Cd, index_a=index.cuda())
+        for e, (b, f) in enumerate(((0, rows // 2), (rows // 2, rows))):
+            assert torch.equal(Cd[e].cpu(), A[index[b:f].long()].t() @ B[b:f])
+        Cr = torch.as_strided(out, (2, N), (far, 1))
+        one, _ = spans([1, 1])
+        gpu_lib.gemm_grouped(Ad, Wd, one.cuda(), Cr, trans_b=trans)
+        assert torch.equal(Cr.cpu(), torch.stack([A[0] @ Wf[0], A[1] @ Wf[1]]))
