@@ -275,8 +275,8 @@ int gemm_f32_group_rows(int64_t n, int64_t groups, int64_t per_row,
  * places from offsets[groups] on.  An index outside its matrix is never
  * followed: such a row of A counts as zeros, such a row of C is not written.
  * Offsets are taken into [0, rows] and a group that ends before it begins is
- * empty; places named by two groups (offsets that fall) and rows of C named
- * twice get one of the values, or none.  beta == 0 does not read C.
+ * empty; what offsets that fall (places of two groups) or a row of C named twice
+ * leave in the rows of C concerned is not specified.  beta == 0 does not read C.
  * Sums and the update are as gemm_f32_fused's; K == 0 gives the
  * update of an empty sum.  The summation order depends on the sizes,
  * alignments and offsets only.
@@ -308,6 +308,8 @@ int gemm_f32_grouped(int transB, int64_t rows, int64_t N, int64_t K,
  * written: a group without places gets beta * C_g (+0.0 when beta == 0; C is
  * not read then).  For weights stored transposed exchange A and B.  With a
  * column of ones for A (M = 1) it sums B's rows: the gradient of the biases.
+ * With M or N of at most 64 and 4096 places or more it may use the stream's
+ * workspace of partial sums.
  *
  * Errors as gemm_f32_grouped; strideC below M rows of ldc GEMM_F32_ERR_ALIAS.
  * groups, M or N == 0 is a successful no-op.
@@ -339,6 +341,9 @@ int gemm_f32_grouped_wgrad(int64_t rows, int64_t M, int64_t N,
  *                       exchanged; its H is G, the gradient of X op(D) scaled;
  *   the gradient of D_g is gemm_f32_grouped_wgrad of X (by order) and G,
  *   the gradient of U_g that of H and dY (by order).
+ * An adapter's values, also infinite ones and NaN, reach the rows of that adapter
+ * only.  Up to 64 rows (and places, with R up to 128) it takes two launches and
+ * the stream's workspace of partial sums, otherwise three launches.
  *
  * Errors as gemm_f32_fused and gemm_f32_grouped; H or Y overlapping
  * anything else GEMM_F32_ERR_ALIAS.  R, groups or places == 0 leaves the

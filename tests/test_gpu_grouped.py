@@ -631,9 +631,10 @@ def test_captured_graphs_replay_as_eager(gpu_lib, T):
                 assert torch.equal(a, b), f"replay {rep} of graph {i} differs"
 
 
-def test_two_streams_at_once(gpu_lib):
+@pytest.mark.parametrize("T", [40, 700])
+def test_two_streams_at_once(gpu_lib, T):
     """Calls on two streams overlap without sharing anything."""
-    a, b = state(80, 700), state(81, 700)
+    a, b = state(80, T), state(81, T)
     want = [[t.clone() for t in together(gpu_lib, s)] for s in (a, b)]
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream(), torch.cuda.Stream()]
