@@ -73,6 +73,7 @@ template <int R, int BK, int kWaves, bool KC, int V, bool kGatherK = false>
 struct Operand {
   static_assert(!(KC && kGatherK), "gathered k needs the rows contiguous");
   static constexpr int kLds = R * BK;
+  static constexpr int kCopyWaves = kWaves;
   static constexpr int kCopies = R * BK / V / (kWaves * 64);   // copies a lane makes
   static_assert(R * BK % (V * kWaves * 64) == 0, "copies divide evenly over the threads");
   static_assert(KC || R % 64 == 0, "the [k][r] swizzle needs 64-wide rows");
@@ -177,6 +178,8 @@ template <int BK, class OpA_, class OpB_>
 struct Source {
   using OpA = OpA_;
   using OpB = OpB_;
+  static constexpr int kWaves = OpA::kCopyWaves;
+  static_assert(kWaves == OpB::kCopyWaves, "the same waves copy both operands");
   OpA a;
   OpB b;
   int64_t lda, ldb;
@@ -202,7 +205,8 @@ struct Source {
   }
 };
 
-// The K loop of a BM x BN tile, wave tiles WM x WN, over src's K-tiles.
+// The K loop of a BM x BN tile, wave tiles WM x WN, over src's K-tiles.  src may
+// copy with more waves than the tile has: those beyond only copy.
 // pool: 2 (BM + BN) BK floats of LDS, read by no wave any more.
 template <int BM, int BN, int BK, int WM, int WN, class Src>
 __device__ __forceinline__ void k_loop(float* pool, Src& src, int wave, int lane,
@@ -262,10 +266,32 @@ __device__ __forceinline__ void k_loop(float* pool, Src& src, int wave, int lane
   constexpr int kReadsPer = (kReadsPerGroup + kHalf - 1) / kHalf;
   constexpr int kCopiesPer = (kTileCopies + kHalf - 1) / kHalf;
 
+  const int ktiles = src.tiles();
+  if constexpr (Src::kWaves > kWavesM * (BN / WN)) {
+    if (wave >= kWavesM * (BN / WN)) {   // the same copies and barriers as below
+      src.seek(0);
+#pragma unroll
+      for (int idx = 0; idx < kTileCopies; ++idx) src.copy(lds_a0, lds_b0, idx);
+      src.seek(1);
+      __builtin_amdgcn_s_waitcnt(0);
+      __syncthreads();
+#pragma unroll
+      for (int idx = 0; idx < kTileCopies; ++idx) src.copy(lds_a1, lds_b1, idx);
+      for (int t = 0; t < ktiles; ++t) {
+        src.seek(t + 2);
+        __builtin_amdgcn_s_waitcnt(0);
+        __syncthreads();
+#pragma unroll
+        for (int idx = 0; idx < kTileCopies; ++idx)
+          src.copy(t & 1 ? lds_a1 : lds_a0, t & 1 ? lds_b1 : lds_b0, idx);
+      }
+      __builtin_amdgcn_s_waitcnt(0);
+      return;
+    }
+  }
   // Branch-free steps: the copies of a K-tile past the end re-read the last
   // one into the buffer no longer needed; the last step reads fragments it does
   // not use.
-  const int ktiles = src.tiles();
   Frag f0, f1;
   src.seek(0);
 #pragma unroll
@@ -332,11 +358,10 @@ __device__ __forceinline__ void k_loop(float* pool, Src& src, int wave, int lane
 
 // Mixed tiles: 128 x 128 for whole rounds of the CUs; what is left over, if it
 // fills at most three quarters of a round or there is no whole round, as 64 x 64
-// quarters of its tiles.  (Grouped product of 8192 x 1024 x 2048 in 8 uneven groups:
-// 287 us, against 334 us with 128 x 128 tiles only, whose fifth round of the CUs is a
-// quarter full, and 319 us with 64 x 64 tiles only; in even groups, four whole
-// rounds, 264, 263 and 296 us.)  The grid has a workgroup for every tile and 3 kCus
-// more.
+// quarters of its tiles.  (Grouped product of 8192 x 1024 x 2048 in 8 uneven groups,
+// 4.25 rounds: 281 us, against 334 us with 128 x 128 tiles only and 319 us with 64 x
+// 64 tiles only; in even groups, four whole rounds, 261, 263 and 296 us.)  The grid
+// has a workgroup for every tile and 3 kCus more.
 constexpr unsigned kCus = 256;
 
 struct MixedTile {

@@ -11,12 +11,13 @@ namespace {
 
 using namespace grouped;
 
-template <int BM, int BN, int BK, int WM, int WN, bool kTB, int V>
+// kWaves waves copy, the first (BM / WM) (BN / WN) of them multiply.
+template <int BM, int BN, int BK, int WM, int WN, bool kTB, int V,
+          int kWaves = (BM / WM) * (BN / WN)>
 __device__ __forceinline__ void grouped_tile(float* pool, const int* row_a, const int* row_c,
                                              bool absent, const GroupedProblem& p,
                                              const Epilogue& ep, int g, int n0, int wave,
                                              int lane) {
-  constexpr int kWaves = (BM / WM) * (BN / WN);
   const float* B = p.B + g * p.sb;
   Source<BK, Operand<BM, BK, kWaves, true, V>, Operand<BN, BK, kWaves, kTB, V>> src(
       p.lda, p.ldb, p.K, wave, lane);
@@ -28,6 +29,7 @@ __device__ __forceinline__ void grouped_tile(float* pool, const int* row_a, cons
   }
   floatx16 acc[WM / 32][WN / 32];
   k_loop<BM, BN, BK, WM, WN>(pool, src, wave, lane, acc);
+  if (kWaves > (BM / WM) * (BN / WN) && wave >= (BM / WM) * (BN / WN)) return;
   const int row0 = (wave % (BM / WM)) * WM;
   if (absent) {   // rows whose index is outside count as zeros
 #pragma unroll
@@ -65,10 +67,11 @@ __device__ __forceinline__ void find_rows(const GroupedProblem& p, Place& at, in
   at.absent = __syncthreads_or(outside);
 }
 
-// 16-byte copies, in mixed tiles; a group's last row tile of at most 64 places is
-// 64 x 128.
+// 16-byte copies, in mixed tiles of 8 waves; four of them multiply a quarter.
+// (64 x 128 tiles for a group's last 64 places or fewer made no shape faster and
+// 8192 x 1024 x 1408 slower, 228 against 197 us.)
 template <bool kTB>
-__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
+__global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4)))
     grouped_mixed_kernel(GroupedProblem p, Epilogue ep, int tiles_n, unsigned cap) {
   constexpr int BM = 128, BN = 128, BK = 32;
   __shared__ __attribute__((aligned(16))) float pool[2 * (BM + BN) * BK];
@@ -87,13 +90,10 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
   if (at.m0 >= at.end || at.n0 >= p.N) return;
   find_rows<BM>(p, at, row_a, row_c);
   if (mt.quarter) {
-    grouped_tile<64, 64, BK, 32, 32, kTB, 4>(pool, row_a, row_c, at.absent, p, ep, at.g, at.n0,
-                                             wave, lane);
-  } else if (at.end - at.m0 <= 64) {
-    grouped_tile<64, 128, BK, 32, 64, kTB, 4>(pool, row_a, row_c, at.absent, p, ep, at.g, at.n0,
-                                              wave, lane);
+    grouped_tile<64, 64, BK, 32, 32, kTB, 4, 8>(pool, row_a, row_c, at.absent, p, ep, at.g, at.n0,
+                                                wave, lane);
   } else {
-    grouped_tile<128, 128, BK, 64, 64, kTB, 4>(pool, row_a, row_c, at.absent, p, ep, at.g, at.n0,
+    grouped_tile<128, 128, BK, 64, 32, kTB, 4>(pool, row_a, row_c, at.absent, p, ep, at.g, at.n0,
                                                wave, lane);
   }
 }
@@ -130,10 +130,10 @@ hipError_t launch_mixed(const GroupedProblem& p, const Epilogue& e, hipStream_t 
   if (cap * tiles_n + 3 * kCus > 0x7fffffff) return hipErrorInvalidConfiguration;
   const dim3 grid = tile_grid(cap * tiles_n + 3 * kCus);
   if (p.tb) {
-    hipLaunchKernelGGL((grouped_mixed_kernel<true>), grid, dim3(256), 0, s, p, e, (int)tiles_n,
+    hipLaunchKernelGGL((grouped_mixed_kernel<true>), grid, dim3(512), 0, s, p, e, (int)tiles_n,
                        (unsigned)cap);
   } else {
-    hipLaunchKernelGGL((grouped_mixed_kernel<false>), grid, dim3(256), 0, s, p, e, (int)tiles_n,
+    hipLaunchKernelGGL((grouped_mixed_kernel<false>), grid, dim3(512), 0, s, p, e, (int)tiles_n,
                        (unsigned)cap);
   }
   return hipGetLastError();
@@ -176,10 +176,15 @@ hipError_t launch_grouped(const GroupedProblem& call, const Epilogue& e, hipStre
   // about how many 128 x 128 tiles
   const int64_t tiles =
       ((int64_t)p.rows / 128 + p.groups / 2) * (((int64_t)p.N + 127) / 128);
-  // below a round of the CUs 64 x 64 tiles, four workgroups a CU
-  if (wide)
-    return tiles < (int64_t)kCus ? launch_even<64, 64, 32, 32, 32, 4, 4>(p, e, s)
-                                 : launch_mixed(p, e, s);
+  if (wide) {
+    // 64 x 64 tiles, four workgroups a CU, below a round of the CUs (21 groups of 261,
+    // 1280 x 384: 71 us against 87 us in mixed tiles), where the second round would be
+    // neither nearly empty nor full (8 of 512, 1024 x 1280: 111 against 123), and for
+    // groups that fill few of the rows of 128 (64 of 128, 512 x 768: 78 against 86)
+    const bool small = tiles < kCus || (tiles >= kCus / 4 * 5 && tiles < 2 * kCus) ||
+                       p.rows <= 192 * (int64_t)p.groups;
+    return small ? launch_even<64, 64, 32, 32, 32, 4, 4>(p, e, s) : launch_mixed(p, e, s);
+  }
   // single floats: 128 x 128 tiles where they make two rounds of the CUs (8 x 1000 x
   // 1023 x 2047: 336 us against 452 us), 64 x 64 below (16 x 200 x 511 x 1025: 88
   // against 74 us)
