@@ -20,6 +20,7 @@
 #include <vector>
 
 #include "gemm_f32_internal.h"
+#include "grouped_internal.h"
 #include "read_probe.h"
 #include "stamps.h"
 #include "tuning_gfx950.h"

@@ -197,11 +197,6 @@ struct NoallocScratch {
 };
 int noalloc_scratch(int dev, hipStream_t s, NoallocScratch* out);
 
-// ---- the host checks and the per-stream partial sums, for other entry files -
-int host_check_device(int* dev);                    // gfx950 only; the current device
-int host_check_pointer(const void* p, int dev);     // memory that device can reach
-int host_partials(int dev, hipStream_t s, size_t floats, float** out);
-
 // ---- the shader clock under fp32 MFMA load (clock_probe.hip) ---------------
 // kClockProbeWorkgroups workgroups of 4 waves, each wave 4 x iters MFMAs;
 // workgroup w writes [s_memtime, s_memrealtime] at its start and end to

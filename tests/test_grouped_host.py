@@ -185,3 +185,16 @@ def test_products_refuse_tensors_whose_rows_overlap():
             binding._pitch(Gpu(s0, 1), "A")
     with pytest.raises(ValueError, match="offsets"):
         binding._groups_of(torch.zeros(0, dtype=torch.int32))
+
+
+def test_recorded_traffic_still_belongs_to_its_kernels():
+    """The grouped products' declarations stay out of the sources that the other
+    kernels' counter records are hashed over: a changed hash drops the record."""
+    import json
+    from pathlib import Path
+
+    from dense_fp32_gemm_f32_amd.prof_summary import source_hash
+    records = json.loads((Path(__file__).parent.parent / "profiles" / "traffic.json").read_text())
+    assert records
+    for kernel, record in records.items():
+        assert record["source_sha256"] == source_hash(kernel), kernel
