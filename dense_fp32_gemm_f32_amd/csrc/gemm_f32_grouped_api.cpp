@@ -210,11 +210,10 @@ int gemm_f32_grouped_wgrad(int64_t rows, int64_t M, int64_t N, int64_t groups,
   e.alpha = alpha;
   e.beta = beta;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (!gemmf32::wgrad_thin(p)) return launched(gemmf32::launch_grouped_wgrad(p, e, s));
   float* part = nullptr;
-  const size_t floats = gemmf32::wgrad_thin_floats(p);
+  const size_t floats = gemmf32::grouped_wgrad_floats(p);
   if (floats > 0) rc = gemmf32::host_partials(dev, s, floats, &part);
-  return rc != GEMM_F32_OK ? rc : launched(gemmf32::launch_wgrad_thin(p, e, part, s));
+  return rc != GEMM_F32_OK ? rc : launched(gemmf32::launch_grouped_wgrad(p, e, part, s));
 }
 
 int gemm_f32_adapters(int trans, int64_t M, int64_t N, int64_t K, int64_t R, int64_t groups,

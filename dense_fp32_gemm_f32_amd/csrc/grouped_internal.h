@@ -41,13 +41,18 @@ struct GroupedProblem {
 hipError_t launch_grouped(const GroupedProblem& p, const Epilogue& e, hipStream_t s);
 // the same for few rows in a group, or few columns (kernels_grouped_rows.hip)
 hipError_t launch_grouped_rows(const GroupedProblem& p, const Epilogue& e, hipStream_t s);
-hipError_t launch_grouped_wgrad(const GroupedProblem& p, const Epilogue& e, hipStream_t s);
+// The gradient, and the floats of workspace (part) it takes.
+hipError_t launch_grouped_wgrad(const GroupedProblem& p, const Epilogue& e, float* part,
+                                hipStream_t s);
+size_t grouped_wgrad_floats(const GroupedProblem& p);
 // the same for M or N of at most 64 (kernels_grouped_wgrad_thin.hip), and the
-// floats of workspace it takes
+// launch that adds the slices' sums in part, slices x groups x M x N
 bool wgrad_thin(const GroupedProblem& p);
 size_t wgrad_thin_floats(const GroupedProblem& p);
 hipError_t launch_wgrad_thin(const GroupedProblem& p, const Epilogue& e, float* part,
                              hipStream_t s);
+hipError_t launch_wgrad_join(const GroupedProblem& p, const Epilogue& e, int slices,
+                             const float* part, hipStream_t s);
 
 // gemm_f32_adapters after its checks: matrices as stored (trans: each transposed).
 struct AdapterProblem {

@@ -3,6 +3,9 @@
 //
 // Both operands have their rows contiguous and are gathered along k (the
 // places), so a K-tile's matrix rows are fetched one K-tile ahead of its copies.
+// Where C has few tiles, long groups are cut into slices of their places.
+#include <algorithm>
+
 #include "grouped_tile.h"
 
 namespace gemmf32 {
@@ -35,24 +38,32 @@ __device__ __forceinline__ int nth_largest(const int* offsets, int groups, int r
 template <int BM, int BN, int BK, int WM, int WN, int V, int kMinWaves>
 __global__ void __launch_bounds__((BM / WM) * (BN / WN) * 64)
     __attribute__((amdgpu_waves_per_eu(kMinWaves)))
-    grouped_wgrad_kernel(GroupedProblem p, Epilogue ep, int tiles_m, int tiles_n) {
+    grouped_wgrad_kernel(GroupedProblem p, Epilogue ep, int tiles_m, int tiles_n, int slices,
+                         float* part) {
   constexpr int kWaves = (BM / WM) * (BN / WN);
   __shared__ __attribute__((aligned(16))) float pool[2 * (BM + BN) * BK];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   // the groups' tiles in order of the groups' sizes, each group's spread over
-  // the XCDs in contiguous ranges
-  const unsigned id = tile_id(), tiles = (unsigned)tiles_m * tiles_n;
-  if (id >= tiles * p.groups) return;
-  const int g = p.groups <= 64 ? nth_largest(p.offsets, p.groups, p.rows, (int)(id / tiles), lane)
-                               : (int)(id / tiles);
+  // the XCDs in contiguous ranges, a slice's together
+  const unsigned id = tile_id(), tiles = (unsigned)tiles_m * tiles_n, each = tiles * slices;
+  if (id >= each * p.groups) return;
+  const int g = p.groups <= 64 ? nth_largest(p.offsets, p.groups, p.rows, (int)(id / each), lane)
+                               : (int)(id / each);
+  const unsigned at = (unsigned)xcd_contiguous_id((int)(id % each), (int)each);
+  const int slice = (int)(at / tiles);
   int tm, tn;
-  tile_coords(xcd_contiguous_id((int)(id % tiles), (int)tiles), tiles_m, tiles_n, tm, tn);
+  tile_coords((int)(at % tiles), tiles_m, tiles_n, tm, tn);
   int begin, end;
   group_span(p.offsets, g, p.rows, begin, end);
+  if (slices > 1) {   // whole K-tiles of the group's places
+    const int64_t len = ((int64_t)(end - begin) + slices * BK - 1) / (slices * BK) * BK;
+    begin = (int)min((int64_t)end, begin + slice * len);
+    end = (int)min((int64_t)end, begin + len);
+  }
   begin = __builtin_amdgcn_readfirstlane(begin);
   end = __builtin_amdgcn_readfirstlane(end);
-  // an empty group may begin behind the last place: no index entry to look at
+  // an empty span may begin behind the last place: no index entry to look at
   const bool none = begin == end;
   Source<BK, Operand<BM, BK, kWaves, false, V, true>, Operand<BN, BK, kWaves, false, V, true>> src(
       p.lda, p.ldb, end - begin, wave, lane);
@@ -63,40 +74,73 @@ __global__ void __launch_bounds__((BM / WM) * (BN / WN) * 64)
   src.first = begin;
   floatx16 acc[WM / 32][WN / 32];
   k_loop<BM, BN, BK, WM, WN>(pool, src, wave, lane, acc);
-  store_blocks<WM / 32, WN / 32>(acc, p.C + g * p.sc, p.ldc, p.M, p.N,
-                                 tm * BM + (wave % (BM / WM)) * WM,
-                                 tn * BN + (wave / (BM / WM)) * WN, lane, false, ep);
+  const int m0 = tm * BM + (wave % (BM / WM)) * WM, n0 = tn * BN + (wave / (BM / WM)) * WN;
+  if (slices > 1) {
+    float* C = part + ((int64_t)slice * p.groups + g) * p.M * p.N;
+    store_blocks<WM / 32, WN / 32>(acc, C, p.N, p.M, p.N, m0, n0, lane, false, Epilogue{});
+  } else {
+    store_blocks<WM / 32, WN / 32>(acc, p.C + g * p.sc, p.ldc, p.M, p.N, m0, n0, lane, false, ep);
+  }
 }
 
 template <int BM, int BN, int BK, int WM, int WN, int V, int kMinWaves>
-hipError_t launch(const GroupedProblem& p, const Epilogue& e, hipStream_t s) {
+hipError_t launch(const GroupedProblem& p, const Epilogue& e, int slices, float* part,
+                  hipStream_t s) {
   const int64_t tiles_m = ((int64_t)p.M + BM - 1) / BM, tiles_n = ((int64_t)p.N + BN - 1) / BN;
-  const int64_t n = tiles_m * tiles_n * p.groups;
+  const int64_t n = tiles_m * tiles_n * slices * p.groups;
   if (n > 0x7fffffff) return hipErrorInvalidConfiguration;
   hipLaunchKernelGGL((grouped_wgrad_kernel<BM, BN, BK, WM, WN, V, kMinWaves>), tile_grid(n),
-                     dim3((BM / WM) * (BN / WN) * 64), 0, s, p, e, (int)tiles_m, (int)tiles_n);
-  return hipGetLastError();
+                     dim3((BM / WM) * (BN / WN) * 64), 0, s, p, e, (int)tiles_m, (int)tiles_n,
+                     slices, part);
+  const hipError_t err = hipGetLastError();
+  return err != hipSuccess || slices == 1 ? err : launch_wgrad_join(p, e, slices, part, s);
 }
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
+int64_t tiles_of(const GroupedProblem& p, int side) {
+  return ((int64_t)p.M + side - 1) / side * (((int64_t)p.N + side - 1) / side) * p.groups;
+}
+
+// 128 x 128 tiles, two a CU, where they make two rounds or more (16 groups of
+// 512, 1024 x 1024: 148 us against 168 us for 64 x 64; 1024 x 2048 in 8 uneven
+// groups of 8192 places in all: 289 against 328 us; 1023 x 2047 with single-float
+// copies, 8000 places: 362 against 459 us); below that a tile of a long group
+// would run alone (3000 + 1000, 1024 x 1024: 219 against 108 us)
+bool large_tiles(const GroupedProblem& p) { return tiles_of(p, 128) >= 512; }
+
+// Below that up to four workgroups of 64 x 64 a CU, by slices of 256 places or more
+// in groups of average size and of 2048 in a group that has nearly all, whose sums
+// go through the workspace and a second launch (2 groups of 2048, 256 x 256: 16 us
+// against 54 us in one slice; 1 of 4096, 768 x 768: 59 against 129; 2 of 2000, 511 x
+// 300, single floats: 40 against 120; 2 of 4096, 1024 x 512: 89 against 132; 8 of 256,
+// 256 x 256, stays in one slice: 11 against 13 for 2).
+int slices_of(const GroupedProblem& p) {
+  if (large_tiles(p)) return 1;
+  const int64_t s = std::min(1024 / tiles_of(p, 64),
+                             std::max(p.rows / (256 * (int64_t)p.groups), (int64_t)p.rows / 2048));
+  return (int)std::max((int64_t)1, s);
+}
+
 }  // namespace
 
-hipError_t launch_grouped_wgrad(const GroupedProblem& p, const Epilogue& e, hipStream_t s) {
+size_t grouped_wgrad_floats(const GroupedProblem& p) {
+  if (wgrad_thin(p)) return wgrad_thin_floats(p);
+  const int slices = slices_of(p);
+  return slices > 1 ? (size_t)slices * p.groups * p.M * p.N : 0;
+}
+
+hipError_t launch_grouped_wgrad(const GroupedProblem& p, const Epilogue& e, float* part,
+                                hipStream_t s) {
+  if (wgrad_thin(p)) return launch_wgrad_thin(p, e, part, s);
   const bool wide = aligned16(p.A) && aligned16(p.B) && p.lda % 4 == 0 && p.ldb % 4 == 0 &&
                     p.M % 4 == 0 && p.N % 4 == 0;
-  // 128 x 128 tiles, two a CU, where they make two rounds or more (16 groups of
-  // 512, 1024 x 1024: 148 us against 168 us for 64 x 64; 1024 x 2048 in 8 uneven
-  // groups of 8192 places in all: 289 against 328 us; 1023 x 2047 with single-float
-  // copies, 8000 places: 362 against 459 us); below that a tile of a long group
-  // would run alone (3000 + 1000, 1024 x 1024: 219 against 108 us)
-  const int64_t tiles = ((int64_t)p.M + 127) / 128 * (((int64_t)p.N + 127) / 128) * p.groups;
-  const bool many = tiles >= 512;
-  if (!wide)
-    return many ? launch<128, 128, 16, 64, 32, 1, 2>(p, e, s)
-                : launch<64, 64, 16, 32, 32, 1, 4>(p, e, s);
-  return many ? launch<128, 128, 32, 64, 32, 4, 2>(p, e, s)
-              : launch<64, 64, 32, 32, 32, 4, 4>(p, e, s);
+  if (large_tiles(p))
+    return wide ? launch<128, 128, 32, 64, 32, 4, 2>(p, e, 1, part, s)
+                : launch<128, 128, 16, 64, 32, 1, 2>(p, e, 1, part, s);
+  const int slices = slices_of(p);
+  return wide ? launch<64, 64, 32, 32, 32, 4, 4>(p, e, slices, part, s)
+              : launch<64, 64, 16, 32, 32, 1, 4>(p, e, slices, part, s);
 }
 
 }  // namespace gemmf32

@@ -198,6 +198,14 @@ void launch(const GroupedProblem& p, const Epilogue& e, const ThinPlan& pl, floa
 
 bool wgrad_thin(const GroupedProblem& p) { return p.M <= 64 || p.N <= 64; }
 
+hipError_t launch_wgrad_join(const GroupedProblem& p, const Epilogue& e, int slices,
+                             const float* part, hipStream_t s) {
+  const int64_t all = (int64_t)p.groups * p.M * p.N, wgs = (all + 255) / 256;
+  hipLaunchKernelGGL(wgrad_join_kernel, dim3((unsigned)(wgs < 4096 ? wgs : 4096)), dim3(256), 0, s,
+                     p, e, slices, part);
+  return hipGetLastError();
+}
+
 size_t wgrad_thin_floats(const GroupedProblem& p) {
   const ThinPlan pl = plan_thin(p);
   return pl.slices > 1 ? (size_t)pl.slices * p.groups * p.M * p.N : 0;
@@ -217,10 +225,7 @@ hipError_t launch_wgrad_thin(const GroupedProblem& p, const Epilogue& e, float* 
   }
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess || pl.slices == 1) return err;
-  const int64_t all = (int64_t)p.groups * p.M * p.N, wgs = (all + 255) / 256;
-  hipLaunchKernelGGL(wgrad_join_kernel, dim3((unsigned)(wgs < 4096 ? wgs : 4096)), dim3(256), 0, s,
-                     p, e, pl.slices, part);
-  return hipGetLastError();
+  return launch_wgrad_join(p, e, pl.slices, part, s);
 }
 
 }  // namespace gemmf32

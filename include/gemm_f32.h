@@ -308,7 +308,7 @@ int gemm_f32_grouped(int transB, int64_t rows, int64_t N, int64_t K,
  * written: a group without places gets beta * C_g (+0.0 when beta == 0; C is
  * not read then).  For weights stored transposed exchange A and B.  With a
  * column of ones for A (M = 1) it sums B's rows: the gradient of the biases.
- * With M or N of at most 64 and 4096 places or more it may use the stream's
+ * From 512 places on, where C has few elements for them, it uses the stream's
  * workspace of partial sums.
  *
  * Errors as gemm_f32_grouped; strideC below M rows of ldc GEMM_F32_ERR_ALIAS.

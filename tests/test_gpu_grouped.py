@@ -351,6 +351,16 @@ def test_wgrad_long_group(gpu_lib):
         wgrad_case(gpu_lib, [3000, 0, 17000], M, N, False, True, 1.0, 0.0, False, 37)
 
 
+@pytest.mark.parametrize("M,N", [(100, 140), (68, 512), (129, 67), (300, 257)])
+def test_wgrad_slices(gpu_lib, M, N):
+    """Few outputs and long groups: slices that end at, inside and before the
+    group's last K-tile, groups shorter than their slices, and none at all."""
+    for counts in ([5000, 0, 3], [2049], [0, 0, 4097, 31], [512] * 3, [640, 1, 639]):
+        wgrad_case(gpu_lib, counts, M, N, True, True, 1.0, 0.0, True, 60)
+        wgrad_case(gpu_lib, counts, M, N, False, True, 0.5, -2.0, True, 61)
+        wgrad_case(gpu_lib, counts, M, N, True, False, -1.0, 1.0, False, 62, (1, 3, 5), (1, 0, 2))
+
+
 def test_wgrad_indexes_outside_count_as_zeros(gpu_lib):
     g = gen(38)
     rows, M, N = 60, 64, 64
@@ -793,3 +803,39 @@ def test_offsets_beyond_32_bits(gpu_lib):
         one, _ = spans([1, 1])
         gpu_lib.gemm_grouped(Ad, Wd, one.cuda(), Cr, trans_b=trans)
         assert torch.equal(Cr.cpu(), torch.stack([A[0] @ Wf[0], A[1] @ Wf[1]]))
+
+
+@pytest.mark.filterwarnings("ignore:The CUDA Graph is empty")
+@pytest.mark.parametrize("M,N", [(100, 140), (16, 2048)])
+def test_sliced_wgrad_under_capture(gpu_lib, M, N):
+    """Sums of slices need the stream's workspace: refused without one, and
+    replayed with new inputs after a call has made it."""
+    offsets = spans([3000, 0, 1500])[0].cuda()
+    A, B = torch.zeros(4500, M, device="cuda"), torch.zeros(4500, N, device="cuda")
+    C = torch.empty(3, M, N, device="cuda")
+    torch.cuda.synchronize()
+    assert gpu_lib.gemm_f32_release_workspaces() == 0
+    s, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        with pytest.raises(gpu_lib.GemmError) as err:
+            gpu_lib.gemm_grouped_wgrad(A, B, offsets, C)
+    assert err.value.status == 6
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        gpu_lib.gemm_grouped_wgrad(A, B, offsets, C)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        gpu_lib.gemm_grouped_wgrad(A, B, offsets, C)
+    for seed in (63, 64, 65):
+        r = gen(seed)
+        a, b = draw(r, 4500, M, integer=True), draw(r, 4500, N, integer=True)
+        A.copy_(a)
+        B.copy_(b)
+        C.fill_(float("nan"))
+        torch.cuda.synchronize()
+        H.say(f"sliced wgrad replay M={M} N={N} seed={seed}")
+        g.replay()
+        torch.cuda.synchronize()
+        want = torch.stack([a[:3000].t() @ b[:3000], torch.zeros(M, N), a[3000:].t() @ b[3000:]])
+        assert torch.equal(C.cpu(), want)
