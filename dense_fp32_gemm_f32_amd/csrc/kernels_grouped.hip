@@ -162,6 +162,10 @@ bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 hipError_t launch_grouped(const GroupedProblem& call, const Epilogue& e, hipStream_t s) {
   GroupedProblem p = call;
   if (p.rows_a == 0) p.K = 0;   // every row of A is outside: empty sums
+  // 16-byte copies need whole chunks of both operands inside: bases, pitches
+  // and strides of 16 bytes, and the contiguous sizes multiples of 4
+  const bool wide = aligned16(p.A) && aligned16(p.B) && p.lda % 4 == 0 && p.ldb % 4 == 0 &&
+                    (p.groups == 1 || p.sb % 4 == 0) && p.K % 4 == 0 && (p.tb || p.N % 4 == 0);
   // few rows in a group, few columns, or few sums: bound by one read of B or of A,
   // or by the latency of a tile (16 groups of 32, 1024 x 1024: 27 us against 43 us
   // for the tiles; of 64: 34 against 43; of 96: 49 against 43; 64 groups of 48: 130
@@ -169,10 +173,13 @@ hipError_t launch_grouped(const GroupedProblem& call, const Epilogue& e, hipStre
   const int64_t busy = p.rows < p.groups ? p.rows : p.groups, sums = (int64_t)p.rows * p.N;
   if (p.N <= 64 || p.rows <= 32 * busy || (p.rows <= 64 * busy && sums <= 1 << 20) || sums <= 1 << 18)
     return launch_grouped_rows(p, e, s);
-  // 16-byte copies need whole chunks of both operands inside: bases, pitches
-  // and strides of 16 bytes, and the contiguous sizes multiples of 4
-  const bool wide = aligned16(p.A) && aligned16(p.B) && p.lda % 4 == 0 && p.ldb % 4 == 0 &&
-                    (p.groups == 1 || p.sb % 4 == 0) && p.K % 4 == 0 && (p.tb || p.N % 4 == 0);
+  // about as many 64 x 64 tiles as leave three CUs in eight idle, with single-float copies
+  // as one and a half rounds of them (2 groups of 512, 4096 x 512: 74 us against 86 us
+  // for the tiles; 3 of 512, 1024 x 512, half as many tiles more: 33 against 26; 3 of
+  // 500, 1501 x 1001: 69 against 90; 8 of 250, 513 x 1023, half as many more: 45
+  // against 37)
+  const int64_t tiles64 = ((int64_t)p.rows / 64 + p.groups / 2) * (((int64_t)p.N + 63) / 64);
+  if (tiles64 <= (wide ? kCus / 8 * 5 : kCus / 2 * 3)) return launch_grouped_rows(p, e, s);
   // about how many 128 x 128 tiles
   const int64_t tiles =
       ((int64_t)p.rows / 128 + p.groups / 2) * (((int64_t)p.N + 127) / 128);
