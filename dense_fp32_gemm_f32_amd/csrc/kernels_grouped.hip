@@ -139,19 +139,14 @@ hipError_t launch_mixed(const GroupedProblem& p, const Epilogue& e, hipStream_t 
   return hipGetLastError();
 }
 
-template <int BM, int BN, int BK, int WM, int WN, int V, int kMinWaves>
+template <int BM, int BN, int BK, int WM, int WN, bool kTB, int V, int kMinWaves>
 hipError_t launch_even(const GroupedProblem& p, const Epilogue& e, hipStream_t s) {
   const int64_t tiles_n = ((int64_t)p.N + BN - 1) / BN;
   const int64_t cap = most_row_tiles(p.rows, p.groups, BM);
   if (cap * tiles_n > 0x7fffffff) return hipErrorInvalidConfiguration;
-  const dim3 grid = tile_grid(cap * tiles_n), block((BM / WM) * (BN / WN) * 64);
-  if (p.tb) {
-    hipLaunchKernelGGL((grouped_even_kernel<BM, BN, BK, WM, WN, true, V, kMinWaves>), grid, block,
-                       0, s, p, e, (int)tiles_n, (unsigned)cap);
-  } else {
-    hipLaunchKernelGGL((grouped_even_kernel<BM, BN, BK, WM, WN, false, V, kMinWaves>), grid, block,
-                       0, s, p, e, (int)tiles_n, (unsigned)cap);
-  }
+  hipLaunchKernelGGL((grouped_even_kernel<BM, BN, BK, WM, WN, kTB, V, kMinWaves>),
+                     tile_grid(cap * tiles_n), dim3((BM / WM) * (BN / WN) * 64), 0, s, p, e,
+                     (int)tiles_n, (unsigned)cap);
   return hipGetLastError();
 }
 
@@ -173,30 +168,41 @@ hipError_t launch_grouped(const GroupedProblem& call, const Epilogue& e, hipStre
   const int64_t busy = p.rows < p.groups ? p.rows : p.groups, sums = (int64_t)p.rows * p.N;
   if (p.N <= 64 || p.rows <= 32 * busy || (p.rows <= 64 * busy && sums <= 1 << 20) || sums <= 1 << 18)
     return launch_grouped_rows(p, e, s);
-  // about as many 64 x 64 tiles as leave three CUs in eight idle, with single-float copies
-  // as one and a half rounds of them (2 groups of 512, 4096 x 512: 74 us against 86 us
-  // for the tiles; 3 of 512, 1024 x 512, half as many tiles more: 33 against 26; 3 of
-  // 500, 1501 x 1001: 69 against 90; 8 of 250, 513 x 1023, half as many more: 45
-  // against 37)
-  const int64_t tiles64 = ((int64_t)p.rows / 64 + p.groups / 2) * (((int64_t)p.N + 63) / 64);
-  if (tiles64 <= (wide ? kCus / 8 * 5 : kCus / 2 * 3)) return launch_grouped_rows(p, e, s);
-  // about how many 128 x 128 tiles
+  // about how many 128 x 128 and 64 x 64 tiles
   const int64_t tiles =
       ((int64_t)p.rows / 128 + p.groups / 2) * (((int64_t)p.N + 127) / 128);
+  const int64_t tiles64 = ((int64_t)p.rows / 64 + p.groups / 2) * (((int64_t)p.N + 63) / 64);
   if (wide) {
+    // tiles that leave three CUs in eight idle (2 groups of 512, 4096 x 512: 74 us
+    // against 86 us for the tiles; 3 of 512, 1024 x 512, half as many tiles more: 33
+    // against 26)
+    if (tiles64 <= kCus / 8 * 5) return launch_grouped_rows(p, e, s);
     // 64 x 64 tiles, four workgroups a CU, below a round of the CUs (21 groups of 261,
     // 1280 x 384: 71 us against 87 us in mixed tiles), where the second round would be
     // neither nearly empty nor full (8 of 512, 1024 x 1280: 111 against 123), and for
     // groups that fill few of the rows of 128 (64 of 128, 512 x 768: 78 against 86)
     const bool small = tiles < kCus || (tiles >= kCus / 4 * 5 && tiles < 2 * kCus) ||
                        p.rows <= 192 * (int64_t)p.groups;
-    return small ? launch_even<64, 64, 32, 32, 32, 4, 4>(p, e, s) : launch_mixed(p, e, s);
+    if (!small) return launch_mixed(p, e, s);
+    return p.tb ? launch_even<64, 64, 32, 32, 32, true, 4, 4>(p, e, s)
+                : launch_even<64, 64, 32, 32, 32, false, 4, 4>(p, e, s);
   }
-  // single floats: 128 x 128 tiles where they make two rounds of the CUs (8 x 1000 x
-  // 1023 x 2047: 336 us against 452 us), 64 x 64 below (16 x 200 x 511 x 1025: 88
+  // copies of single floats.  B stored N x K: below four rounds of 128 x 128 tiles the
+  // kernel for few rows, whose 16-byte loads fit any row (3 groups of 500, 1501 x 1001:
+  // 56 us against 75 us in 64 x 64 tiles; 16 of 437, 515 x 1027: 92 against 136 in tiles
+  // of 128; 4 of 3000, 1027 x 1025: 287 against 338; 2 of 4096, 2047 x 1001: 392
+  // against 335; 8 of 2048, 2049 x 2047: 1978 against 1314).
+  if (p.tb)
+    return tiles < 4 * (int64_t)kCus ? launch_grouped_rows(p, e, s)
+                                     : launch_even<128, 128, 16, 64, 32, true, 1, 2>(p, e, s);
+  // Stored K x N its runs end inside lines: only below one and a half rounds of 64 x
+  // 64 tiles (3 of 500, 1501 x 1001: 69 against 90 us; 8 of 250, 513 x 1023, half as many
+  // tiles more: 45 against 37); then those, and 128 x 128 tiles where they make two
+  // rounds (8 x 1000 x 1023 x 2047: 336 us against 452 us; 16 x 200 x 511 x 1025: 88
   // against 74 us)
-  if (tiles >= 2 * (int64_t)kCus) return launch_even<128, 128, 16, 64, 32, 1, 2>(p, e, s);
-  return launch_even<64, 64, 16, 32, 32, 1, 4>(p, e, s);
+  if (tiles64 <= kCus / 2 * 3) return launch_grouped_rows(p, e, s);
+  return tiles >= 2 * (int64_t)kCus ? launch_even<128, 128, 16, 64, 32, false, 1, 2>(p, e, s)
+                                    : launch_even<64, 64, 16, 32, 32, false, 1, 4>(p, e, s);
 }
 
 }  // namespace gemmf32

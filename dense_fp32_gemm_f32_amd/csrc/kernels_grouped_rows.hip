@@ -72,12 +72,18 @@ hipError_t launch(const GroupedProblem& p, const Epilogue& e, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Many workgroups: 64 columns each; B stored K x N in 4 waves that look one step
-// ahead, so that four workgroups share a CU (32 x 1024 x 2048 with 6 places a
-// group: 49 us against 52 us for 8 waves that look two steps ahead).
+// Many workgroups: 64 columns each, in 4 waves that look one step ahead, so that
+// four workgroups share a CU (B stored K x N, 32 x 1024 x 2048 with 6 places a group:
+// 49 us against 52 us for 8 waves that look two steps ahead; stored N x K, 64 groups
+// of 24, 1024 x 1024: 58 against 72 us for 8 waves of chunks of 64 k); with 16 places
+// and B stored N x K those 8 waves (64 groups of one, 1024 x 2048: 97 against 111 us).
 template <int RM>
 hipError_t launch_many(const GroupedProblem& p, const Epilogue& e, hipStream_t s) {
-  return p.tb ? launch<8, RM, 4, true, 4>(p, e, s) : launch<4, RM, 4, false, 1>(p, e, s);
+  if (!p.tb) return launch<4, RM, 4, false, 1>(p, e, s);
+  if constexpr (RM == 1)
+    return launch<8, 1, 4, true, 4>(p, e, s);
+  else
+    return launch<4, RM, 4, true, 1>(p, e, s);
 }
 
 // Few workgroups: 16 waves each, 32 or 16 columns.
