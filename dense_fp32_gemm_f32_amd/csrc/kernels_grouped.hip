@@ -195,12 +195,12 @@ hipError_t launch_grouped(const GroupedProblem& call, const Epilogue& e, hipStre
   if (p.tb)
     return tiles < 4 * (int64_t)kCus ? launch_grouped_rows(p, e, s)
                                      : launch_even<128, 128, 16, 64, 32, true, 1, 2>(p, e, s);
-  // Stored K x N its runs end inside lines: only below one and a half rounds of 64 x
-  // 64 tiles (3 of 500, 1501 x 1001: 69 against 90 us; 8 of 250, 513 x 1023, half as many
-  // tiles more: 45 against 37); then those, and 128 x 128 tiles where they make two
-  // rounds (8 x 1000 x 1023 x 2047: 336 us against 452 us; 16 x 200 x 511 x 1025: 88
-  // against 74 us)
-  if (tiles64 <= kCus / 2 * 3) return launch_grouped_rows(p, e, s);
+  // Stored K x N below four rounds of 64 x 64 tiles, where the last round counts for
+  // most (13 of 161, 769 x 1001: 61 against 68 us; 16 of 200, 511 x 1025: 58 against
+  // 72; 2 of 1300, 1501 x 1001: 112 against 122; 8 of 250, 513 x 1023, two whole rounds:
+  // 44 against 37; 8 of 512, 2049 x 1023, four: 235 against 214); then those, and 128 x
+  // 128 tiles where they make two rounds (8 x 1000 x 1023 x 2047: 333 us against 452)
+  if (tiles64 < 4 * (int64_t)kCus) return launch_grouped_rows(p, e, s);
   return tiles >= 2 * (int64_t)kCus ? launch_even<128, 128, 16, 64, 32, false, 1, 2>(p, e, s)
                                     : launch_even<64, 64, 16, 32, 32, false, 1, 4>(p, e, s);
 }

@@ -57,16 +57,18 @@ __global__ void __launch_bounds__(kWaves * 64)
   }
 }
 
-// kWaves waves, chunks of 16 kU k; with B stored K x N a strip's runs of whole lines
-// are read once and non-temporally (64 groups of 1024 x 1024, weights not in a
-// cache: 51 against 56 us; stored N x K a load reads half lines, which a
-// non-temporal load fetches twice: 56 against 54 us).
+// kWaves waves, chunks of 16 kU k; with B stored K x N and 16 places a strip's runs of
+// whole lines are read once and non-temporally (64 groups of 1024 x 1024, weights not
+// in a cache: 51 against 56 us; stored N x K a load reads half lines, which a
+// non-temporal load fetches twice: 56 against 54 us).  Not with 32 places, whose
+// groups may have several tiles (13 groups of 161, 769 x 1001: 61 against 70 us; 64 of
+// 24, 1024 x 1024: 66 against 69).
 template <int kWaves, int RM, int NB, bool kTB, int kU>
 hipError_t launch(const GroupedProblem& p, const Epilogue& e, hipStream_t s) {
   const int64_t strips = ((int64_t)p.N + 16 * NB - 1) / (16 * NB);
   const int64_t cap = most_row_tiles(p.rows, p.groups, 16 * RM);
   if (cap * strips > 0x7fffffff) return hipErrorInvalidConfiguration;
-  constexpr bool kOnce = !kTB && (kWaves == 4 || (kWaves == 16 && NB == 2));
+  constexpr bool kOnce = !kTB && RM == 1 && (kWaves == 4 || (kWaves == 16 && NB == 2));
   hipLaunchKernelGGL((grouped_rows_kernel<kWaves, RM, NB, kTB, kU, kOnce>), tile_grid(cap * strips),
                      dim3(kWaves * 64), 0, s, p, e, (int)strips, (unsigned)cap);
   return hipGetLastError();
