@@ -173,8 +173,8 @@ hipError_t launch_grouped(const GroupedProblem& call, const Epilogue& e, hipStre
       ((int64_t)p.rows / 128 + p.groups / 2) * (((int64_t)p.N + 127) / 128);
   const int64_t tiles64 = ((int64_t)p.rows / 64 + p.groups / 2) * (((int64_t)p.N + 63) / 64);
   if (wide) {
-    // tiles that leave three CUs in eight idle (2 groups of 512, 4096 x 512: 74 us
-    // against 86 us for the tiles; 3 of 512, 1024 x 512, half as many tiles more: 33
+    // tiles that leave three CUs in eight idle (2 groups of 512, 4096 x 512: 60 us
+    // against 86 us for the tiles; 3 of 512, 1024 x 512, half as many tiles more: 30
     // against 26)
     if (tiles64 <= kCus / 8 * 5) return launch_grouped_rows(p, e, s);
     // 64 x 64 tiles, four workgroups a CU, below a round of the CUs (21 groups of 261,

@@ -211,6 +211,27 @@ def test_grouped_larger(gpu_lib, K, N, trans):
         grouped_case(gpu_lib, counts, K, N, trans, False, True, True, False, 18)
 
 
+# 24 uneven groups, one of them empty: enough tiles that every tiled kernel takes some
+# width (even and odd, two thirds of a round over one, four rounds and more)
+MANY_TILES = [0] + [100 + (131 * i) % 400 for i in range(1, 24)]
+
+
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("K,N", [(0, 600), (4, 600), (100, 600), (36, 440), (132, 2048),
+                                 (1, 601), (17, 601), (127, 601), (3, 2047), (65, 2047)])
+def test_grouped_uneven_tiles(gpu_lib, K, N, trans):
+    grouped_case(gpu_lib, MANY_TILES, K, N, trans, True, True, True, True, 66)
+    grouped_case(gpu_lib, MANY_TILES, K, N, trans, False, False, False, False, 67)
+
+
+@pytest.mark.parametrize("pads,shifts", [((4, 8, 4), (0, 0, 0)), ((1, 3, 5), (0, 0, 0)),
+                                         ((0, 0, 0), (1, 2, 3)), ((0, 0, 3), (0, 0, 1))])
+@pytest.mark.parametrize("N", [600, 2048])
+def test_grouped_uneven_tiles_pitches(gpu_lib, N, pads, shifts):
+    for trans in (False, True):
+        grouped_case(gpu_lib, MANY_TILES, 48, N, trans, True, False, True, True, 68, pads, shifts)
+
+
 def test_grouped_shared_weight_and_bias(gpu_lib):
     """Strides of 0: one weight and one bias for every group."""
     g = gen(19)
