@@ -206,9 +206,13 @@ struct Source {
 };
 
 // The K loop of a BM x BN tile, wave tiles WM x WN, over src's K-tiles.  src may
-// copy with more waves than the tile has: those beyond only copy.
+// copy with more waves than the tile has: those beyond only copy.  kNoSpare: no
+// copies past the last K-tile, a branch around each copy instead.  (The gradient
+// of 40 weights of 513 x 257 over 7 places each, one K-tile: 20 us against 24 us; of 8
+// of 1024 x 2048 over 1024: 291 against 294; but the rows' gradient 2048 x 1024: 300
+// against 293.)
 // pool: 2 (BM + BN) BK floats of LDS, read by no wave any more.
-template <int BM, int BN, int BK, int WM, int WN, class Src>
+template <int BM, int BN, int BK, int WM, int WN, bool kNoSpare = false, class Src>
 __device__ __forceinline__ void k_loop(float* pool, Src& src, int wave, int lane,
                                        floatx16 (&acc)[WM / 32][WN / 32]) {
   using OpA = typename Src::OpA;
@@ -289,20 +293,23 @@ __device__ __forceinline__ void k_loop(float* pool, Src& src, int wave, int lane
       return;
     }
   }
-  // Branch-free steps: the copies of a K-tile past the end re-read the last
-  // one into the buffer no longer needed; the last step reads fragments it does
-  // not use.
+  // One form of step for all: the copies of a K-tile past the end (where there are
+  // any) re-read the last one into the buffer no longer needed; the last step reads
+  // fragments it does not use.
+  auto copied = [&](int t) { return !kNoSpare || t < ktiles; };
   Frag f0, f1;
   src.seek(0);
 #pragma unroll
   for (int idx = 0; idx < kTileCopies; ++idx) src.copy(lds_a0, lds_b0, idx);
-  src.seek(1);
+  if (copied(1)) src.seek(1);
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
 #pragma unroll
   for (int idx = 0; idx < kReadsPerGroup; ++idx) read_one(f0, lds_a0, lds_b0, 0, idx);
+  if (copied(1)) {
 #pragma unroll
-  for (int idx = 0; idx < kTileCopies; ++idx) src.copy(lds_a1, lds_b1, idx);
+    for (int idx = 0; idx < kTileCopies; ++idx) src.copy(lds_a1, lds_b1, idx);
+  }
 
   auto step = [&](int t, auto cur_tag) {
     constexpr int kCur = decltype(cur_tag)::value;
@@ -310,7 +317,8 @@ __device__ __forceinline__ void k_loop(float* pool, Src& src, int wave, int lane
     float* lb = kCur ? lds_b1 : lds_b0;
     float* la_next = kCur ? lds_a0 : lds_a1;
     float* lb_next = kCur ? lds_b0 : lds_b1;
-    src.seek(t + 2);
+    const bool more = copied(t + 2);
+    if (more) src.seek(t + 2);
 #pragma unroll
     for (int q = 0; q < kGroups; ++q) {
       Frag& fc = (q & 1) ? f1 : f0;
@@ -341,7 +349,7 @@ __device__ __forceinline__ void k_loop(float* pool, Src& src, int wave, int lane
               read_one(fn, la_next, lb_next, 0, i * kReadsPer + r);
 #pragma unroll
           for (int l = 0; l < kCopiesPer; ++l)
-            if (i * kCopiesPer + l < kTileCopies) src.copy(la, lb, i * kCopiesPer + l);
+            if (i * kCopiesPer + l < kTileCopies && more) src.copy(la, lb, i * kCopiesPer + l);
           __builtin_amdgcn_sched_barrier(0);
         }
       }

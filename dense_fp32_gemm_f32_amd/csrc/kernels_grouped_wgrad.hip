@@ -73,7 +73,7 @@ __global__ void __launch_bounds__((BM / WM) * (BN / WN) * 64)
   src.gb = Gather{none ? nullptr : p.ib, p.rows_b};
   src.first = begin;
   floatx16 acc[WM / 32][WN / 32];
-  k_loop<BM, BN, BK, WM, WN>(pool, src, wave, lane, acc);
+  k_loop<BM, BN, BK, WM, WN, true>(pool, src, wave, lane, acc);
   const int m0 = tm * BM + (wave % (BM / WM)) * WM, n0 = tn * BN + (wave / (BM / WM)) * WN;
   if (slices > 1) {
     float* C = part + ((int64_t)slice * p.groups + g) * p.M * p.N;
