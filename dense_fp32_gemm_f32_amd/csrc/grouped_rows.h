@@ -201,6 +201,18 @@ __device__ __forceinline__ void rows_product(float* red, const float* A, int64_t
 
   // ---- the waves' tiles ---------------------------------------------------------
   constexpr int BN = 16 * NB, BM = 16 * RM;
+  // a row that is not there: zeros times weights that are not finite were NaN
+#pragma unroll
+  for (int i = 0; i < RM; ++i) {
+    const unsigned there = (unsigned)__ballot(a_in[i]) & 0xffffu;
+    if (there != 0xffffu) {
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (!(there >> (4 * h + r) & 1)) acc[i][j][r] = 0.f;
+    }
+  }
 #pragma unroll
   for (int i = 0; i < RM; ++i)
 #pragma unroll

@@ -273,7 +273,7 @@ int gemm_f32_group_rows(int64_t n, int64_t groups, int64_t per_row,
  *
  * What no place names stays as it was: rows of C, groups without places,
  * places from offsets[groups] on.  An index outside its matrix is never
- * followed: such a row of A counts as zeros, such a row of C is not written.
+ * followed: such a row of A leaves an empty sum, such a row of C is not written.
  * Offsets are taken into [0, rows] and a group that ends before it begins is
  * empty; what offsets that fall (places of two groups) or a row of C named twice
  * leave in the rows of C concerned is not specified.  beta == 0 does not read C.
@@ -304,10 +304,11 @@ int gemm_f32_grouped(int transB, int64_t rows, int64_t N, int64_t K,
  *   C_g = alpha * sum_i A[ia(i)]^T B[ib(i)] + beta * C_g
  * with A of rowsA rows of M floats, B of rowsB rows of N, C_g = C + g *
  * strideC (M x N, pitch ldc).  Offsets and indexes as gemm_f32_grouped; a row
- * of A or B whose index is outside its matrix counts as zeros.  Every C_g is
- * written: a group without places gets beta * C_g (+0.0 when beta == 0; C is
- * not read then).  For weights stored transposed exchange A and B.  With a
- * column of ones for A (M = 1) it sums B's rows: the gradient of the biases.
+ * of A or B whose index is outside its matrix counts as zeros (opposite a row
+ * that is not finite: zeros or NaN).  Every C_g is written: a group without
+ * places gets beta * C_g (+0.0 when beta == 0; C is not read then).  For
+ * weights stored transposed exchange A and B.  With a column of ones for A
+ * (M = 1) it sums B's rows: the gradient of the biases.
  * From 512 places on, where C has few elements for them, it uses the stream's
  * workspace of partial sums.
  *

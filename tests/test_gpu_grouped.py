@@ -232,6 +232,30 @@ def test_grouped_uneven_tiles_pitches(gpu_lib, N, pads, shifts):
         grouped_case(gpu_lib, MANY_TILES, 48, N, trans, True, False, True, True, 68, pads, shifts)
 
 
+@pytest.mark.parametrize("rows,N", [(90, 64), (90, 200), (3000, 1024), (3000, 1025)])
+@pytest.mark.parametrize("trans", [False, True])
+def test_grouped_rows_outside_meet_no_weight(gpu_lib, rows, N, trans):
+    """A row of A whose index is outside gives the update of an empty sum, also
+    where the weights it would meet are not finite, in every kernel."""
+    g = gen(69)
+    K = 64
+    A, W = draw(g, rows, K, integer=True), torch.full((2, K, N), float("inf"))
+    W[1] = draw(g, K, N, integer=True)
+    b = draw(g, 2, N, integer=True)
+    half = rows // 2
+    offsets, _ = spans([half, rows - half])
+    ia = torch.arange(rows).int()
+    ia[:half] = -1
+    ia[half + 1] = rows
+    H.say(f"grouped rows outside rows={rows} N={N} trans={trans}")
+    B = W.transpose(1, 2).contiguous() if trans else W
+    got = gpu_lib.gemm_grouped(A.cuda(), B.cuda(), offsets.cuda(), trans_b=trans, bias=b.cuda(),
+                               index_a=ia.cuda()).cpu()
+    want = A @ W[1] + b[1]
+    want[:half], want[half + 1] = b[0], b[1]
+    assert torch.equal(got, want)
+
+
 def test_grouped_shared_weight_and_bias(gpu_lib):
     """Strides of 0: one weight and one bias for every group."""
     g = gen(19)
