@@ -22,7 +22,6 @@
 #include <type_traits>
 
 #include "grouped_internal.h"
-#include "lds_dma.h"
 #include "mfma_common.h"
 
 namespace gemmf32 {
@@ -34,19 +33,31 @@ using namespace mfma;
 static __device__ __attribute__((aligned(16))) const float kZeros[4] = {0.f, 0.f, 0.f, 0.f};
 
 // Lane l copies V floats from g into LDS at lds_wave + V l.  The address of
-// LDS comes from M0, saved and restored around the copy; written as inline
-// assembly so that the kernel's own waits alone order copies and reads.
+// LDS comes from M0, saved and restored around the copy, which needs one wait
+// state behind the write (s_nop); written as inline assembly so that the
+// kernel's own waits alone order copies and reads.  (load_lds16, which leaves
+// M0 to the compiler, makes the 64 x 64 tiles slower: 4096 x 1280 x 1024 in one
+// group, N x K: 94 against 99 us.)
 template <int V>
 __device__ __forceinline__ void copy_to_lds(const float* g, float* lds_wave) {
+  static_assert(V == 1 || V == 4, "copies of 4 or 16 bytes");
+  const uint32_t lds_addr = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds_wave);
+  uint32_t saved;
   if constexpr (V == 4) {
-    load_lds16(g, lds_wave);
-  } else {
-    const uint32_t lds_addr = __builtin_amdgcn_readfirstlane(
-        (uint32_t)(uintptr_t)((__attribute__((address_space(3))) float*)lds_wave));
-    uint32_t saved;
     asm volatile(
         "s_mov_b32 %0, m0\n\t"
         "s_mov_b32 m0, %2\n\t"
+        "s_nop 0\n\t"
+        "global_load_lds_dwordx4 %1, off\n\t"
+        "s_mov_b32 m0, %0"
+        : "=&s"(saved)
+        : "v"(g), "s"(lds_addr)
+        : "memory");
+  } else {
+    asm volatile(
+        "s_mov_b32 %0, m0\n\t"
+        "s_mov_b32 m0, %2\n\t"
+        "s_nop 0\n\t"
         "global_load_lds_dword %1, off\n\t"
         "s_mov_b32 m0, %0"
         : "=&s"(saved)

@@ -37,20 +37,16 @@ namespace {
 using namespace mfma;
 
 // One global_load_lds_dword: lane l copies the float at base + off_bytes into
-// LDS at lds_wave + 4 l.  The LDS address comes from M0 (saved and restored
-// around it); written as inline assembly, as the 16-byte copy is, so that the
-// kernel alone decides which waits reads of a buffer need.
+// LDS at lds_wave + 4 l.  The LDS address comes from M0 (a write of it needs one
+// wait state before the copy); written as inline assembly, as the 16-byte copy
+// is, so that the kernel alone decides which waits reads of a buffer need.
 __device__ __forceinline__ void load_lds4(uint32_t off_bytes, const void* base, float* lds_wave) {
-  const uint32_t lds_addr = __builtin_amdgcn_readfirstlane(
-      (uint32_t)(uintptr_t)((__attribute__((address_space(3))) float*)lds_wave));
-  uint32_t saved;
+  const uint32_t lds_addr = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds_wave);
   asm volatile(
-      "s_mov_b32 %0, m0\n\t"
-      "s_mov_b32 m0, %3\n\t"
-      "global_load_lds_dword %1, %2\n\t"
-      "s_mov_b32 m0, %0"
-      : "=&s"(saved)
-      : "v"(off_bytes), "s"(base), "s"(lds_addr)
+      "s_nop 0\n\t"
+      "global_load_lds_dword %0, %1"
+      :
+      : "v"(off_bytes), "s"(base), "{m0}"(lds_addr)
       : "memory");
 }
 
@@ -91,7 +87,11 @@ __device__ __forceinline__ void d4_k_loop(float* lds_a0, float* lds_b0, float* l
     return reinterpret_cast<const char*>(((uint64_t)hi << 32) | lo);
   };
   auto bases = [&](int t) {
-    return Bases{uniform(a_base + (int64_t)t * a_step), uniform(b_base + (int64_t)t * b_step)};
+    Bases bs{uniform(a_base + (int64_t)t * a_step), uniform(b_base + (int64_t)t * b_step)};
+    // a load may take its address from a scalar five wait states after a vector
+    // instruction wrote it; the compiler does not see the copies' loads
+    asm volatile("s_nop 4" : "+s"(bs.a), "+s"(bs.b));
+    return bs;
   };
   // copy idx of a tile into the LDS buffer (la, lb)
   auto dma_one = [&](float* la, float* lb, const Bases& bs, int idx) {

@@ -52,16 +52,12 @@ constexpr int kTargetWaves = 4096;   // 16 per CU
 // mfma::load_lds16 with the non-temporal hint (nt): B^T is read once, so
 // its lines need not stay in the caches.
 __device__ __forceinline__ void load_lds16_nt(const float* g, float* lds_wave) {
-  const uint32_t lds_addr = __builtin_amdgcn_readfirstlane(
-      (uint32_t)(uintptr_t)((__attribute__((address_space(3))) float*)lds_wave));
-  uint32_t saved;
+  const uint32_t lds_addr = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds_wave);
   asm volatile(
-      "s_mov_b32 %0, m0\n\t"
-      "s_mov_b32 m0, %2\n\t"
-      "global_load_lds_dwordx4 %1, off nt\n\t"
-      "s_mov_b32 m0, %0"
-      : "=&s"(saved)
-      : "v"(g), "s"(lds_addr)
+      "s_nop 0\n\t"
+      "global_load_lds_dwordx4 %0, off nt"
+      :
+      : "v"(g), "{m0}"(lds_addr)
       : "memory");
 }
 template <bool NT>
