@@ -228,6 +228,19 @@ std::mutex g_ws_mu;
 std::map<std::pair<int, uintptr_t>, Workspace>* g_ws = nullptr;   // partial sums
 std::map<std::pair<int, uintptr_t>, Workspace>* g_xs = nullptr;   // exchange slots
 
+// Host threads may call on one stream at once.  A call that takes a workspace
+// holds its stream's turn from before it looks the workspace up until the last
+// launch that uses it is enqueued: otherwise another call's partial sums could
+// be enqueued between a call's partial sums and the launch that adds them.
+// Streams share kTurns locks; no call holds two.
+constexpr int kTurns = 64;
+std::mutex g_turns[kTurns];
+
+std::unique_lock<std::mutex> take_turn(int dev, hipStream_t s) {
+  const uint64_t h = ((uint64_t)(uintptr_t)s + (uint64_t)dev) * UINT64_C(0x9E3779B97F4A7C15);
+  return std::unique_lock<std::mutex>(g_turns[h >> 58]);
+}
+
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // A buffer of at least `need` bytes from `table` for (dev, s).  clear: a new
@@ -347,6 +360,7 @@ int run_entry(const Entry& e, const Op& op, const Problem& p, int dev, hipStream
                  p.N, p.K, (long long)p.lda, (long long)p.ldb, (long long)p.ldc,
                  e.name.c_str());
   hipError_t err = hipSuccess;
+  std::unique_lock<std::mutex> turn;   // held where a workspace is used
   switch (e.kind) {
     case Kind::Mfma:
     case Kind::MfmaSplitK: {
@@ -359,6 +373,7 @@ int run_entry(const Entry& e, const Op& op, const Problem& p, int dev, hipStream
           if (need > fixed->partial_floats) return GEMM_F32_ERR_SCRATCH;
           partials = fixed->partials;
         } else {
+          turn = take_turn(dev, s);
           const int rc = get_workspace(dev, s, need, &partials);
           if (rc != GEMM_F32_OK) return rc;
         }
@@ -376,6 +391,7 @@ int run_entry(const Entry& e, const Op& op, const Problem& p, int dev, hipStream
         if (pl.partial_floats > 0) partials = fixed->partials;
         if (pl.slot_words > 0) pl.slots = fixed->slots;
       } else {
+        if (pl.partial_floats > 0 || pl.slot_words > 0) turn = take_turn(dev, s);
         if (pl.partial_floats > 0) {
           const int rc = get_workspace(dev, s, pl.partial_floats, &partials);
           if (rc != GEMM_F32_OK) return rc;
@@ -669,7 +685,9 @@ Op make_op(int transA, int transB, float alpha, float beta, const float* bias = 
 namespace gemmf32 {
 int host_check_device(int* dev) { return check_device(dev); }
 int host_check_pointer(const void* p, int dev) { return check_pointer(p, dev); }
-int host_partials(int dev, hipStream_t s, size_t floats, float** out) {
+int host_partials(int dev, hipStream_t s, size_t floats, std::unique_lock<std::mutex>* turn,
+                  float** out) {
+  *turn = take_turn(dev, s);
   return get_workspace(dev, s, floats, out);
 }
 }  // namespace gemmf32
@@ -754,9 +772,12 @@ int reduce_sum_f32(int64_t n, const float* x, float* out, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
   const gemmf32::ReducePlan pl = gemmf32::plan_reduce(n);
   unsigned long long* slots = nullptr;
-  if (pl.groups > 1 &&
-      (rc = get_exchange_slots(dev, s, (size_t)pl.groups, &slots)) != GEMM_F32_OK)
-    return rc;
+  std::unique_lock<std::mutex> turn;
+  if (pl.groups > 1) {
+    turn = take_turn(dev, s);
+    rc = get_exchange_slots(dev, s, (size_t)pl.groups, &slots);
+    if (rc != GEMM_F32_OK) return rc;
+  }
   if (gemmf32::launch_reduce_sum(n, x, out, slots, s) != hipSuccess) {
     (void)hipGetLastError();
     return GEMM_F32_ERR_LAUNCH;
@@ -860,6 +881,8 @@ const char* gemm_f32_kernel_name(int index) {
 }
 
 int gemm_f32_release_workspaces(void) {
+  std::unique_lock<std::mutex> turns[kTurns];   // no call between lookup and launch
+  for (int i = 0; i < kTurns; ++i) turns[i] = std::unique_lock<std::mutex>(g_turns[i]);
   std::lock_guard<std::mutex> lk(g_ws_mu);
   int rc = GEMM_F32_OK;
   int cur = -1;

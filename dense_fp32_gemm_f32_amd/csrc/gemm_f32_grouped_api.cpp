@@ -211,8 +211,9 @@ int gemm_f32_grouped_wgrad(int64_t rows, int64_t M, int64_t N, int64_t groups,
   e.beta = beta;
   hipStream_t s = static_cast<hipStream_t>(stream);
   float* part = nullptr;
+  std::unique_lock<std::mutex> turn;
   const size_t floats = gemmf32::grouped_wgrad_floats(p);
-  if (floats > 0) rc = gemmf32::host_partials(dev, s, floats, &part);
+  if (floats > 0) rc = gemmf32::host_partials(dev, s, floats, &turn, &part);
   return rc != GEMM_F32_OK ? rc : launched(gemmf32::launch_grouped_wgrad(p, e, part, s));
 }
 
@@ -285,7 +286,8 @@ int gemm_f32_adapters(int trans, int64_t M, int64_t N, int64_t K, int64_t R, int
   a.trans = t;
   if (gemmf32::adapters_few(a)) {
     float* part = nullptr;
-    rc = gemmf32::host_partials(dev, s, gemmf32::adapters_few_floats(a), &part);
+    std::unique_lock<std::mutex> turn;
+    rc = gemmf32::host_partials(dev, s, gemmf32::adapters_few_floats(a), &turn, &part);
     return rc != GEMM_F32_OK ? rc : launched(gemmf32::launch_adapters_few(a, part, s));
   }
   // the projection: gemm_f32_fused, or the grouped product's kernels with one group

@@ -6,6 +6,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <mutex>
 
 #include "gemm_f32_internal.h"
 
@@ -14,7 +15,10 @@ namespace gemmf32 {
 // The host checks and the per-stream partial sums that gemm_f32_api.cpp has.
 int host_check_device(int* dev);                    // gfx950 only; the current device
 int host_check_pointer(const void* p, int dev);     // memory that device can reach
-int host_partials(int dev, hipStream_t s, size_t floats, float** out);
+// turn: keeps other host threads' calls on this stream from launching until the
+// caller lets it go, behind its last launch that uses the partial sums
+int host_partials(int dev, hipStream_t s, size_t floats, std::unique_lock<std::mutex>* turn,
+                  float** out);
 
 // Place i (0 <= i < rows) belongs to group g when offsets[g] <= i < offsets[g+1].
 // Product (launch_grouped):   C[ic(i)] = act(alpha s_g A[ia(i)] op(B_g) + beta C[ic(i)] + bias_g)
