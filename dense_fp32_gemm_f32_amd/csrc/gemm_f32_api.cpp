@@ -360,7 +360,7 @@ int run_entry(const Entry& e, const Op& op, const Problem& p, int dev, hipStream
                  p.N, p.K, (long long)p.lda, (long long)p.ldb, (long long)p.ldc,
                  e.name.c_str());
   hipError_t err = hipSuccess;
-  std::unique_lock<std::mutex> turn;   // held where a workspace is used
+  std::unique_lock<std::mutex> turn;   // held where a workspace or the fixed array is used
   switch (e.kind) {
     case Kind::Mfma:
     case Kind::MfmaSplitK: {
@@ -368,12 +368,12 @@ int run_entry(const Entry& e, const Op& op, const Problem& p, int dev, hipStream
       const MfmaPlan pl = plan_mfma(v, p, e.kind == Kind::MfmaSplitK);
       float* partials = nullptr;
       if (pl.slices > 1) {
+        turn = take_turn(dev, s);
         const size_t need = (size_t)pl.slices * p.M * p.N;
         if (fixed) {
           if (need > fixed->partial_floats) return GEMM_F32_ERR_SCRATCH;
           partials = fixed->partials;
         } else {
-          turn = take_turn(dev, s);
           const int rc = get_workspace(dev, s, need, &partials);
           if (rc != GEMM_F32_OK) return rc;
         }
@@ -385,13 +385,13 @@ int run_entry(const Entry& e, const Op& op, const Problem& p, int dev, hipStream
       const auto& v = gemmf32::skinny_variant(e.sub);
       gemmf32::SkinnyPlan pl = v.plan(p, v.target_splits);
       float* partials = nullptr;
+      if (pl.partial_floats > 0 || pl.slot_words > 0) turn = take_turn(dev, s);
       if (fixed) {
         if (pl.partial_floats > fixed->partial_floats || pl.slot_words > fixed->slot_words)
           return GEMM_F32_ERR_SCRATCH;
         if (pl.partial_floats > 0) partials = fixed->partials;
         if (pl.slot_words > 0) pl.slots = fixed->slots;
       } else {
-        if (pl.partial_floats > 0 || pl.slot_words > 0) turn = take_turn(dev, s);
         if (pl.partial_floats > 0) {
           const int rc = get_workspace(dev, s, pl.partial_floats, &partials);
           if (rc != GEMM_F32_OK) return rc;

@@ -65,8 +65,8 @@ hipError_t skinny(const gemmf32::Problem&, const gemmf32::SkinnyPlan&, float* pa
                   const gemmf32::Epilogue&, hipStream_t) {
   return two_launches(part);
 }
-const gemmf32::SkinnyVariant kSkinny = {"skinny", 16, 4, 1, false, false, 0, false, false, plan,
-                                        skinny};
+const gemmf32::SkinnyVariant kSkinny = {"skinnyx_w8_c2_u2_s0_vec", 16, 4, 1, false, false, 0, false,
+                                        false, plan, skinny};
 }  // namespace
 
 namespace gemmf32 {
@@ -79,7 +79,12 @@ const SkinnyVariant& skinny_variant(int) { return kSkinny; }
 hipError_t launch_ref(const Problem&, hipStream_t) { return hipSuccess; }
 hipError_t launch_scale(const Problem&, const Epilogue&, hipStream_t) { return hipSuccess; }
 hipError_t launch_clock_probe(int, unsigned long long*, hipStream_t) { return hipSuccess; }
-int noalloc_scratch(int, hipStream_t, NoallocScratch*) { return GEMM_F32_ERR_SCRATCH; }
+int noalloc_scratch(int, hipStream_t, NoallocScratch* out) {
+  static float fixed[64];
+  out->partials = fixed;
+  out->partial_floats = 64;
+  return GEMM_F32_OK;
+}
 ReducePlan plan_reduce(int64_t) { return {}; }
 hipError_t launch_reduce_sum(int64_t, const float*, float*, unsigned long long*, hipStream_t) {
   return hipSuccess;
@@ -118,7 +123,10 @@ int wgrad(void* stream) {
                                 64, nullptr, 0.f, mem(3), 32, 1024, stream);
 }
 int few_rows(void* stream) {
-  return gemm_f32_run_kernel(0, 8, 32, 64, mem(1), 64, mem(2), 32, mem(3), 32, stream);
+  return gemm_f32(8, 32, 64, mem(1), 64, mem(2), 32, mem(3), 32, stream);
+}
+int noalloc(void* stream) {
+  return gemm_f32_noalloc(8, 32, 64, mem(1), 64, mem(2), 32, mem(3), 32, stream);
 }
 
 void run(const char* name, int (*call)(void*), void* stream) {
@@ -141,6 +149,7 @@ int main() {
     run("adapters", adapters, stream);
     run("wgrad", wgrad, stream);
     run("few_rows", few_rows, stream);
+    run("noalloc", noalloc, stream);
   }
   return gemm_f32_release_workspaces();
 }

@@ -27,7 +27,7 @@ def lines(tmp_path_factory):
     return r.stdout.splitlines()
 
 
-@pytest.mark.parametrize("name", ["adapters", "wgrad", "few_rows"])
+@pytest.mark.parametrize("name", ["adapters", "wgrad", "few_rows", "noalloc"])
 def test_calls_on_one_stream_are_not_split(lines, name):
     found = [re.fullmatch(rf"{name} calls (\d+) refused (\d+) wrong (\d+)", l) for l in lines]
     found = [tuple(map(int, m.groups())) for m in found if m]
