@@ -10,6 +10,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include <atomic>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
@@ -241,6 +242,16 @@ std::unique_lock<std::mutex> take_turn(int dev, hipStream_t s) {
   return std::unique_lock<std::mutex>(g_turns[h >> 58]);
 }
 
+// The handle under which a stream's workspaces are kept.  hipStreamPerThread is
+// one handle for another stream in every host thread: a number of the thread's
+// own then, which no handle is and no later thread gets again.
+uintptr_t stream_key(hipStream_t s) {
+  if (s != hipStreamPerThread) return (uintptr_t)s;
+  static std::atomic<uintptr_t> threads{0};
+  static thread_local const uintptr_t mine = ++threads;
+  return ~mine;
+}
+
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // A buffer of at least `need` bytes from `table` for (dev, s).  clear: a new
@@ -250,7 +261,7 @@ int grow_workspace(std::map<std::pair<int, uintptr_t>, Workspace>*& table, int d
                    hipStream_t s, size_t need, bool clear, void** out) {
   if (std::getenv("GEMM_F32_TEST_FAIL_WORKSPACE")) return GEMM_F32_ERR_WORKSPACE;
   if (!table) table = new std::map<std::pair<int, uintptr_t>, Workspace>();
-  Workspace& w = (*table)[{dev, (uintptr_t)s}];
+  Workspace& w = (*table)[{dev, stream_key(s)}];
   if (w.bytes < need) {
     // a stream being captured into a graph can neither allocate nor clear:
     // the workspace must have been grown by an earlier call on that stream

@@ -50,8 +50,9 @@
  * stream).  Work is enqueued on it and the call returns without waiting; the
  * caller synchronises.  Calls on one stream are ordered by the stream; calls
  * on different streams may run concurrently (each stream has its own
- * workspace).  Host threads may call at once, also on one stream: the launches
- * of a call that uses a workspace are enqueued together.
+ * workspace; hipStreamPerThread has one in each thread).  Host threads may call
+ * at once, also on one stream: the launches of a call that uses a workspace are
+ * enqueued together.
  *
  * Errors.  Every function returns a status; no exceptions cross the ABI and
  * there is no global error state.  Arguments are checked before anything is

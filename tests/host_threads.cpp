@@ -50,10 +50,12 @@ hipError_t hipMemsetAsync(void* p, int v, size_t n, hipStream_t) {
 // ---- the launches -------------------------------------------------------------
 namespace {
 std::atomic<int> g_calls{0}, g_wrong{0};
+thread_local float* g_part = nullptr;   // the workspace of this thread's last launch
 
 // Two launches that pass a value through the workspace.
 hipError_t two_launches(float* part) {
   const float mine = (float)++g_calls;
+  g_part = part;
   *(volatile float*)part = mine;
   std::this_thread::sleep_for(std::chrono::microseconds(200));
   if (*(volatile float*)part != mine) ++g_wrong;
@@ -142,6 +144,23 @@ void run(const char* name, int (*call)(void*), void* stream) {
   std::printf("%s calls %d refused %d wrong %d\n", name, g_calls.load(), refused.load(),
               g_wrong.load());
 }
+
+// Threads that call on hipStreamPerThread, each its own stream: the workspaces
+// in use by more than one of them.
+void run_per_thread() {
+  std::vector<std::thread> threads;
+  std::vector<float*> part(4);
+  for (int t = 0; t < 4; ++t)
+    threads.emplace_back([&part, t] {
+      for (int i = 0; i < 2; ++i)
+        if (adapters(hipStreamPerThread) == GEMM_F32_OK) part[t] = g_part;
+    });
+  for (auto& t : threads) t.join();
+  int shared = 0;
+  for (int i = 0; i < 4; ++i)
+    for (int j = 0; j < i; ++j) shared += part[i] == part[j];
+  std::printf("per_thread got %d shared %d\n", part[0] && part[1] && part[2] && part[3], shared);
+}
 }  // namespace
 
 int main() {
@@ -151,5 +170,6 @@ int main() {
     run("few_rows", few_rows, stream);
     run("noalloc", noalloc, stream);
   }
+  run_per_thread();
   return gemm_f32_release_workspaces();
 }

@@ -32,3 +32,8 @@ def test_calls_on_one_stream_are_not_split(lines, name):
     found = [re.fullmatch(rf"{name} calls (\d+) refused (\d+) wrong (\d+)", l) for l in lines]
     found = [tuple(map(int, m.groups())) for m in found if m]
     assert found == [(200, 0, 0)] * 2
+
+
+def test_each_threads_own_stream_has_its_own_workspace(lines):
+    """hipStreamPerThread is one handle for another stream in every thread."""
+    assert "per_thread got 1 shared 0" in lines
