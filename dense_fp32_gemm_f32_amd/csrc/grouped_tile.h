@@ -9,7 +9,7 @@
 //
 //   - the rows of a KC operand, or the k of an RC operand, may be gathered
 //     through an index;
-//   - k past the end, and gathered k whose index is outside the matrix, are
+//   - k past the end, and gathered k whose index is outside either matrix, are
 //     copied from a block of zeros in global memory, so K needs no padding and no
 //     value outside is ever read.  Rows that are not there read row 0 and columns
 //     past the last read column 0: they reach only sums that are not stored, or,
@@ -85,6 +85,7 @@ struct Operand {
   static_assert(!(KC && kGatherK), "gathered k needs the rows contiguous");
   static constexpr int kLds = R * BK;
   static constexpr int kCopyWaves = kWaves;
+  static constexpr bool kGathered = kGatherK;
   static constexpr int kCopies = R * BK / V / (kWaves * 64);   // copies a lane makes
   static_assert(R * BK % (V * kWaves * 64) == 0, "copies divide evenly over the threads");
   static_assert(KC || R % 64 == 0, "the [k][r] swizzle needs 64-wide rows");
@@ -145,11 +146,11 @@ struct Operand {
       }
     }
   }
-  __device__ __forceinline__ void copy(int v, float* lds, int64_t ld, int k0, int k_end, int limit,
+  // in (gathered k): this k is inside and has a row in both operands
+  __device__ __forceinline__ void copy(int v, float* lds, int64_t ld, int k0, int k_end, bool in,
                                        int wave, int lane) const {
     const float* g;
     if constexpr (kGatherK) {
-      const bool in = k_of(v, wave, lane) < k_end - k0 && (unsigned)row[v] < (unsigned)limit;
       g = in ? src[v] + (int64_t)row[v] * ld : kZeros;
     } else {
       g = src[v] + (KC ? (int64_t)k0 : (int64_t)k0 * ld);
@@ -207,11 +208,26 @@ struct Source {
     a.fetch_rows(ga, first, k0, k_end, wave, lane);
     b.fetch_rows(gb, first, k0, k_end, wave, lane);
   }
-  __device__ __forceinline__ void copy(float* la, float* lb, int idx) const {
+  // Copies of a K-tile go out in order of idx.  Both operands gathered along k: a
+  // place whose row is outside either matrix is zeros in both, so that it adds
+  // nothing, whatever stands opposite.  Copy v of either operand has the same k, so
+  // one test serves both (1023 x 2047 over 8000 places: 350 us; with each operand's
+  // copy testing both rows 368, each its own row only 355).
+  bool in[OpA::kGathered ? OpA::kCopies : 1];
+  __device__ __forceinline__ void copy(float* la, float* lb, int idx) {
+    const int v = idx < OpA::kCopies ? idx : idx - OpA::kCopies;
+    if constexpr (OpA::kGathered) {
+      static_assert(std::is_same<OpA, OpB>::value, "the operands' copies are alike");
+      if (idx < OpA::kCopies)
+        in[v] = OpA::k_of(v, wave, lane) < k_end - k0 && (unsigned)a.row[v] < (unsigned)ga.limit &&
+                (unsigned)b.row[v] < (unsigned)gb.limit;
+    }
+    bool there = true;
+    if constexpr (OpA::kGathered) there = in[v];
     if (idx < OpA::kCopies) {
-      a.copy(idx, la, lda, k0, k_end, ga.limit, wave, lane);
+      a.copy(v, la, lda, k0, k_end, there, wave, lane);
     } else {
-      b.copy(idx - OpA::kCopies, lb, ldb, k0, k_end, gb.limit, wave, lane);
+      b.copy(v, lb, ldb, k0, k_end, there, wave, lane);
     }
   }
 };

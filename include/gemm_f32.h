@@ -305,10 +305,10 @@ int gemm_f32_grouped(int transB, int64_t rows, int64_t N, int64_t K,
  * every group g, over its places i,
  *   C_g = alpha * sum_i A[ia(i)]^T B[ib(i)] + beta * C_g
  * with A of rowsA rows of M floats, B of rowsB rows of N, C_g = C + g *
- * strideC (M x N, pitch ldc).  Offsets and indexes as gemm_f32_grouped; a row
- * of A or B whose index is outside its matrix counts as zeros (opposite a row
- * that is not finite: zeros or NaN).  Every C_g is written: a group without
- * places gets beta * C_g (+0.0 when beta == 0; C is not read then).  For
+ * strideC (M x N, pitch ldc).  Offsets and indexes as gemm_f32_grouped; a place
+ * whose row of A or of B is outside its matrix adds nothing, whatever the other
+ * row holds.  Every C_g is written: a group without places gets the update of
+ * an empty sum, alpha * 0 + beta * C_g (C is not read when beta == 0).  For
  * weights stored transposed exchange A and B.  With a column of ones for A
  * (M = 1) it sums B's rows: the gradient of the biases.
  * From 512 places on, where C has few elements for them, it uses the stream's
