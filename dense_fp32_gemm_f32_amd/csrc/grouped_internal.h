@@ -51,7 +51,6 @@ hipError_t launch_grouped_wgrad(const GroupedProblem& p, const Epilogue& e, floa
 size_t grouped_wgrad_floats(const GroupedProblem& p);
 // the same for M or N of at most 64 (kernels_grouped_wgrad_thin.hip), and the
 // launch that adds the slices' sums in part, slices x groups x M x N
-bool wgrad_thin(const GroupedProblem& p);
 size_t wgrad_thin_floats(const GroupedProblem& p);
 hipError_t launch_wgrad_thin(const GroupedProblem& p, const Epilogue& e, float* part,
                              hipStream_t s);

@@ -4,6 +4,7 @@
 // The group sizes are known on the device only, so the grid covers the most row
 // tiles that the places can need; each workgroup finds its tile from the
 // offsets (a scan of 64 groups in a wave) and ends at once if there is none.
+#include "grouped_routes.h"
 #include "grouped_tile.h"
 
 namespace gemmf32 {
@@ -150,59 +151,26 @@ hipError_t launch_even(const GroupedProblem& p, const Epilogue& e, hipStream_t s
   return hipGetLastError();
 }
 
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-
 }  // namespace
 
 hipError_t launch_grouped(const GroupedProblem& call, const Epilogue& e, hipStream_t s) {
   GroupedProblem p = call;
   if (p.rows_a == 0) p.K = 0;   // every row of A is outside: empty sums
-  // 16-byte copies need whole chunks of both operands inside: bases, pitches
-  // and strides of 16 bytes, and the contiguous sizes multiples of 4
-  const bool wide = aligned16(p.A) && aligned16(p.B) && p.lda % 4 == 0 && p.ldb % 4 == 0 &&
-                    (p.groups == 1 || p.sb % 4 == 0) && p.K % 4 == 0 && (p.tb || p.N % 4 == 0);
-  // few rows in a group, few columns, or few sums: bound by one read of B or of A,
-  // or by the latency of a tile (16 groups of 32, 1024 x 1024: 27 us against 43 us
-  // for the tiles; of 64: 34 against 43; of 96: 49 against 43; 64 groups of 48: 130
-  // against 77)
-  const int64_t busy = p.rows < p.groups ? p.rows : p.groups, sums = (int64_t)p.rows * p.N;
-  if (p.N <= 64 || p.rows <= 32 * busy || (p.rows <= 64 * busy && sums <= 1 << 20) || sums <= 1 << 18)
-    return launch_grouped_rows(p, e, s);
-  // about how many 128 x 128 and 64 x 64 tiles
-  const int64_t tiles =
-      ((int64_t)p.rows / 128 + p.groups / 2) * (((int64_t)p.N + 127) / 128);
-  const int64_t tiles64 = ((int64_t)p.rows / 64 + p.groups / 2) * (((int64_t)p.N + 63) / 64);
-  if (wide) {
-    // tiles that leave three CUs in eight idle (2 groups of 512, 4096 x 512: 60 us
-    // against 86 us for the tiles; 3 of 512, 1024 x 512, half as many tiles more: 30
-    // against 26)
-    if (tiles64 <= kCus / 8 * 5) return launch_grouped_rows(p, e, s);
-    // 64 x 64 tiles, four workgroups a CU, below a round of the CUs (21 groups of 261,
-    // 1280 x 384: 71 us against 87 us in mixed tiles), where the second round would be
-    // neither nearly empty nor full (8 of 512, 1024 x 1280: 111 against 123), and for
-    // groups that fill few of the rows of 128 (64 of 128, 512 x 768: 78 against 86)
-    const bool small = tiles < kCus || (tiles >= kCus / 4 * 5 && tiles < 2 * kCus) ||
-                       p.rows <= 192 * (int64_t)p.groups;
-    if (!small) return launch_mixed(p, e, s);
-    return p.tb ? launch_even<64, 64, 32, 32, 32, true, 4, 4>(p, e, s)
-                : launch_even<64, 64, 32, 32, 32, false, 4, 4>(p, e, s);
+  switch (product_kernel(p)) {
+    case ProductKernel::Rows:
+      return launch_grouped_rows(p, e, s);
+    case ProductKernel::Mixed:
+      return launch_mixed(p, e, s);
+    case ProductKernel::Even64:
+      return p.tb ? launch_even<64, 64, 32, 32, 32, true, 4, 4>(p, e, s)
+                  : launch_even<64, 64, 32, 32, 32, false, 4, 4>(p, e, s);
+    case ProductKernel::Even64Single:   // stored K x N only
+      return launch_even<64, 64, 16, 32, 32, false, 1, 4>(p, e, s);
+    case ProductKernel::Even128Single:
+      return p.tb ? launch_even<128, 128, 16, 64, 32, true, 1, 2>(p, e, s)
+                  : launch_even<128, 128, 16, 64, 32, false, 1, 2>(p, e, s);
   }
-  // copies of single floats.  B stored N x K: below four rounds of 128 x 128 tiles the
-  // kernel for few rows, whose 16-byte loads fit any row (3 groups of 500, 1501 x 1001:
-  // 56 us against 75 us in 64 x 64 tiles; 16 of 437, 515 x 1027: 92 against 136 in tiles
-  // of 128; 4 of 3000, 1027 x 1025: 287 against 338; 2 of 4096, 2047 x 1001: 392
-  // against 335; 8 of 2048, 2049 x 2047: 1978 against 1314).
-  if (p.tb)
-    return tiles < 4 * (int64_t)kCus ? launch_grouped_rows(p, e, s)
-                                     : launch_even<128, 128, 16, 64, 32, true, 1, 2>(p, e, s);
-  // Stored K x N below four rounds of 64 x 64 tiles, where the last round counts for
-  // most (13 of 161, 769 x 1001: 61 against 68 us; 16 of 200, 511 x 1025: 58 against
-  // 72; 2 of 1300, 1501 x 1001: 112 against 122; 8 of 250, 513 x 1023, two whole rounds:
-  // 44 against 37; 8 of 512, 2049 x 1023, four: 235 against 214); then those, and 128 x
-  // 128 tiles where they make two rounds (8 x 1000 x 1023 x 2047: 333 us against 452)
-  if (tiles64 < 4 * (int64_t)kCus) return launch_grouped_rows(p, e, s);
-  return tiles >= 2 * (int64_t)kCus ? launch_even<128, 128, 16, 64, 32, false, 1, 2>(p, e, s)
-                                    : launch_even<64, 64, 16, 32, 32, false, 1, 4>(p, e, s);
+  return hipErrorInvalidValue;
 }
 
 }  // namespace gemmf32

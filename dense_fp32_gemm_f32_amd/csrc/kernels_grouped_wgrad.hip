@@ -4,8 +4,7 @@
 // Both operands have their rows contiguous and are gathered along k (the
 // places), so a K-tile's matrix rows are fetched one K-tile ahead of its copies.
 // Where C has few tiles, long groups are cut into slices of their places.
-#include <algorithm>
-
+#include "grouped_routes.h"
 #include "grouped_tile.h"
 
 namespace gemmf32 {
@@ -103,51 +102,23 @@ hipError_t launch(const GroupedProblem& p, const Epilogue& e, int slices, float*
   return err != hipSuccess || slices == 1 ? err : launch_wgrad_join(p, e, slices, part, s);
 }
 
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-
-int64_t tiles_of(const GroupedProblem& p, int side) {
-  return ((int64_t)p.M + side - 1) / side * (((int64_t)p.N + side - 1) / side) * p.groups;
-}
-
-// 128 x 128 tiles, two a CU, where they make two rounds or more (16 groups of
-// 512, 1024 x 1024: 148 us against 168 us for 64 x 64; 1024 x 2048 in 8 uneven
-// groups of 8192 places in all: 289 against 328 us; 1023 x 2047 with single-float
-// copies, 8000 places: 362 against 459 us); below that a tile of a long group
-// would run alone (3000 + 1000, 1024 x 1024: 219 against 108 us)
-bool large_tiles(const GroupedProblem& p) { return tiles_of(p, 128) >= 512; }
-
-// Below that up to four workgroups of 64 x 64 a CU, by slices of 256 places or more
-// in groups of average size and of 2048 in a group that has nearly all, whose sums
-// go through the workspace and a second launch (2 groups of 2048, 256 x 256: 16 us
-// against 54 us in one slice; 1 of 4096, 768 x 768: 59 against 129; 2 of 2000, 511 x
-// 300, single floats: 40 against 120; 2 of 4096, 1024 x 512: 89 against 132; 8 of 256,
-// 256 x 256, stays in one slice: 11 against 13 for 2).
-int slices_of(const GroupedProblem& p) {
-  if (large_tiles(p)) return 1;
-  const int64_t s = std::min(1024 / tiles_of(p, 64),
-                             std::max(p.rows / (256 * (int64_t)p.groups), (int64_t)p.rows / 2048));
-  return (int)std::max((int64_t)1, s);
-}
-
 }  // namespace
 
 size_t grouped_wgrad_floats(const GroupedProblem& p) {
   if (wgrad_thin(p)) return wgrad_thin_floats(p);
-  const int slices = slices_of(p);
+  const int slices = gradient_tiles(p).slices;
   return slices > 1 ? (size_t)slices * p.groups * p.M * p.N : 0;
 }
 
 hipError_t launch_grouped_wgrad(const GroupedProblem& p, const Epilogue& e, float* part,
                                 hipStream_t s) {
   if (wgrad_thin(p)) return launch_wgrad_thin(p, e, part, s);
-  const bool wide = aligned16(p.A) && aligned16(p.B) && p.lda % 4 == 0 && p.ldb % 4 == 0 &&
-                    p.M % 4 == 0 && p.N % 4 == 0;
-  if (large_tiles(p))
-    return wide ? launch<128, 128, 32, 64, 32, 4, 2>(p, e, 1, part, s)
-                : launch<128, 128, 16, 64, 32, 1, 2>(p, e, 1, part, s);
-  const int slices = slices_of(p);
-  return wide ? launch<64, 64, 32, 32, 32, 4, 4>(p, e, slices, part, s)
-              : launch<64, 64, 16, 32, 32, 1, 4>(p, e, slices, part, s);
+  const GradientTiles t = gradient_tiles(p);
+  if (t.large)
+    return t.wide ? launch<128, 128, 32, 64, 32, 4, 2>(p, e, 1, part, s)
+                  : launch<128, 128, 16, 64, 32, 1, 2>(p, e, 1, part, s);
+  return t.wide ? launch<64, 64, 32, 32, 32, 4, 4>(p, e, t.slices, part, s)
+                : launch<64, 64, 16, 32, 32, 1, 4>(p, e, t.slices, part, s);
 }
 
 }  // namespace gemmf32

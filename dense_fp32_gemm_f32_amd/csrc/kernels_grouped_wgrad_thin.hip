@@ -196,8 +196,6 @@ void launch(const GroupedProblem& p, const Epilogue& e, const ThinPlan& pl, floa
 
 }  // namespace
 
-bool wgrad_thin(const GroupedProblem& p) { return p.M <= 64 || p.N <= 64; }
-
 hipError_t launch_wgrad_join(const GroupedProblem& p, const Epilogue& e, int slices,
                              const float* part, hipStream_t s) {
   const int64_t all = (int64_t)p.groups * p.M * p.N, wgs = (all + 255) / 256;
