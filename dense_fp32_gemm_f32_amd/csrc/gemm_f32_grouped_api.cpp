@@ -2,14 +2,17 @@
 // belong to different weights, the gradient of those weights, and low-rank
 // adapters beside a shared projection.  Argument checks here, in the order of
 // the other entry points (sizes, pitches, NULL pointers, alignment, aliasing,
-// the device, reachability), then one launch each; the adapters are the shared
-// projection through gemm_f32_fused and two grouped products.
+// the device, reachability), then the launches: one for the rows' order and the
+// products, one or two (slices and their sum) for the gradient, two for adapters
+// of few rows, else three (the projection, H as a grouped product, the pass that
+// adds H op(U) to Y).
 #include "../../include/gemm_f32.h"
 
 #include <hip/hip_runtime.h>
 
 #include "gemm_f32_internal.h"
 #include "grouped_internal.h"
+#include "grouped_routes.h"
 
 using gemmf32::AdapterProblem;
 using gemmf32::Epilogue;
@@ -74,12 +77,6 @@ int launched(hipError_t e) {
   if (e == hipSuccess) return GEMM_F32_OK;
   (void)hipGetLastError();
   return GEMM_F32_ERR_LAUNCH;
-}
-
-// 16-byte copies fit both operands of X op(W).
-bool wide(const float* X, int64_t ldx, const float* W, int64_t ldw, int64_t N, int64_t K, bool t) {
-  return (((uintptr_t)X | (uintptr_t)W) & 15u) == 0 && ldx % 4 == 0 && ldw % 4 == 0 && K % 4 == 0 &&
-         (t || N % 4 == 0);
 }
 
 template <class T>
@@ -290,25 +287,19 @@ int gemm_f32_adapters(int trans, int64_t M, int64_t N, int64_t K, int64_t R, int
     rc = gemmf32::host_partials(dev, s, gemmf32::adapters_few_floats(a), &turn, &part);
     return rc != GEMM_F32_OK ? rc : launched(gemmf32::launch_adapters_few(a, part, s));
   }
-  // the projection: gemm_f32_fused, or the grouped product's kernels with one group
-  // where they are faster: 192 to 255 tiles of 128 x 128 (2048 x 1536 x 1024: 59 us
-  // against 67; 3000 x 1024 x 2048: 111 against 127), and few rows with W stored
-  // transposed (100 x 2048 x 2048: 19 against 37 us)
-  const int64_t tiles = (M + 127) / 128 * ((N + 127) / 128);
-  if ((tiles >= 192 && tiles < 256 && wide(X, ldx, W, ldw, N, K, t)) ||
-      (t && M <= 128 && M * N <= 1 << 18)) {
-    GroupedProblem b;
-    b.A = X;
-    b.lda = ldx;
-    b.rows_a = b.rows_c = b.rows = (int)M;
-    b.B = W;
-    b.ldb = ldw;
-    b.C = Y;
-    b.ldc = ldy;
-    b.groups = 1;
-    b.N = (int)N;
-    b.K = (int)K;
-    b.tb = t;
+  GroupedProblem b;   // the projection, all rows in one group
+  b.A = X;
+  b.lda = ldx;
+  b.rows_a = b.rows_c = b.rows = (int)M;
+  b.B = W;
+  b.ldb = ldw;
+  b.C = Y;
+  b.ldc = ldy;
+  b.groups = 1;
+  b.N = (int)N;
+  b.K = (int)K;
+  b.tb = t;
+  if (gemmf32::projection_grouped(b)) {
     Epilogue e;
     e.bias = bias;
     rc = launched(gemmf32::launch_grouped(b, e, s));

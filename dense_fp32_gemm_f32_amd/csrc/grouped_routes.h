@@ -67,6 +67,23 @@ inline ProductKernel product_kernel(const GroupedProblem& p) {
   return tiles >= 2 * kRound ? ProductKernel::Even128Single : ProductKernel::Even64Single;
 }
 
+// ---- the adapters' shared projection, M x N over K, where its rows are not few --------
+// By the grouped product's kernels with one group, else by gemm_f32_fused:
+//   - from 192 tiles of 128 x 128 on, where gemm_f32_fused takes those tiles, while the
+//     64 x 64 tiles still make three rounds of the CUs or fewer (2048 x 1536 x 1024, three
+//     rounds: 59 us against 70; 3000 x 1024 x 2048: 111 against 130; 1792 x 2048 x 1024,
+//     four: 76 against 70);
+//   - few rows with W stored transposed (100 x 2048 x 2048: 19 us against 37; 128 x
+//     1024 x 4096: 25 against 69; 65 x 4096 x 1024, past the limit: 21 against 21).
+inline bool projection_grouped(const GroupedProblem& p) {
+  const int64_t M = p.rows, N = p.N;
+  const bool wide = on_16_bytes(p.A) && on_16_bytes(p.B) && p.lda % 4 == 0 && p.ldb % 4 == 0 &&
+                    p.K % 4 == 0 && (p.tb || p.N % 4 == 0);
+  auto tiles_of = [&](int64_t side) { return (M + side - 1) / side * ((N + side - 1) / side); };
+  return (wide && tiles_of(128) >= 192 && tiles_of(64) <= 3 * 256) ||
+         (p.tb && M <= 128 && M * N <= 1 << 18);
+}
+
 // ---- C_g = alpha sum_i A[ia(i)]^T B[ib(i)] + beta C_g -------------------------------
 // M or N of at most 64: the kernel that reads the wide operand once
 // (kernels_grouped_wgrad_thin.hip, which plans its own slices)

@@ -1,6 +1,7 @@
 // Prints the kernel that each call read from the input takes, one a line:
 //   product  <N x K> <rows> <N> <K> <groups> <lda> <ldb> <strideB>
 //   gradient <rows> <M> <N> <groups> <lda> <ldb>
+//   projection <N x K> <M> <N> <K> <lda> <ldb>
 // with operands on 16 bytes.
 #include <iostream>
 #include <string>
@@ -17,6 +18,10 @@ int main() {
     if (kind == "product") {
       std::cin >> p.tb >> p.rows >> p.N >> p.K >> p.groups >> p.lda >> p.ldb >> p.sb;
       std::cout << kProduct[(int)product_kernel(p)] << "\n";
+    } else if (kind == "projection") {
+      p.groups = 1;
+      std::cin >> p.tb >> p.rows >> p.N >> p.K >> p.lda >> p.ldb;
+      std::cout << (projection_grouped(p) ? "grouped" : "fused") << "\n";
     } else {
       std::cin >> p.rows >> p.M >> p.N >> p.groups >> p.lda >> p.ldb;
       const GradientTiles t = gradient_tiles(p);

@@ -52,3 +52,26 @@ def test_every_kernel_has_a_case():
     assert {k for k in tiles.GRADIENT if "thin" not in k} == {
         "64, 4 floats", "64, 1 float", "64, 4 floats, slices", "64, 1 float, slices",
         "128, 4 floats", "128, 1 float"}
+
+
+@pytest.mark.parametrize("trans", [0, 1])
+@pytest.mark.parametrize("M,N,want", [
+    (1408, 2048, "fused"),     # 176 tiles of 128 x 128: gemm_f32_fused takes smaller ones
+    (2048, 1536, "grouped"), (3000, 1024, "grouped"), (1600, 1856, "grouped"),
+    # four rounds of 64 x 64 tiles: one round of 128 x 128 is faster
+    (1664, 2048, "fused"), (1792, 2048, "fused"), (4096, 896, "fused"), (1920, 2048, "fused"),
+    (2040, 2040, "fused"), (2304, 2048, "fused")])
+def test_projection_of_adapters_by_rounds(routes, trans, M, N, want):
+    for K in (512, 1024, 2048):
+        assert routes("projection", trans, M, N, K, K, K if trans else N) == want
+    # sizes or pitches that 16 bytes do not fit
+    assert routes("projection", trans, M, N, 1023, 1023, 1023 if trans else N) == "fused"
+    assert routes("projection", trans, M, N, 1024, 1025, 1024 if trans else N) == "fused"
+
+
+@pytest.mark.parametrize("trans,M,N,want", [
+    (1, 100, 2048, "grouped"), (1, 128, 2048, "grouped"), (1, 129, 2048, "fused"),
+    (1, 65, 4096, "fused"), (0, 100, 2048, "fused")])
+def test_projection_of_adapters_few_rows(routes, trans, M, N, want):
+    for K in (512, 2048, 2049):
+        assert routes("projection", trans, M, N, K, K, K if trans else N) == want
