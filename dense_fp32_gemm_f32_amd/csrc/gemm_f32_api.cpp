@@ -233,7 +233,8 @@ std::map<std::pair<int, uintptr_t>, Workspace>* g_xs = nullptr;   // exchange sl
 // holds its stream's turn from before it looks the workspace up until the last
 // launch that uses it is enqueued: otherwise another call's partial sums could
 // be enqueued between a call's partial sums and the launch that adds them.
-// Streams share kTurns locks; no call holds two.
+// Streams share kTurns locks; no call holds two.  The fixed array has one turn for
+// each device, as one stream may have two handles (NULL and hipStreamLegacy).
 constexpr int kTurns = 64;
 std::mutex g_turns[kTurns];
 
@@ -379,7 +380,7 @@ int run_entry(const Entry& e, const Op& op, const Problem& p, int dev, hipStream
       const MfmaPlan pl = plan_mfma(v, p, e.kind == Kind::MfmaSplitK);
       float* partials = nullptr;
       if (pl.slices > 1) {
-        turn = take_turn(dev, s);
+        turn = take_turn(dev, fixed ? nullptr : s);
         const size_t need = (size_t)pl.slices * p.M * p.N;
         if (fixed) {
           if (need > fixed->partial_floats) return GEMM_F32_ERR_SCRATCH;
@@ -396,7 +397,7 @@ int run_entry(const Entry& e, const Op& op, const Problem& p, int dev, hipStream
       const auto& v = gemmf32::skinny_variant(e.sub);
       gemmf32::SkinnyPlan pl = v.plan(p, v.target_splits);
       float* partials = nullptr;
-      if (pl.partial_floats > 0 || pl.slot_words > 0) turn = take_turn(dev, s);
+      if (pl.partial_floats > 0 || pl.slot_words > 0) turn = take_turn(dev, fixed ? nullptr : s);
       if (fixed) {
         if (pl.partial_floats > fixed->partial_floats || pl.slot_words > fixed->slot_words)
           return GEMM_F32_ERR_SCRATCH;

@@ -145,6 +145,13 @@ void run(const char* name, int (*call)(void*), void* stream) {
               g_wrong.load());
 }
 
+// Calls on the two handles of the legacy default stream in turn.
+int both_handles(void* stream) {
+  static std::atomic<int> n{0};
+  (void)stream;
+  return noalloc(++n % 2 ? nullptr : (void*)hipStreamLegacy);
+}
+
 // Threads that call on hipStreamPerThread, each its own stream: the workspaces
 // in use by more than one of them.
 void run_per_thread() {
@@ -170,6 +177,7 @@ int main() {
     run("few_rows", few_rows, stream);
     run("noalloc", noalloc, stream);
   }
+  run("both_handles", both_handles, nullptr);
   run_per_thread();
   return gemm_f32_release_workspaces();
 }

@@ -34,6 +34,10 @@ def test_calls_on_one_stream_are_not_split(lines, name):
     assert found == [(200, 0, 0)] * 2
 
 
+def test_two_handles_of_one_stream_share_the_fixed_array_in_turn(lines):
+    assert "both_handles calls 200 refused 0 wrong 0" in lines
+
+
 def test_each_threads_own_stream_has_its_own_workspace(lines):
     """hipStreamPerThread is one handle for another stream in every thread."""
     assert "per_thread got 1 shared 0" in lines
