@@ -56,13 +56,17 @@ inline ProductKernel product_kernel(const GroupedProblem& p) {
   // kernel for few rows, whose 16-byte loads fit any row (3 groups of 500, 1501 x 1001:
   // 56 us against 75 us in 64 x 64 tiles; 16 of 437, 515 x 1027: 92 against 136 in tiles
   // of 128; 4 of 3000, 1027 x 1025: 287 against 338; 2 of 4096, 2047 x 1001: 392
-  // against 335; 8 of 2048, 2049 x 2047: 1978 against 1314).
+  // against 335; 8 of 2048, 2049 x 2047: 1978 against 1314).  Some shapes below lose up
+  // to a quarter; over 215 shapes of 2 to 24 groups the rule is 2 % above the faster
+  // of the two on average, and rules by the fill of the last round are no nearer.
   if (p.tb) return tiles < 4 * kRound ? ProductKernel::Rows : ProductKernel::Even128Single;
   // Stored K x N below four rounds of 64 x 64 tiles, where the last round counts for
   // most (13 of 161, 769 x 1001: 61 against 68 us; 16 of 200, 511 x 1025: 58 against
   // 72; 2 of 1300, 1501 x 1001: 112 against 122; 8 of 250, 513 x 1023, two whole rounds:
   // 44 against 37; 8 of 512, 2049 x 1023, four: 235 against 214); then those, and 128 x
-  // 128 tiles where they make two rounds (8 x 1000 x 1023 x 2047: 333 us against 452)
+  // 128 tiles where they make two rounds (8 x 1000 x 1023 x 2047: 333 us against 452).
+  // Over the same 215 shapes 5 % above the fastest of the three on average, by the
+  // fill of the last round 5 to 7 %.
   if (tiles64 < 4 * kRound) return ProductKernel::Rows;
   return tiles >= 2 * kRound ? ProductKernel::Even128Single : ProductKernel::Even64Single;
 }

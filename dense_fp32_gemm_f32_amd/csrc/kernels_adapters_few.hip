@@ -12,7 +12,7 @@
 //      element; the first column blocks write H.
 //
 // The slices are added in order, so repeats give the same bits.  (32 rows, 2048 x
-// 2048, rank 16, 8 adapters: 11 + 5 us, against 52 us for the projection by
+// 2048, rank 16, 8 adapters: 10.5 + 6 us, against 52 us for the projection by
 // gemm_f32_fused, whose 32 tiles leave most CUs idle, and two grouped products.)
 #include "grouped_rows.h"
 

@@ -63,6 +63,8 @@ def kernel_sources(kernel: str | None = None) -> list[str]:
         files += ["kernels_skinny.hip"]
     elif kernel.startswith("reduce_"):
         files += ["kernels_reduce.hip"]
+    elif kernel == "grouped":   # the grouped products and adapters, all together
+        files += ["mfma_common.h", *(f for f in every if "group" in f or "adapters" in f)]
     else:
         return every
     return sorted(files)
