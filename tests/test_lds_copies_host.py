@@ -45,8 +45,8 @@ OBJDUMP = Path("/opt/rocm/llvm/bin/llvm-objdump")
 
 def unwaited(listing):
     """Loads into LDS of a disassembly that come too soon behind the scalar they
-    use: one wait state behind a write of M0, five behind a vector instruction's
-    write of a scalar of their address."""
+    use: one wait state behind a scalar write of M0, five behind a vector
+    instruction's write of M0 or of a scalar of their address."""
     found, past = [], []
     for line in listing.splitlines():
         code = line.split("//")[0].strip()
@@ -59,9 +59,10 @@ def unwaited(listing):
             for before in reversed(past):
                 if states < 1 and re.match(r"s_\w+ m0,", before):
                     found.append((before, code))
-                written = re.match(r"v_read(?:first)?lane_b32 s(\d+),", before)
-                if (states < 5 and pair and written
-                        and int(pair[1]) <= int(written[1]) <= int(pair[2])):
+                written = re.match(r"v_read(?:first)?lane_b32 (?:s(\d+)|m0),", before)
+                if states < 5 and written and (
+                        written[1] is None
+                        or (pair and int(pair[1]) <= int(written[1]) <= int(pair[2]))):
                     found.append((before, code))
                 nop = re.match(r"s_nop (\d+)", before)
                 states += int(nop[1]) + 1 if nop else 1
@@ -75,6 +76,7 @@ def unwaited(listing):
     ("v_readfirstlane_b32 s1, v0\ns_nop 3\nglobal_load_lds_dword v0, s[0:1]", 1),
     ("v_readfirstlane_b32 s1, v0\ns_nop 4\nglobal_load_lds_dword v0, s[0:1]", 0),
     ("v_readlane_b32 s2, v0, 3\nglobal_load_lds_dword v0, s[0:1]", 0),
+    ("v_readfirstlane_b32 m0, v0\ns_nop 0\nglobal_load_lds_dword v0, s[0:1]", 1),
 ])
 def test_the_disassembly_check_counts_wait_states(text, found):
     assert len(unwaited(text)) == found
