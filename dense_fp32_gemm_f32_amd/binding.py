@@ -31,6 +31,9 @@ STATUS_NAMES = {
     9: "GEMM_F32_ERR_POINTER", 10: "GEMM_F32_ERR_INVALID_ARG", 11: "GEMM_F32_ERR_SCRATCH",
 }
 ACT_NONE, ACT_RELU = 0, 1
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+Q4_INT, Q4_E2M1 = 0, 1
+SCALE_F32, SCALE_F16, SCALE_BF16, SCALE_E8M0 = 0, 1, 2, 3
 EXPORTS = ["gemm_f32", "gemm_f32_ex", "gemm_f32_ref_gpu", "gemm_f32_status_string",
            "gemm_f32_selected_kernel", "gemm_f32_selected_kernel_ex", "gemm_f32_version",
            "gemm_f32_kernel_count", "gemm_f32_kernel_name", "gemm_f32_run_kernel",
@@ -38,8 +41,11 @@ EXPORTS = ["gemm_f32", "gemm_f32_ex", "gemm_f32_ref_gpu", "gemm_f32_status_strin
            "gemm_f32_selected_kernel_batched", "reduce_sum_f32", "gemm_f32_fused",
            "gemm_f32_run_kernel_fused", "gemm_f32_noalloc", "gemm_f32_clock_probe",
            "gemm_f32_group_rows", "gemm_f32_grouped", "gemm_f32_grouped_wgrad",
-           "gemm_f32_adapters"]
+           "gemm_f32_adapters", "gemm_f32_route", "gemm_f32_route_grad", "gemm_f32_join_rows",
+           "gemm_f32_join_rows_grad", "gemm_f32_q4", "gemm_f32_q4_grouped", "gemm_f32_norm",
+           "gemm_f32_clip"]
 MAX_GROUPS = 1024
+MAX_TOP = 64
 CLOCK_PROBE_WORKGROUPS = 1024
 
 
@@ -124,6 +130,27 @@ def load(lib_path=None):
                                       vp, i64, vp, i64, i64, vp, i64, i64, vp, vp, i64, vp, i64,
                                       vp]
     lib.gemm_f32_adapters.restype = ci
+    lib.gemm_f32_route.argtypes = [i64, i64, i64, vp, i64, vp, ci, i64, i64, ci, ci, f32, vp, vp,
+                                   vp]
+    lib.gemm_f32_route.restype = ci
+    lib.gemm_f32_route_grad.argtypes = [i64, i64, i64, vp, i64, ci, ci, f32, vp, vp, vp, i64, vp]
+    lib.gemm_f32_route_grad.restype = ci
+    lib.gemm_f32_join_rows.argtypes = [i64, i64, i64, vp, i64, vp, vp, i64, f32, vp, i64, vp]
+    lib.gemm_f32_join_rows.restype = ci
+    lib.gemm_f32_join_rows_grad.argtypes = [i64, i64, i64, vp, i64, vp, i64, vp, vp, i64, vp, i64,
+                                            vp, vp]
+    lib.gemm_f32_join_rows_grad.restype = ci
+    lib.gemm_f32_q4.argtypes = [i64, i64, i64, f32, vp, i64, ci, i64, vp, i64, ci, vp, i64, vp,
+                                i64, f32, vp, i64, vp, ci, vp]
+    lib.gemm_f32_q4.restype = ci
+    lib.gemm_f32_q4_grouped.argtypes = [i64, i64, i64, i64, vp, f32, vp, i64, i64, vp, ci, i64, vp,
+                                        i64, i64, ci, vp, i64, i64, vp, i64, i64, f32, vp, i64,
+                                        i64, vp, vp, i64, ci, vp]
+    lib.gemm_f32_q4_grouped.restype = ci
+    lib.gemm_f32_norm.argtypes = [i64, vp, vp, vp, vp]
+    lib.gemm_f32_norm.restype = ci
+    lib.gemm_f32_clip.argtypes = [i64, vp, vp, vp, f32, vp, vp]
+    lib.gemm_f32_clip.restype = ci
     _lib = lib
     return lib
 
@@ -211,6 +238,53 @@ def gemm_f32_adapters(trans, M, N, K, R, groups, places, offsets, order, scale, 
     return load().gemm_f32_adapters(trans, M, N, K, R, groups, places, offsets, order, scale, X,
                                     ldx, W, ldw, D, ldd, strideD, U, ldu, strideU, bias, H, ldh,
                                     Y, ldy, stream)
+
+
+def gemm_f32_route(tokens, experts, top, logits, ldl, bias, score, groups, group_top, group_best,
+                   renorm, scale, choice, weight, stream=0) -> int:
+    return load().gemm_f32_route(tokens, experts, top, logits, ldl, bias, score, groups, group_top,
+                                 group_best, renorm, scale, choice, weight, stream)
+
+
+def gemm_f32_route_grad(tokens, experts, top, logits, ldl, score, renorm, scale, choice, dweight,
+                        dlogits, lddl, stream=0) -> int:
+    return load().gemm_f32_route_grad(tokens, experts, top, logits, ldl, score, renorm, scale,
+                                      choice, dweight, dlogits, lddl, stream)
+
+
+def gemm_f32_join_rows(tokens, top, N, H, ldh, weight, choice, groups, beta, Y, ldy,
+                       stream=0) -> int:
+    return load().gemm_f32_join_rows(tokens, top, N, H, ldh, weight, choice, groups, beta, Y, ldy,
+                                     stream)
+
+
+def gemm_f32_join_rows_grad(tokens, top, N, dY, lddy, H, ldh, weight, choice, groups, dH, lddh,
+                            dweight, stream=0) -> int:
+    return load().gemm_f32_join_rows_grad(tokens, top, N, dY, lddy, H, ldh, weight, choice, groups,
+                                          dH, lddh, dweight, stream)
+
+
+def gemm_f32_q4(M, N, K, alpha, A, lda, format, group, codes, ldq, scale_type, scale, lds, zero,
+                ldz, beta, C, ldc, bias, act, stream=0) -> int:
+    return load().gemm_f32_q4(M, N, K, alpha, A, lda, format, group, codes, ldq, scale_type, scale,
+                              lds, zero, ldz, beta, C, ldc, bias, act, stream)
+
+
+def gemm_f32_q4_grouped(rows, N, K, groups, offsets, alpha, A, lda, rowsA, indexA, format, group,
+                        codes, ldq, strideQ, scale_type, scale, lds, strideS, zero, ldz, strideZ,
+                        beta, C, ldc, rowsC, indexC, bias, strideBias, act, stream=0) -> int:
+    return load().gemm_f32_q4_grouped(rows, N, K, groups, offsets, alpha, A, lda, rowsA, indexA,
+                                      format, group, codes, ldq, strideQ, scale_type, scale, lds,
+                                      strideS, zero, ldz, strideZ, beta, C, ldc, rowsC, indexC,
+                                      bias, strideBias, act, stream)
+
+
+def gemm_f32_norm(count, x, n, norm, stream=0) -> int:
+    return load().gemm_f32_norm(count, x, n, norm, stream)
+
+
+def gemm_f32_clip(count, x, n, out, max_norm, norm, stream=0) -> int:
+    return load().gemm_f32_clip(count, x, n, out, max_norm, norm, stream)
 
 
 def gemm_f32_ref_gpu(M, N, K, A, lda, B, ldb, C, ldc, stream=0) -> int:
@@ -713,6 +787,250 @@ def gemm_adapters_grad(dY, X, W, down, up, offsets, order, H, *, trans=False, sc
                 gemm_grouped_wgrad(dY, H, offsets, index_a=order))
     return (dX, gemm_grouped_wgrad(X, G, offsets, index_a=order),
             gemm_grouped_wgrad(H, dY, offsets, index_b=order))
+
+
+# ---- around an expert layer ----------------------------------------------------
+
+def _entries(t, name, dtype, device, rows, cols):
+    """Pointer of a contiguous rows x cols tensor on ``device`` (0 for None)."""
+    if t is None:
+        return 0
+    if t.dtype is not dtype or tuple(t.shape) != (rows, cols) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {rows}x{cols} {dtype} tensor")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device} (got {t.device})")
+    return t.data_ptr()
+
+
+def route(logits, top, *, bias=None, score=SCORE_SOFTMAX, groups=1, group_top=None, group_best=1,
+          renorm=False, scale=1.0):
+    """The ``top`` experts of each row of ``logits`` (tokens x experts) by softmax
+    or sigmoid scores plus ``bias`` (experts floats or None), and their weights:
+    scale * score, over the sum of the token's chosen scores with ``renorm``.  With
+    ``groups`` of experts only those of the ``group_top`` best groups are taken, a
+    group's score being its best value or the sum of its best ``group_best`` = 2.
+    Returns (choice, weight), tokens x top: int32 with -1 (and weight 0) where too
+    few experts are left, as group_rows takes them, and float32."""
+    import torch
+    dev = _gpu(logits, "logits")
+    ptr, ldl, tokens, experts = _matrix(logits, "logits", dev)
+    top, groups = int(top), int(groups)
+    choice = logits.new_empty((tokens, max(top, 0)), dtype=torch.int32)
+    weight = logits.new_empty((tokens, max(top, 0)))
+    rc = _on(logits, gemm_f32_route, tokens, experts, top, ptr, ldl,
+             _vector(bias, "bias", dev, experts), int(score), groups,
+             groups if group_top is None else int(group_top), int(group_best), 1 if renorm else 0,
+             scale, choice.data_ptr(), weight.data_ptr())
+    if rc != GEMM_F32_OK:
+        raise GemmError(rc, "gemm_f32_route")
+    return choice, weight
+
+
+def route_grad(dweight, logits, choice, *, score=SCORE_SOFTMAX, renorm=False, scale=1.0,
+               dlogits=None):
+    """Gradient of route's weights with respect to the logits, from the weights'
+    (tokens x top) and the choices that route returned.  Returns dlogits."""
+    import torch
+    dev = _gpu(logits, "logits")
+    ptr, ldl, tokens, experts = _matrix(logits, "logits", dev)
+    if choice.dim() != 2:
+        raise ValueError("choice must be tokens x top")
+    top = choice.shape[1]
+    c = _entries(choice, "choice", torch.int32, dev, tokens, top)
+    dw = _entries(dweight, "dweight", torch.float32, dev, tokens, top)
+    if dlogits is None:
+        dlogits = logits.new_empty((tokens, experts))
+    d, ldd, _, _ = _matrix(dlogits, "dlogits", dev, tokens, experts)
+    rc = _on(logits, gemm_f32_route_grad, tokens, experts, top, ptr, ldl, int(score),
+             1 if renorm else 0, scale, c, dw, d, ldd)
+    if rc != GEMM_F32_OK:
+        raise GemmError(rc, "gemm_f32_route_grad")
+    return dlogits
+
+
+def join_rows(H, weight, choice=None, Y=None, *, groups=MAX_GROUPS, beta=0.0):
+    """Y[t] = sum over j of weight[t, j] * H[t * top + j], plus beta * Y[t]: the
+    experts' rows of each token added up.  Entries whose choice (int32, tokens x
+    top; None: all count) is outside [0, groups) are left out.  Returns Y."""
+    import torch
+    dev = _gpu(H, "H")
+    if weight.dim() != 2:
+        raise ValueError("weight must be tokens x top")
+    tokens, top = weight.shape
+    h, ldh, _, N = _matrix(H, "H", dev, tokens * top)
+    w = _entries(weight, "weight", torch.float32, dev, tokens, top)
+    c = _entries(choice, "choice", torch.int32, dev, tokens, top)
+    if Y is None:
+        Y = H.new_empty((tokens, N))
+    y, ldy, _, _ = _matrix(Y, "Y", dev, tokens, N)
+    rc = _on(H, gemm_f32_join_rows, tokens, top, N, h, ldh, w, c, int(groups), beta, y, ldy)
+    if rc != GEMM_F32_OK:
+        raise GemmError(rc, "gemm_f32_join_rows")
+    return Y
+
+
+def join_rows_grad(dY, H, weight, choice=None, dH=None, *, groups=MAX_GROUPS):
+    """Gradients of join_rows for the gradient dY of Y: (dH, dweight), zeros at the
+    entries that are left out."""
+    import torch
+    dev = _gpu(H, "H")
+    if weight.dim() != 2:
+        raise ValueError("weight must be tokens x top")
+    tokens, top = weight.shape
+    h, ldh, _, N = _matrix(H, "H", dev, tokens * top)
+    dy, lddy, _, _ = _matrix(dY, "dY", dev, tokens, N)
+    w = _entries(weight, "weight", torch.float32, dev, tokens, top)
+    c = _entries(choice, "choice", torch.int32, dev, tokens, top)
+    if dH is None:
+        dH = H.new_empty((tokens * top, N))
+    d, lddh, _, _ = _matrix(dH, "dH", dev, tokens * top, N)
+    dweight = H.new_empty((tokens, top))
+    rc = _on(H, gemm_f32_join_rows_grad, tokens, top, N, dy, lddy, h, ldh, w, c, int(groups), d,
+             lddh, dweight.data_ptr())
+    if rc != GEMM_F32_OK:
+        raise GemmError(rc, "gemm_f32_join_rows_grad")
+    return dH, dweight
+
+
+def _scale_type(t):
+    import torch
+    types = {torch.float32: SCALE_F32, torch.float16: SCALE_F16, torch.bfloat16: SCALE_BF16,
+             torch.uint8: SCALE_E8M0, torch.float8_e8m0fnu: SCALE_E8M0}
+    if t.dtype not in types:
+        raise TypeError(f"scale must be float32, float16, bfloat16 or e8m0 bytes, not {t.dtype}")
+    return types[t.dtype]
+
+
+def _packed(t, name, device, lead, rows, cols):
+    """(pointer, pitch, stride) of a tensor lead + (rows, cols) on ``device`` whose
+    rows are contiguous, in elements; lead is () or (groups,)."""
+    if tuple(t.shape) != (*lead, rows, cols):
+        raise ValueError(f"{name} must be {'x'.join(map(str, (*lead, rows, cols)))}, got "
+                         f"{'x'.join(map(str, t.shape))}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device} (got {t.device})")
+    s = t.stride()
+    return t.data_ptr(), _rows(rows, cols, s[-2], s[-1], name), s[0] if lead else 0
+
+
+def _q4(codes, scale, zero, group, format, device, lead, K):
+    """The arguments of 4-bit weights, N x K (for each of lead): (N, format ... ldz)
+    and the three strides."""
+    import torch
+    if codes.dtype is not torch.uint8 or codes.dim() != len(lead) + 2:
+        raise TypeError(f"codes must be a {len(lead) + 2}-D uint8 tensor")
+    group = int(group)
+    if group < 1:
+        raise ValueError("group must be positive")
+    N, along = codes.shape[-2], (K + group - 1) // group
+    q, ldq, sq = _packed(codes, "codes", device, lead, N, (K + 1) // 2)
+    kind = _scale_type(scale)
+    s, lds, ss = _packed(scale, "scale", device, lead, N, along)
+    z, ldz, sz = 0, 1, 0
+    if zero is not None:
+        if zero.dtype is not torch.uint8:
+            raise TypeError("zero must be a uint8 tensor")
+        z, ldz, sz = _packed(zero, "zero", device, lead, N, along)
+    return N, int(format), group, q, ldq, sq, kind, s, lds, ss, z, ldz, sz
+
+
+def gemm_q4(A, codes, scale, C=None, *, zero=None, group=128, format=Q4_INT, alpha=1.0, beta=0.0,
+            bias=None, act=ACT_NONE):
+    """C = act(alpha * A @ W.T + beta * C + bias) with W (N x K) in 4 bits: ``codes``
+    uint8, N x (K + 1) // 2, the even k in a byte's low half; ``scale`` N x groups of
+    K, float32, float16, bfloat16 or e8m0 bytes; Q4_INT: (code - zero) * scale with
+    ``zero`` uint8 like scale (None: 8), Q4_E2M1: the e2m1 value * scale.  ``group`` is
+    a power of two from 32 on.  (q4.quantize makes them from a matrix.)  Returns C."""
+    dev = _gpu(A, "A")
+    a, lda, M, K = _matrix(A, "A", dev)
+    N, fmt, group, q, ldq, _, kind, s, lds, _, z, ldz, _ = _q4(codes, scale, zero, group, format,
+                                                               dev, (), K)
+    if C is None:
+        C = A.new_empty((M, N))
+    c, ldc, _, _ = _matrix(C, "C", dev, M, N)
+    rc = _on(A, gemm_f32_q4, M, N, K, alpha, a, lda, fmt, group, q, ldq, kind, s, lds, z, ldz,
+             beta, c, ldc, _vector(bias, "bias", dev, N), int(act))
+    if rc != GEMM_F32_OK:
+        raise GemmError(rc, "gemm_f32_q4")
+    return C
+
+
+def gemm_q4_grouped(A, codes, scale, offsets, C=None, *, zero=None, group=128, format=Q4_INT,
+                    alpha=1.0, beta=0.0, bias=None, act=ACT_NONE, index_a=None, index_c=None):
+    """gemm_grouped with weights in 4 bits: C[index_c[i]] = act(alpha * A[index_a[i]]
+    @ W[g].T + beta * C[index_c[i]] + bias[g]) for every place i of group g, with
+    ``codes``, ``scale`` and ``zero`` as gemm_q4 takes them, one matrix for each group.
+    Returns C."""
+    dev, groups = _gpu(A, "A"), _groups_of(offsets)
+    a, lda, rows_a, K = _matrix(A, "A", dev)
+    N, fmt, group, q, ldq, sq, kind, s, lds, ss, z, ldz, sz = _q4(codes, scale, zero, group, format,
+                                                                  dev, (groups,), K)
+    rows = (index_a.shape[0] if index_a is not None else
+            index_c.shape[0] if index_c is not None else rows_a)
+    ia, ic = _index(index_a, "index_a", dev, rows), _index(index_c, "index_c", dev, rows)
+    if C is None:
+        C = A.new_empty((rows, N))
+    c, ldc, rows_c, _ = _matrix(C, "C", dev, cols=N)
+    bptr, sbias = _biases(bias, dev, groups, N)
+    rc = _on(A, gemm_f32_q4_grouped, rows, N, K, groups, _index(offsets, "offsets", dev), alpha, a,
+             lda, rows_a, ia, fmt, group, q, ldq, sq, kind, s, lds, ss, z, ldz, sz, beta, c, ldc,
+             rows_c, ic, bptr, sbias, int(act))
+    if rc != GEMM_F32_OK:
+        raise GemmError(rc, "gemm_f32_q4_grouped")
+    return C
+
+
+def _arrays(tensors, name, device):
+    """Host tables of the pointers and sizes of contiguous float32 tensors."""
+    import torch
+    f32 = torch.float32
+    for t in tensors:
+        if t.dtype is not f32 or not t.is_contiguous():
+            raise TypeError(f"{name} must hold contiguous float32 tensors")
+        if t.device != device:
+            raise ValueError(f"{name} must be on {device} (got {t.device})")
+    n = len(tensors)
+    return ((ctypes.c_void_p * n)(*[t.data_ptr() for t in tensors]),
+            (ctypes.c_int64 * n)(*[t.numel() for t in tensors]))
+
+
+def _norm_of(tensors, out, max_norm, norm):
+    import torch
+    tensors = list(tensors)
+    if not tensors:
+        raise ValueError("there are no tensors")
+    dev = _gpu(tensors[0], "tensors")
+    x, n = _arrays(tensors, "tensors", dev)
+    y = None
+    if out is not None:
+        out = list(out)
+        y, m = _arrays(out, "out", dev)
+        if len(out) != len(tensors) or m[:] != n[:]:
+            raise ValueError("out must hold a tensor of the same size for each")
+    if norm is None:
+        norm = torch.empty(1, dtype=torch.float32, device=dev)
+    ptr = _vector(norm, "norm", dev, 1)
+    if max_norm is None:
+        rc, what = _on(tensors[0], gemm_f32_norm, len(tensors), x, n, ptr), "gemm_f32_norm"
+    else:
+        rc, what = (_on(tensors[0], gemm_f32_clip, len(tensors), x, n, y, max_norm, ptr),
+                    "gemm_f32_clip")
+    if rc != GEMM_F32_OK:
+        raise GemmError(rc, what)
+    return norm
+
+
+def norm(tensors, norm=None):
+    """The norm of all elements of contiguous float32 GPU tensors (a model's
+    gradients) together, as a 1-element tensor, summed in 64 bits."""
+    return _norm_of(tensors, None, None, norm)
+
+
+def clip_norm(tensors, max_norm, out=None, norm=None):
+    """The tensors scaled by max_norm / norm where their norm together is above
+    max_norm: in place, or into the tensors of ``out``.  A norm that is not finite
+    leaves them as they are.  Returns the norm before, a 1-element tensor."""
+    return _norm_of(tensors, out, max_norm, norm)
 
 
 class _device:

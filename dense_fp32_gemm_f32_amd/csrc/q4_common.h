@@ -1,0 +1,151 @@
+// What the kernels of the products with 4-bit weights share.
+//
+// An fp32 value is the sum of three bf16 values exactly (its 24 significant bits
+// in three times 8), and a 4-bit weight without its scale, code - zero or the e2m1
+// value, is one bf16 value exactly.  So the fp32 product is three bf16 products
+// whose terms are exact and whose sums the matrix instruction holds in fp32, at a
+// third of the bf16 rate (about 450 TFLOP/s by the library's own 1350) where the
+// fp32 matrix instruction has 157.  The scale is the group's: a group's sum is
+// formed without it and added, times the scale, to the output's sum in fp32.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "experts_internal.h"
+
+namespace gemmf32 {
+namespace q4 {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// The high halves of b and a, a's below b's.
+__device__ __forceinline__ uint32_t high_halves(float a, float b) {
+  return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+}
+
+// Eight fp32 values as three times eight bf16 values (parts[0] the highest).  The
+// parts are cut off, not rounded: each remainder is exact and has the value's
+// sign, and nothing overflows.  A value that is not finite has itself as its first
+// part and zeros behind it.
+__device__ __forceinline__ void split8(const float (&x)[8], u32x4 (&parts)[3]) {
+  float y[8], h[8];
+  float probe = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    y[i] = x[i];
+    probe = fmaf(x[i], 0.f, probe);   // NaN if any is not finite
+  }
+  const bool finite = probe == 0.f;
+#pragma unroll
+  for (int part = 0; part < 3; ++part) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = __uint_as_float(__float_as_uint(y[i]) & 0xffff0000u);
+    if (!finite) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t u = __float_as_uint(x[i]);
+        if ((u & 0x7f800000u) == 0x7f800000u)   // a NaN stays one with its low bits cut off
+          h[i] = part > 0 ? 0.f
+                          : __uint_as_float((u & 0xffff0000u) | ((u & 0x7fffffu) ? 0x400000u : 0u));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) parts[part][i] = high_halves(h[2 * i], h[2 * i + 1]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = y[i] - h[i];
+  }
+}
+
+// Eight weights without their scale, from a dword of codes (the first k in its low
+// bits).  int codes: read as e4m3 with a scale of 2^9, the bytes 0 .. 15 are the
+// values 0 .. 15 (the format is linear there), so that one instruction converts
+// two; minus the zero point they are whole numbers of at most 8 bits.
+template <bool kE2m1>
+__device__ __forceinline__ bf16x8 weights8(uint32_t x, float zero) {
+  u32x4 w;
+  if constexpr (kE2m1) {
+    bf16x2 v[4];
+    v[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, 1.f, 0);
+    v[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, 1.f, 1);
+    v[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, 1.f, 2);
+    v[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, 1.f, 3);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __builtin_bit_cast(uint32_t, v[i]);
+  } else {
+    const uint32_t lo = x & 0x0f0f0f0fu, hi = (x >> 4) & 0x0f0f0f0fu;
+    const f32x2 e0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(lo, 512.f, false),
+                e1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(lo, 512.f, true),
+                o0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(hi, 512.f, false),
+                o1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(hi, 512.f, true);
+    w[0] = high_halves(e0[0] - zero, o0[0] - zero);
+    w[1] = high_halves(e0[1] - zero, o0[1] - zero);
+    w[2] = high_halves(e1[0] - zero, o1[0] - zero);
+    w[3] = high_halves(e1[1] - zero, o1[1] - zero);
+  }
+  return __builtin_bit_cast(bf16x8, w);
+}
+
+// Entry i of the scales, as fp32.  e8m0 is the exponent of a power of two, 255 NaN.
+__device__ __forceinline__ float load_scale(const void* scale, int type, int64_t i) {
+  if (type == kScaleF32) return static_cast<const float*>(scale)[i];
+  if (type == kScaleF16) return (float)static_cast<const _Float16*>(scale)[i];
+  if (type == kScaleBf16)
+    return __uint_as_float((uint32_t) static_cast<const uint16_t*>(scale)[i] << 16);
+  const uint32_t e = static_cast<const uint8_t*>(scale)[i];
+  return __uint_as_float(e == 255 ? 0x7fc00000u : e == 0 ? 0x00400000u : e << 23);
+}
+
+// 32 consecutive codes of a row from k on (a multiple of 32); those past the last
+// are zeros and their bytes are not read.
+__device__ __forceinline__ u32x4 load_codes(const uint8_t* row, int64_t k, int64_t K) {
+  u32x4 v = {0u, 0u, 0u, 0u};
+  if (k + 32 <= K) {
+    __builtin_memcpy(&v, row + k / 2, sizeof(v));
+  } else if (k < K) {
+    const int bytes = (int)(K - k + 1) / 2;
+    for (int i = 0; i < bytes; ++i) {
+      const uint32_t b = row[k / 2 + i];
+#pragma unroll
+      for (int d = 0; d < 4; ++d)
+        if (i >> 2 == d) v[d] |= b << 8 * (i & 3);
+    }
+  }
+  return v;
+}
+
+// Lane group g (16 lanes) has dwords 0 .. 3 of codes 32 g + 0 .. 31; afterwards
+// dword i holds codes 32 i + 8 g + 0 .. 7: the transposition of four groups and
+// four registers.
+__device__ __forceinline__ u32x4 by_steps(u32x4 v) {
+  const auto a = __builtin_amdgcn_permlane32_swap(v[0], v[2], false, false);
+  const auto b = __builtin_amdgcn_permlane32_swap(v[1], v[3], false, false);
+  const auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+  const auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+  return u32x4{c[0], c[1], d[0], d[1]};
+}
+
+__device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// One group's matrix of weights.
+struct Weights {
+  const uint8_t* codes;
+  const uint8_t* zero;   // NULL: 8
+  const void* scale;
+  int64_t scale0;        // entry of row 0, group 0
+  __device__ __forceinline__ Weights(const Q4Problem& p, int g)
+      : codes(p.codes + g * p.sq),
+        zero(p.zero ? p.zero + g * p.sz : nullptr),
+        scale(p.scale),
+        scale0(g * p.ss) {}
+};
+
+}  // namespace q4
+}  // namespace gemmf32

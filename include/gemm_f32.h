@@ -365,6 +365,189 @@ int gemm_f32_adapters(int trans, int64_t M, int64_t N, int64_t K, int64_t R,
                       float *Y, int64_t ldy, void *stream);
 
 /*
+ * gemm_f32_route -- a router's choices and their weights, from its logits: what
+ * gemm_f32_group_rows orders and gemm_f32_join_rows weighs.  For each of `tokens`
+ * rows of `experts` logits (pitch ldl), s = softmax or sigmoid of the row
+ * (`score`), v = s + bias (bias NULL: v = s; it takes part in the choice, not in
+ * the weight), and
+ *   choice[t*top + j]  the expert of the (j+1)-largest v, equal ones in the order
+ *                      of their numbers;
+ *   weight[t*top + j]  scale * s of that expert; with renorm, scale * s / (the sum
+ *                      of s over the token's choices).
+ * The experts may lie in `groups` groups of equal size, one after the other: only
+ * those of the group_top groups with the best score can be chosen, a group's score
+ * being the largest v in it (group_best 1) or the sum of its two largest
+ * (group_best 2; of its one, where one can be chosen).  groups 1 and group_top 1
+ * put no such limit.
+ *
+ * An expert whose logit or v is NaN or -infinity is not chosen (+infinity counts
+ * as the largest finite number) and has s = 0.  Where fewer than `top` can be, the
+ * rest of the token's choices are -1 with weight 0: no group, to
+ * gemm_f32_group_rows.  Choices are decided in 64 bits (without a bias, and
+ * without sums of two, by the logits themselves); weights are fp32.
+ *
+ * choice and weight: tokens x top, contiguous.  Errors: negative sizes, tokens
+ * above GEMM_F32_MAX_DIM, experts above GEMM_F32_MAX_GROUPS, top above
+ * GEMM_F32_MAX_TOP, groups below 1 or no divisor of experts
+ * GEMM_F32_ERR_INVALID_DIM; ldl below a row GEMM_F32_ERR_INVALID_LD; an unknown
+ * score, group_top outside [1, groups], group_best other than 1 or 2
+ * GEMM_F32_ERR_INVALID_ARG; NULL, alignment, overlap, device and reachability as
+ * gemm_f32_group_rows.  tokens or top == 0 is a successful no-op; experts == 0
+ * gives choices of -1.
+ */
+#define GEMM_F32_MAX_TOP 64
+#define GEMM_F32_SCORE_SOFTMAX 0
+#define GEMM_F32_SCORE_SIGMOID 1
+int gemm_f32_route(int64_t tokens, int64_t experts, int64_t top,
+                   const float *logits, int64_t ldl, const float *bias,
+                   int score, int64_t groups, int64_t group_top, int group_best,
+                   int renorm, float scale,
+                   int32_t *choice, float *weight, void *stream);
+
+/*
+ * gemm_f32_route_grad -- the gradient of gemm_f32_route's weights: dlogits (tokens
+ * x experts, pitch lddl) from dweight (tokens x top, contiguous) and the choices it
+ * wrote, with the same logits, score, renorm and scale.  The choice itself has no
+ * gradient, the bias neither.  Every entry of dlogits is written: 0 for an expert
+ * whose logit is NaN or -infinity; a choice outside [0, experts) adds nothing, and
+ * an expert named twice gets both.  Checks and errors as gemm_f32_route (top may be
+ * 0: dlogits are zeros).
+ */
+int gemm_f32_route_grad(int64_t tokens, int64_t experts, int64_t top,
+                        const float *logits, int64_t ldl,
+                        int score, int renorm, float scale,
+                        const int32_t *choice, const float *dweight,
+                        float *dlogits, int64_t lddl, void *stream);
+
+/*
+ * gemm_f32_join_rows -- the experts' rows added up for each token: with H one row
+ * of N floats for each choice (tokens * top rows, pitch ldh, as gemm_f32_grouped
+ * scatters them by indexC = order),
+ *   Y[t] = sum_j weight[t*top + j] * H[t*top + j] + beta * Y[t]
+ * over the entries whose choice is in [0, groups); choice NULL: all of them.  The
+ * rows of other entries are not read.  A token without an entry gets beta * Y[t].
+ * beta == 0 does not read Y.  Sums are fp32, in the order of j.
+ *
+ * Errors: negative sizes, tokens * top or N above GEMM_F32_MAX_DIM, groups above
+ * GEMM_F32_MAX_GROUPS GEMM_F32_ERR_INVALID_DIM; a pitch below a row
+ * GEMM_F32_ERR_INVALID_LD; NULL, alignment, overlap (Y with anything), device and
+ * reachability as gemm_f32_grouped.  tokens or N == 0 is a successful no-op.
+ */
+int gemm_f32_join_rows(int64_t tokens, int64_t top, int64_t N,
+                       const float *H, int64_t ldh, const float *weight,
+                       const int32_t *choice, int64_t groups,
+                       float beta, float *Y, int64_t ldy, void *stream);
+
+/*
+ * gemm_f32_join_rows_grad -- its gradients, for dY: dH[t*top + j] = weight[t*top + j]
+ * * dY[t] (pitch lddh) and dweight[t*top + j] = <dY[t], H[t*top + j]>.  Both are
+ * written for every entry; 0 where the choice is outside [0, groups), whose rows of
+ * H are not read.  Checks and errors as gemm_f32_join_rows; N == 0 gives
+ * dweight 0.
+ */
+int gemm_f32_join_rows_grad(int64_t tokens, int64_t top, int64_t N,
+                            const float *dY, int64_t lddy,
+                            const float *H, int64_t ldh, const float *weight,
+                            const int32_t *choice, int64_t groups,
+                            float *dH, int64_t lddh, float *dweight, void *stream);
+
+/*
+ * gemm_f32_q4 -- C = act(alpha * A W^T + beta * C + bias) with weights W (N x K) held
+ * in 4 bits with a scale for each group of `group` columns:
+ *   GEMM_F32_Q4_INT    W[n][k] = (code - zero[n][k / group]) * scale[n][k / group]
+ *                      with codes and zero points 0 .. 15 (a byte's low bits; any
+ *                      zero point up to 255 is taken as it is), zero NULL: 8;
+ *   GEMM_F32_Q4_E2M1   W[n][k] = e2m1(code) * scale[n][k / group]: sign, two bits of
+ *                      exponent, one of mantissa (0, .5, 1, 1.5, 2, 3, 4, 6); zero
+ *                      must be NULL.
+ * codes: row n at n * ldq bytes, two codes to a byte, the even k in the low half
+ * (an odd K leaves the last high half unread in meaning: any value).  scale: row n at
+ * n * lds, of scale_type GEMM_F32_SCALE_F32, _F16, _BF16 or _E8M0 (one byte, the
+ * power of two 2^(e - 127); 255 is NaN).  zero: one byte each, row n at n * ldz.
+ * group: a power of two from 32 on; one beyond K gives each row one scale.
+ *
+ * A is M x K fp32 with pitch lda; nothing is rounded on the way: an fp32 value is
+ * split into three bf16 values exactly, a weight without its scale is one exactly,
+ * and their products are summed in fp32, a group's sum first, then times its scale.
+ * (So a group's sum of a * code must not pass the largest float, also where the
+ * scale would bring it back.)  Values that are not finite give what the formula
+ * gives.
+ *
+ * Errors as gemm_f32_fused; an unknown format or scale type, a group that is no
+ * power of two or below 32, zero points with e2m1 GEMM_F32_ERR_INVALID_ARG; ldq
+ * below (K + 1) / 2, lds or ldz below the groups of a row GEMM_F32_ERR_INVALID_LD;
+ * pointers need the alignment of their elements.  K == 0 gives the update of an
+ * empty sum; M or N == 0 is a successful no-op.
+ */
+#define GEMM_F32_Q4_INT 0
+#define GEMM_F32_Q4_E2M1 1
+#define GEMM_F32_SCALE_F32 0
+#define GEMM_F32_SCALE_F16 1
+#define GEMM_F32_SCALE_BF16 2
+#define GEMM_F32_SCALE_E8M0 3
+int gemm_f32_q4(int64_t M, int64_t N, int64_t K, float alpha,
+                const float *A, int64_t lda,
+                int format, int64_t group,
+                const uint8_t *codes, int64_t ldq,
+                int scale_type, const void *scale, int64_t lds,
+                const uint8_t *zero, int64_t ldz,
+                float beta, float *C, int64_t ldc,
+                const float *bias, int activation, void *stream);
+
+/*
+ * gemm_f32_q4_grouped -- gemm_f32_grouped with such weights, one matrix for each
+ * group of places: C[ic(i)] = act(alpha * A[ia(i)] W_g^T + beta * C[ic(i)] + bias_g),
+ * W_g's codes at codes + g * strideQ (bytes), scales at scale + g * strideS
+ * (elements), zero points at zero + g * strideZ (bytes).  Places, offsets, indexes
+ * and what stays as it was as gemm_f32_grouped; weights, checks and errors as
+ * gemm_f32_q4 (a negative stride GEMM_F32_ERR_INVALID_LD).
+ */
+int gemm_f32_q4_grouped(int64_t rows, int64_t N, int64_t K,
+                        int64_t groups, const int32_t *offsets, float alpha,
+                        const float *A, int64_t lda, int64_t rowsA,
+                        const int32_t *indexA,
+                        int format, int64_t group,
+                        const uint8_t *codes, int64_t ldq, int64_t strideQ,
+                        int scale_type, const void *scale, int64_t lds,
+                        int64_t strideS,
+                        const uint8_t *zero, int64_t ldz, int64_t strideZ,
+                        float beta, float *C, int64_t ldc, int64_t rowsC,
+                        const int32_t *indexC,
+                        const float *bias, int64_t strideBias, int activation,
+                        void *stream);
+
+/*
+ * gemm_f32_norm -- *norm = sqrt(the sum of the squares of all elements of `count`
+ * arrays): the global norm of a model's gradients.  x and n are host arrays: the
+ * device pointers and the elements of each (an array without elements may be NULL).
+ * Squares are summed in 64 bits, in an order that depends on the sizes only; the
+ * result is rounded once.  Arrays may overlap.  Uses the stream's workspace.
+ *
+ * Errors: a negative count or size, a count above 2^20, an array above 2^40
+ * elements GEMM_F32_ERR_INVALID_DIM; NULL x or n with count > 0, a NULL array with
+ * elements, NULL norm GEMM_F32_ERR_NULL_PTR; alignment, norm inside an array
+ * (GEMM_F32_ERR_ALIAS), device and reachability as reduce_sum_f32.  count == 0
+ * gives +0.0.
+ */
+int gemm_f32_norm(int64_t count, const float *const *x, const int64_t *n,
+                  float *norm, void *stream);
+
+/*
+ * gemm_f32_clip -- the arrays scaled so that their global norm is at most max_norm:
+ * *norm as gemm_f32_norm writes it, and y[i] = x[i] * (max_norm / norm) where the norm
+ * is above max_norm, else y[i] = x[i].  A norm that is not finite (one of the values
+ * is not) leaves y[i] = x[i]: the caller sees it in *norm.  out: host array of the
+ * y, each equal to its x (in place) or apart from everything else; NULL: all in
+ * place.  Where nothing is to scale, arrays in place are not written.
+ *
+ * Checks and errors as gemm_f32_norm; max_norm negative or NaN
+ * GEMM_F32_ERR_INVALID_ARG; a y that overlaps another array, or norm,
+ * GEMM_F32_ERR_ALIAS.
+ */
+int gemm_f32_clip(int64_t count, const float *const *x, const int64_t *n,
+                  float *const *out, float max_norm, float *norm, void *stream);
+
+/*
  * gemm_f32_ref_gpu -- the same operation with the naive one-thread-per-output
  * kernel ("Optimizing a WebGPU Matmul Kernel using Subgroups", sections 1-3:
  * one invocation per element of C, adjacent threads on adjacent columns, k
