@@ -84,5 +84,6 @@ struct Q4Problem {
   bool e2m1 = false;
 };
 hipError_t launch_q4_few(const Q4Problem& p, const Epilogue& e, hipStream_t s);
+hipError_t launch_q4_tiles(const Q4Problem& p, const Epilogue& e, hipStream_t s);
 
 }  // namespace gemmf32

@@ -127,7 +127,7 @@ __device__ void tile(const Q4Problem& p, const Epilogue& ep, const Weights& w, i
 #pragma unroll
         for (int c = 0; c < CT; ++c) {
           const int s = NS == 1 ? 0 : i;
-          const bf16x8 b = weights8<kE2m1>(steps[c][i], kE2m1 ? 0.f : it.zero[c][s]);
+          const bf16x8 b = weights8<kE2m1, false>(steps[c][i], kE2m1 ? 0.f : it.zero[c][s], 1.f);
 #pragma unroll
           for (int t = 0; t < RT; ++t) {
             const f32x4 zero = {0.f, 0.f, 0.f, 0.f};

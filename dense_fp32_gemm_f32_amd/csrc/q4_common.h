@@ -62,19 +62,21 @@ __device__ __forceinline__ void split8(const float (&x)[8], u32x4 (&parts)[3]) {
   }
 }
 
-// Eight weights without their scale, from a dword of codes (the first k in its low
-// bits).  int codes: read as e4m3 with a scale of 2^9, the bytes 0 .. 15 are the
-// values 0 .. 15 (the format is linear there), so that one instruction converts
-// two; minus the zero point they are whole numbers of at most 8 bits.
-template <bool kE2m1>
-__device__ __forceinline__ bf16x8 weights8(uint32_t x, float zero) {
+// Eight weights from a dword of codes (the first k in its low bits), without their
+// scale, or with a scale that is a power of two (kScaled): bf16 values exactly.  int
+// codes: read as e4m3 with a scale of 2^9, the bytes 0 .. 15 are the values 0 .. 15
+// (the format is linear there), so that one instruction converts two; minus the
+// zero point they are whole numbers of at most 8 bits.
+template <bool kE2m1, bool kScaled>
+__device__ __forceinline__ bf16x8 weights8(uint32_t x, float zero, float scale) {
   u32x4 w;
+  const float by = kScaled ? scale : 1.f;
   if constexpr (kE2m1) {
     bf16x2 v[4];
-    v[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, 1.f, 0);
-    v[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, 1.f, 1);
-    v[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, 1.f, 2);
-    v[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, 1.f, 3);
+    v[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, by, 0);
+    v[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, by, 1);
+    v[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, by, 2);
+    v[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, by, 3);
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = __builtin_bit_cast(uint32_t, v[i]);
   } else {
@@ -83,10 +85,11 @@ __device__ __forceinline__ bf16x8 weights8(uint32_t x, float zero) {
                 e1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(lo, 512.f, true),
                 o0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(hi, 512.f, false),
                 o1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(hi, 512.f, true);
-    w[0] = high_halves(e0[0] - zero, o0[0] - zero);
-    w[1] = high_halves(e0[1] - zero, o0[1] - zero);
-    w[2] = high_halves(e1[0] - zero, o1[0] - zero);
-    w[3] = high_halves(e1[1] - zero, o1[1] - zero);
+    auto value = [&](float c) { return kScaled ? (c - zero) * by : c - zero; };
+    w[0] = high_halves(value(e0[0]), value(o0[0]));
+    w[1] = high_halves(value(e0[1]), value(o0[1]));
+    w[2] = high_halves(value(e1[0]), value(o1[0]));
+    w[3] = high_halves(value(e1[1]), value(o1[1]));
   }
   return __builtin_bit_cast(bf16x8, w);
 }
