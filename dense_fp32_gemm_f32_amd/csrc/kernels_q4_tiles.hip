@@ -125,34 +125,63 @@ struct Tiles {
 #pragma unroll
       for (int j = 0; j < kJ; ++j) s[j] = fs[wn * WN + 16 * j + (lane & 15)];
     }
-#pragma unroll
-    for (int i = 0; i < kI; ++i) {
+    if constexpr (kFold) {
+      // two blocks' sums are formed while the two before them are folded in.  The
+      // compiler, left alone, moves the folds behind the refill, whose branches end the
+      // block, and holds (or spills) all sums until then: the empty asm statements want
+      // each fold's result where it is.
+      constexpr int kAtOnce = 2, kGroups = kI * kJ / kAtOnce;
+      f32x4 sum[2][kAtOnce];
       bf16x8 part[3];
 #pragma unroll
-      for (int q = 0; q < 3; ++q)
-        part[q] = *reinterpret_cast<const bf16x8*>(fa + (i * 3 + q) * 1024);
-      if constexpr (kFold) {
-        constexpr int kAtOnce = 4;
+      for (int g = 0; g <= kGroups; ++g) {
+        const int i = g * kAtOnce / kJ, j0 = g * kAtOnce % kJ;
+        if (g < kGroups) {
+          if (j0 == 0) {
 #pragma unroll
-        for (int j0 = 0; j0 < kJ; j0 += kAtOnce) {
-          f32x4 sum[kAtOnce];
+            for (int q = 0; q < 3; ++q)
+              part[q] = *reinterpret_cast<const bf16x8*>(fa + (i * 3 + q) * 1024);
+          }
 #pragma unroll
           for (int q = 0; q < 3; ++q)
 #pragma unroll
             for (int j = 0; j < kAtOnce; ++j) {
               const f32x4 none = {0.f, 0.f, 0.f, 0.f};
-              sum[j] = mfma16(part[q], b[j0 + j], q ? sum[j] : none);
+              sum[g & 1][j] = mfma16(part[q], b[j0 + j], q ? sum[g & 1][j] : none);
             }
-#pragma unroll
-          for (int j = 0; j < kAtOnce; ++j) acc[i][j0 + j] += sum[j] * s[j0 + j];
         }
-      } else {
+        if (g > 0) {
+          const int fi = (g - 1) * kAtOnce / kJ, fj = (g - 1) * kAtOnce % kJ;
+#pragma unroll
+          for (int j = 0; j < kAtOnce; ++j) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              acc[fi][fj + j][r] = fmaf(sum[(g - 1) & 1][j][r], s[fj + j], acc[fi][fj + j][r]);
+            asm volatile("" : "+v"(acc[fi][fj + j]));
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kI; ++i) {
+        bf16x8 part[3];
+#pragma unroll
+        for (int q = 0; q < 3; ++q)
+          part[q] = *reinterpret_cast<const bf16x8*>(fa + (i * 3 + q) * 1024);
 #pragma unroll
         for (int q = 0; q < 3; ++q)
 #pragma unroll
           for (int j = 0; j < kJ; ++j) acc[i][j] = mfma16(part[q], b[j], acc[i][j]);
       }
     }
+  }
+
+  // During step t: the next one's values into the other buffer, and the loads of
+  // those behind it.
+  __device__ __forceinline__ void refill(int t, int steps) {
+    if (t + 1 < steps) convert((t + 1) & 1);
+    if (t + 2 < steps) load(t + 2);
   }
 
   // Places begin .. end - 1, the first BM of them.
@@ -188,15 +217,9 @@ struct Tiles {
       __syncthreads();
       const bool first = wave < kWaves / 2;   // converts first
       for (int t = 0; t < steps; ++t) {
-        if (first) {
-          if (t + 1 < steps) convert((t + 1) & 1);
-          if (t + 2 < steps) load(t + 2);
-          multiply(t & 1);
-        } else {
-          multiply(t & 1);
-          if (t + 1 < steps) convert((t + 1) & 1);
-          if (t + 2 < steps) load(t + 2);
-        }
+        if (first) refill(t, steps);
+        multiply(t & 1);
+        if (!first) refill(t, steps);
         __syncthreads();
       }
     }
