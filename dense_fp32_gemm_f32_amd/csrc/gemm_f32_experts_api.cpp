@@ -8,6 +8,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstdlib>
 #include <new>
 #include <vector>
 
@@ -195,7 +196,8 @@ int run_q4(int64_t rows, int64_t N, int64_t K, int64_t groups, const int32_t* of
   e.bias = bias;
   e.act = activation;
   // few rows in a group: bound by the read of the codes
-  const bool few = rows <= 24 * std::min(rows, groups);
+  static const char* force = getenv("Q4_TILE");
+  const bool few = force ? atoi(force) == 0 : rows <= 24 * std::min(rows, groups);
   hipStream_t s = static_cast<hipStream_t>(stream);
   return launched(few ? gemmf32::launch_q4_few(p, e, s) : gemmf32::launch_q4_tiles(p, e, s));
 }

@@ -30,27 +30,71 @@ __device__ __forceinline__ int slot(int q, int octet, int step) {
   return ((q + 4 * octet + step) & 15) + 16 * octet;
 }
 
-template <int CT, bool kE2m1, int NS>
+template <int CT, int NS>
 struct Item {   // a wave's chunk of its columns
   u32x4 codes[CT];
-  float scale[CT][NS], zero[CT][NS];
+  uint32_t scale[CT][NS], zero[CT][NS];   // as they are stored
 };
 
-template <int CT, bool kE2m1, int NS>
+// kRest: the chunk that passes the end of K, of which nothing behind a row's end is
+// read.  In whole chunks no branch leaves a load out and nothing looks at what is
+// loaded: they stay in flight while the chunk before is multiplied.
+template <int CT, bool kE2m1, int NS, bool kRest>
 __device__ __forceinline__ void fetch(const Q4Problem& p, const Weights& w, int chunk, int n0,
-                                      int lane, Item<CT, kE2m1, NS>& it) {
+                                      int lane, Item<CT, NS>& it) {
   const int64_t K = p.g.K, k0 = (int64_t)chunk * kChunkK;
 #pragma unroll
   for (int c = 0; c < CT; ++c) {
     // columns past the last read the last row: their sums are not stored
     const int64_t n = min(n0 + 16 * c + (lane & 15), p.g.N - 1);
-    it.codes[c] = load_codes(w.codes + n * p.ldq, k0 + 32 * (lane >> 4), K);
+    const uint8_t* row = w.codes + n * p.ldq;
+    if constexpr (kRest)
+      it.codes[c] = last_codes(row, k0 + 32 * (lane >> 4), K);
+    else
+      __builtin_memcpy(&it.codes[c], row + k0 / 2 + 16 * (lane >> 4), sizeof(u32x4));
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
-      const int64_t at = min(k0 + 32 * i, K - 1) >> p.group_shift;
+      const int64_t at = (kRest ? min(k0 + 32 * i, K - 1) : k0 + 32 * i) >> p.group_shift;
       it.scale[c][i] = load_scale(w.scale, p.scale_type, w.scale0 + n * p.lds + at);
-      if constexpr (!kE2m1) it.zero[c][i] = w.zero ? (float)w.zero[n * p.ldz + at] : 8.f;
+      if constexpr (!kE2m1) it.zero[c][i] = w.zero ? w.zero[n * p.ldz + at] : 8;
     }
+  }
+}
+
+// One chunk of a wave: parts are those of its first step in LDS.
+template <int RT, int CT, bool kE2m1, int NS>
+__device__ __forceinline__ void multiply(const Q4Problem& p, const Item<CT, NS>& it, int step0,
+                                         const char* lds, int lane, f32x4 (&acc)[RT][CT]) {
+  u32x4 steps[CT];
+#pragma unroll
+  for (int c = 0; c < CT; ++c) steps[c] = by_steps(it.codes[c]);
+  f32x4 sum[RT][CT];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    bf16x8 a[RT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+      a[t] = *reinterpret_cast<const bf16x8*>(
+          lds + (((step0 + i) * RT + t) * 64 + slot(lane & 15, lane >> 4, step0 + i)) * 16);
+#pragma unroll
+    for (int c = 0; c < CT; ++c) {
+      const int s = NS == 1 ? 0 : i;
+      const bf16x8 b = weights8<kE2m1, false>(steps[c][i], kE2m1 ? 0.f : (float)it.zero[c][s], 1.f);
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        const f32x4 none = {0.f, 0.f, 0.f, 0.f};
+        sum[t][c] = mfma16(a[t], b, NS == 1 && i > 0 ? sum[t][c] : none);
+      }
+    }
+    if (NS == 4 || i == 3) {
+#pragma unroll
+      for (int c = 0; c < CT; ++c) {
+        const float scale = scale_value(it.scale[c][NS == 1 ? 0 : i], p.scale_type);
+#pragma unroll
+        for (int t = 0; t < RT; ++t) acc[t][c] += sum[t][c] * scale;
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);   // else all steps' weights are converted first
   }
 }
 
@@ -72,8 +116,17 @@ __device__ void tile(const Q4Problem& p, const Epilogue& ep, const Weights& w, i
 #pragma unroll
     for (int c = 0; c < CT; ++c) acc[t][c] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  Item<CT, kE2m1, NS> next;
-  if (wave < chunks) fetch(p, w, wave, n0, lane, next);
+  // whole chunks; a part of one behind them is the wave's whose turn it would be
+  const int whole = (int)(K / kChunkK);
+  // chunks on the way into registers: as many as a wave has in a pass
+  constexpr int kAhead = 1;
+  Item<CT, NS> ahead[kAhead];
+  int chunk = wave;
+  if (whole > 0) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      fetch<CT, kE2m1, NS, false>(p, w, min(chunk + i * kWaves, whole - 1), n0, lane, ahead[i]);
+  }
   const unsigned inverse = (65536 + rows - 1) / rows;   // u / rows for u below 65536 / 16
   for (int base = 0; base < chunks; base += kPass<RT>) {
     const int here = min(kPass<RT>, chunks - base);
@@ -106,36 +159,21 @@ __device__ void tile(const Q4Problem& p, const Epilogue& ep, const Weights& w, i
       }
     }
     __syncthreads();
-    for (int chunk = base + wave; chunk < base + here; chunk += kWaves) {
-      const Item<CT, kE2m1, NS> it = next;
-      // this wave's next chunk, in this pass or in the next
-      int ahead = chunk + kWaves;
-      if (ahead >= base + here) ahead = base + here + wave;
-      if (ahead < chunks) fetch(p, w, ahead, n0, lane, next);
-      u32x4 steps[CT];
+    const int to = min(base + here, whole);
+    while (chunk < to) {
 #pragma unroll
-      for (int c = 0; c < CT; ++c) steps[c] = by_steps(it.codes[c]);
-      f32x4 sum[RT][CT];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int step = (chunk - base) * 4 + i;
-        bf16x8 a[RT];
-#pragma unroll
-        for (int t = 0; t < RT; ++t)
-          a[t] = *reinterpret_cast<const bf16x8*>(
-              lds + ((step * RT + t) * 64 + slot(lane & 15, lane >> 4, step)) * 16);
-#pragma unroll
-        for (int c = 0; c < CT; ++c) {
-          const int s = NS == 1 ? 0 : i;
-          const bf16x8 b = weights8<kE2m1, false>(steps[c][i], kE2m1 ? 0.f : it.zero[c][s], 1.f);
-#pragma unroll
-          for (int t = 0; t < RT; ++t) {
-            const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-            sum[t][c] = mfma16(a[t], b, NS == 1 && i > 0 ? sum[t][c] : zero);
-            if (NS == 4 || i == 3) acc[t][c] += sum[t][c] * it.scale[c][s];
-          }
-        }
+      for (int i = 0; i < kAhead; ++i) {
+        if (chunk >= to) break;
+        multiply<RT, CT, kE2m1, NS>(p, ahead[i], (chunk - base) * 4, lds, lane, acc);
+        fetch<CT, kE2m1, NS, false>(p, w, min(chunk + kAhead * kWaves, whole - 1), n0, lane,
+                                    ahead[i]);
+        chunk += kWaves;
       }
+    }
+    if (whole < chunks && base + here == chunks && wave == whole % kWaves) {
+      Item<CT, NS> rest;
+      fetch<CT, kE2m1, NS, true>(p, w, whole, n0, lane, rest);
+      multiply<RT, CT, kE2m1, NS>(p, rest, (whole - base) * 4, lds, lane, acc);
     }
   }
   __syncthreads();
@@ -171,7 +209,7 @@ __device__ void tile(const Q4Problem& p, const Epilogue& ep, const Weights& w, i
 }
 
 template <int CT, bool kE2m1, int NS>
-__global__ void __launch_bounds__(kThreads, 2) q4_few_kernel(Q4Problem p, Epilogue ep) {
+__global__ void __launch_bounds__(kThreads, 4) q4_few_kernel(Q4Problem p, Epilogue ep) {
   __shared__ __attribute__((aligned(16))) char lds[kLdsBytes];
   __shared__ int row_of[kRows];
   const int group = blockIdx.y;

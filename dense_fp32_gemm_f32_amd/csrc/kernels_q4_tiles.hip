@@ -13,6 +13,8 @@
 // column's scale.  A scale that is a power of two is put into the weights instead,
 // which stay bf16 values exactly, and the sums go straight on.
 #include "q4_common.h"
+#include <cstdlib>
+#include <type_traits>
 
 namespace gemmf32 {
 namespace {
@@ -26,86 +28,112 @@ __device__ __forceinline__ int fragment(int r, int o) {
   return (((r + 4 * o) & 15) + 16 * o) * 16;
 }
 
-template <int BM, int BN, int WM, int WN, bool kE2m1, bool kFold>
+// D: steps whose values are on the way into registers.
+// KS: groups of waves, each with every KS-th step and buffers of its own; the first
+// adds the others' sums to its own in order.
+template <int BM, int BN, int WM, int WN, int KS, int D, bool kE2m1, bool kFold>
 struct Tiles {
   static constexpr int kWavesN = BN / WN, kWaves = BM / WM * kWavesN, kThreads = 64 * kWaves;
+  static constexpr int kBM = BM, kBN = BN, kAllThreads = KS * kThreads;
   static constexpr int kI = WM / 16, kJ = WN / 16;
   static constexpr int kOctets = BM * 4 / kThreads;   // of A, a thread's
   static constexpr int kBytesA = BM * 3 * 64, kBytesW = BN * 64, kBytesS = kFold ? BN * 4 : 0;
   static constexpr int kStage = kBytesA + kBytesW + kBytesS;
-  static constexpr int kLds = 2 * kStage + BM * 8;
+  static constexpr int kSums = KS > 1 ? BM * BN * 4 : 0;
+  static constexpr int kBuffers = 2 * kStage > kSums ? 2 * kStage : kSums;
+  static constexpr int kLds = KS * kBuffers + BM * 8;
   static_assert(BM * 4 % kThreads == 0 && BN * 2 <= kThreads && BM <= kThreads, "one share each");
 
   const Q4Problem& p;
-  char* lds;
-  int tid, wave, lane, n0;
+  char* lds;         // of this thread's group
+  int* rows;         // from_row and to_row of all
+  int part_k, tid, wave, lane, n0;   // its group, and its place in that
   const Weights w;
   int64_t K;
   // this thread's share of the loads: octets of A's rows, and 16 codes of a column
-  const float* a[kOctets];       // NULL: a row that is not there
-  const uint8_t* codes;
+  const float* a[kOctets];
+  const uint8_t *codes, *zeros;
   int64_t n;                     // the column whose codes (and scale) it loads
-  float x[kOctets][8];
-  uint32_t c[2];
-  float scale, zero;
+  struct Values {
+    float x[kOctets][8];
+    uint32_t c[2];
+    // as they are stored (bytes as bytes: widened here, they would be masked, and so
+    // waited for, at the end of the loop that loads them)
+    std::conditional_t<kFold, uint32_t, uint8_t> scale;
+    uint8_t zero;
+  } v[D];
   f32x4 acc[kI][kJ];
 
   __device__ __forceinline__ Tiles(const Q4Problem& p, char* lds, int group, int n0)
-      : p(p), lds(lds), tid(threadIdx.x), wave(threadIdx.x >> 6), lane(threadIdx.x & 63), n0(n0),
-        w(p, group), K(p.g.K) {}
+      : p(p), rows(reinterpret_cast<int*>(lds + KS * kBuffers)),
+        part_k(KS > 1 ? __builtin_amdgcn_readfirstlane((int)threadIdx.x / kThreads) : 0),
+        tid((int)threadIdx.x - part_k * kThreads), wave(tid >> 6), lane(tid & 63), n0(n0),
+        w(p, group), K(p.g.K) {
+    this->lds = lds + part_k * kBuffers;
+  }
 
-  // One step's values into registers.
-  __device__ __forceinline__ void load(int step) {
-    const int64_t k0 = (int64_t)step * 32;
+  // The values of one of its group's whole steps into registers.  No branch leaves a
+  // load out and nothing looks at what is loaded, so that the loads of the steps
+  // behind stay in flight when one step's are waited for.
+  __device__ __forceinline__ void load(Values& v, int step) {
+    const int64_t k0 = ((int64_t)step * KS + part_k) * 32;
 #pragma unroll
-    for (int i = 0; i < kOctets; ++i) {
-      const int64_t k = k0 + 8 * (tid & 3);
-      if (a[i] && k + 8 <= K) {
-        __builtin_memcpy(x[i], a[i] + k0, sizeof(x[i]));
-      } else {
+    for (int i = 0; i < kOctets; ++i) __builtin_memcpy(v.x[i], a[i] + k0, sizeof(v.x[i]));
+    __builtin_memcpy(v.c, codes + k0 / 2, sizeof(v.c));
+    load_scales(v, k0);
+  }
+  __device__ __forceinline__ void load_scales(Values& v, int64_t k0) {
+    const int64_t at = k0 >> p.group_shift;
+    const int64_t i = w.scale0 + n * p.lds + at;
+    if constexpr (kFold)
+      v.scale = p.scale_type == kScaleF32 ? static_cast<const uint32_t*>(w.scale)[i]
+                                          : static_cast<const uint16_t*>(w.scale)[i];
+    else
+      v.scale = static_cast<const uint8_t*>(w.scale)[i];
+    if constexpr (!kE2m1) v.zero = zeros[at];
+  }
+
+  // The same for the part of K behind the whole steps: nothing behind a row's end is
+  // read.
+  __device__ __forceinline__ void load_rest(Values& v, int step) {
+    const int64_t k0 = ((int64_t)step * KS + part_k) * 32, left = K - k0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[i][j] = a[i] && k + j < K ? a[i][k0 + j] : 0.f;
+    for (int i = 0; i < kOctets; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int k = 8 * (tid & 3) + j;
+        v.x[i][j] = k < left ? a[i][k0 + j] : 0.f;
       }
-    }
-    if (tid < BN * 2) {
-      const int64_t k = k0 + 16 * (tid & 1);
-      if (k + 16 <= K) {
-        __builtin_memcpy(c, codes + k0 / 2, sizeof(c));
-      } else {   // bytes behind the row's last are not read
-        const int bytes = (int)(K - k + 1) / 2;
-        uint64_t v = 0;
-        for (int i = 0; i < bytes; ++i) v |= (uint64_t)codes[k0 / 2 + i] << 8 * i;
-        c[0] = (uint32_t)v;
-        c[1] = (uint32_t)(v >> 32);
-      }
-      const int64_t at = k0 >> p.group_shift;
-      if (step == 0 || at != (k0 - 32) >> p.group_shift) {
-        scale = load_scale(w.scale, p.scale_type, w.scale0 + n * p.lds + at);
-        if constexpr (!kE2m1) zero = w.zero ? (float)w.zero[n * p.ldz + at] : 8.f;
-      }
-    }
+    uint64_t u = 0;
+    for (int i = 0; i < 8 && 16 * (tid & 1) + 2 * i < left; ++i)
+      u |= (uint64_t)codes[k0 / 2 + i] << 8 * i;
+    v.c[0] = (uint32_t)u;
+    v.c[1] = (uint32_t)(u >> 32);
+    load_scales(v, min(k0, K - 1));
   }
 
   // The registers' values into a buffer.
-  __device__ __forceinline__ void convert(int buffer) {
+  __device__ __forceinline__ void convert(const Values& v, int buffer) {
     char* to = lds + buffer * kStage;
 #pragma unroll
     for (int i = 0; i < kOctets; ++i) {
       const int r = (tid >> 2) + i * (kThreads / 4);
       u32x4 parts[3];
-      split8(x[i], parts);
+      split8(v.x[i], parts);
 #pragma unroll
       for (int part = 0; part < 3; ++part)
         *reinterpret_cast<u32x4*>(to + ((r >> 4) * 3 + part) * 1024 + fragment(r & 15, tid & 3)) =
             parts[part];
     }
-    if (tid < BN * 2) {
+    if (BN * 2 == kThreads || tid < BN * 2) {
       const int col = tid >> 1;
+      const float scale = scale_value(v.scale, kFold ? p.scale_type : kScaleE8m0);
+      const float zero = kE2m1 ? 0.f : w.zero ? (float)v.zero : 8.f;
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         *reinterpret_cast<bf16x8*>(to + kBytesA + (col >> 4) * 1024 +
                                    fragment(col & 15, 2 * (tid & 1) + h)) =
-            weights8<kE2m1, !kFold>(c[h], zero, scale);
+            weights8<kE2m1, !kFold>(v.c[h], zero, scale);
       if constexpr (kFold)
         if ((tid & 1) == 0) reinterpret_cast<float*>(to + kBytesA + kBytesW)[col] = scale;
     }
@@ -130,7 +158,7 @@ struct Tiles {
       // compiler, left alone, moves the folds behind the refill, whose branches end the
       // block, and holds (or spills) all sums until then: the empty asm statements want
       // each fold's result where it is.
-      constexpr int kAtOnce = 2, kGroups = kI * kJ / kAtOnce;
+      constexpr int kAtOnce = kJ % 2 ? 1 : 2, kGroups = kI * kJ / kAtOnce;
       f32x4 sum[2][kAtOnce];
       bf16x8 part[3];
 #pragma unroll
@@ -177,18 +205,11 @@ struct Tiles {
     }
   }
 
-  // During step t: the next one's values into the other buffer, and the loads of
-  // those behind it.
-  __device__ __forceinline__ void refill(int t, int steps) {
-    if (t + 1 < steps) convert((t + 1) & 1);
-    if (t + 2 < steps) load(t + 2);
-  }
-
   // Places begin .. end - 1, the first BM of them.
   __device__ __forceinline__ void run(const Epilogue& ep, int begin, int end) {
-    int* from_row = reinterpret_cast<int*>(lds + 2 * kStage);
-    int* to_row = from_row + BM;
-    if (tid < BM) {
+    int* from_row = rows;
+    int* to_row = rows + BM;
+    if (part_k == 0 && tid < BM) {
       const int place = min(begin + tid, end - 1);
       const int r = p.g.ia ? p.g.ia[place] : place, t = p.g.ic ? p.g.ic[place] : place;
       from_row[tid] = r >= 0 && r < p.g.rows_a ? r : -1;
@@ -198,30 +219,75 @@ struct Tiles {
 #pragma unroll
     for (int i = 0; i < kOctets; ++i) {
       const int r = from_row[(tid >> 2) + i * (kThreads / 4)];
-      a[i] = r >= 0 ? p.g.A + r * p.g.lda + 8 * (tid & 3) : nullptr;
+      // a row that is not there reads the first one; its sums are not used
+      a[i] = p.g.A + max(r, 0) * p.g.lda + 8 * (tid & 3);
     }
-    n = min(n0 + (tid >> 1), p.g.N - 1);   // columns past the last are not stored
+    // columns past the last are not stored; threads without a column load one too
+    n = min(n0 + (tid >> 1) % BN, p.g.N - 1);
     codes = w.codes + n * p.ldq + 8 * (tid & 1);
-    scale = 1.f;
-    zero = 8.f;
+    zeros = w.zero ? w.zero + n * p.ldz : codes;   // a byte that is there, for none
+    // whole steps of each group; none where A has no row at all
+    const int steps = p.g.rows_a > 0 ? (int)(K / (32 * KS)) : 0;
+    // Waves w and w + 4 share a SIMD.  One of them refills before it multiplies: its
+    // refill of a step stands behind the barrier of the step before, so that all waves
+    // run one loop and no path through it leaves loads out.
+    const int first = (__builtin_amdgcn_readfirstlane(threadIdx.x) >> 8 & 1) ^ 1;
+    const int last = steps - 1;
+    if (steps > 0) {
+      Values v0, v1;
+      load(v0, 0);
+      load(v1, min(1, last));
+#pragma unroll
+      for (int d = 1; d <= D; ++d) load(v[d % D], min(d + first, last));
+      convert(v0, 0);
+      if (first) convert(v1, 1);
+      __syncthreads();
+    }
 #pragma unroll
     for (int i = 0; i < kI; ++i)
 #pragma unroll
       for (int j = 0; j < kJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    const int steps = (int)((K + 31) / 32);
     if (steps > 0) {
-      load(0);
-      convert(0);
-      if (steps > 1) load(1);
-      __syncthreads();
-      const bool first = wave < kWaves / 2;   // converts first
-      for (int t = 0; t < steps; ++t) {
-        if (first) refill(t, steps);
-        multiply(t & 1);
-        if (!first) refill(t, steps);
-        __syncthreads();
+      for (int t = 0;;) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+          multiply(t & 1);
+          if (first) __syncthreads();
+          // the step behind the next one of this wave (past the last, that one again,
+          // which nobody reads) into its buffer, and the loads of the one D further
+          Values& next = v[(d + 1) % D];
+          convert(next, (t + first + 1) & 1);
+          load(next, min(t + first + 1 + D, last));
+          if (!first) __syncthreads();
+          if (++t == steps) goto done;   // (a break would lead back to the loop's head)
+        }
       }
+    done:
+      __syncthreads();
+    }
+    if (p.g.rows_a > 0 && K % (32 * KS) != 0) {
+      load_rest(v[0], steps);
+      convert(v[0], 0);
+      __syncthreads();
+      multiply(0);
+      __syncthreads();
+    }
+    if constexpr (KS > 1) {
+      // (the last step's barrier is behind all reads of the buffers)
+      constexpr int kVec = kI * kJ;
+      f32x4* sums = reinterpret_cast<f32x4*>(lds) + wave * kVec * 64 + lane;
+      if (part_k > 0) {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) sums[i * 64] = acc[i / kJ][i % kJ];
+      }
+      __syncthreads();
+      if (part_k > 0) return;
+      for (int g = 1; g < KS; ++g)
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)
+          acc[i / kJ][i % kJ] += *reinterpret_cast<f32x4*>(reinterpret_cast<char*>(sums + i * 64) +
+                                                           g * kBuffers);
     }
     const int wm = wave / kWavesN, wn = wave % kWavesN;
 #pragma unroll
@@ -244,41 +310,46 @@ struct Tiles {
   }
 };
 
-template <int BM, int BN, int WM, int WN, bool kE2m1, bool kFold>
-__global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN), BM* BN >= 256 * 256 ? 1 : 2)
+template <class T>
+__global__ void __launch_bounds__(T::kAllThreads, T::kLds > 80 * 1024 ? 1 : 2)
     q4_tiles_kernel(Q4Problem p, Epilogue ep, unsigned cap) {
-  using T = Tiles<BM, BN, WM, WN, kE2m1, kFold>;
   __shared__ __attribute__((aligned(16))) char lds[T::kLds];
-  const int across = (p.g.N + BN - 1) / BN;
-  RowTiles tiles{p.g.offsets, p.g.groups, p.g.rows, BM, (int)(threadIdx.x & 63), cap, 0};
+  const int across = (p.g.N + T::kBN - 1) / T::kBN;
+  RowTiles tiles{p.g.offsets, p.g.groups, p.g.rows, T::kBM, (int)(threadIdx.x & 63), cap, 0};
   const unsigned total = tiles.total() * (unsigned)across;
   const int id = xcd_position(tile_id(), total);
   if (id < 0) return;
   int group, begin, end;
   unsigned first;
   if (!tiles.find((unsigned)id / across, group, begin, end, first)) return;
-  const int at = begin + (int)((unsigned)id / across - first) * BM;
+  const int at = begin + (int)((unsigned)id / across - first) * T::kBM;
   Epilogue e = ep;
   if (e.bias) e.bias += group * p.g.sbias;
-  T tile(p, lds, group, (int)((unsigned)id % across) * BN);
-  tile.run(e, at, min(end, at + BM));
+  T tile(p, lds, group, (int)((unsigned)id % across) * T::kBN);
+  tile.run(e, at, min(end, at + T::kBM));
 }
 
-template <int BM, int BN, int WM, int WN, bool kE2m1, bool kFold>
+template <class T>
 hipError_t launch(const Q4Problem& p, const Epilogue& e, hipStream_t s) {
-  const int64_t rows = most_row_tiles(p.g.rows, p.g.groups, BM);
-  const int64_t grid = rows * ((p.g.N + BN - 1) / BN);
+  const int64_t rows = most_row_tiles(p.g.rows, p.g.groups, T::kBM);
+  const int64_t grid = rows * ((p.g.N + T::kBN - 1) / T::kBN);
   if (grid > INT64_C(0x7fffffff)) return hipErrorInvalidValue;
-  q4_tiles_kernel<BM, BN, WM, WN, kE2m1, kFold>
-      <<<tile_grid(grid), 64 * (BM / WM) * (BN / WN), 0, s>>>(p, e, (unsigned)rows);
+  q4_tiles_kernel<T><<<tile_grid(grid), T::kAllThreads, 0, s>>>(p, e, (unsigned)rows);
   return hipGetLastError();
 }
 
 template <bool kE2m1, bool kFold>
 hipError_t by_tile(const Q4Problem& p, const Epilogue& e, hipStream_t s) {
   const int64_t large = ((int64_t)p.g.rows / 256 + p.g.groups / 2) * ((p.g.N + 255) / 256);
-  if (large >= 192) return launch<256, 256, 64, 128, kE2m1, kFold>(p, e, s);
-  return launch<128, 128, 64, 64, kE2m1, kFold>(p, e, s);
+  static const int force = getenv("Q4_TILE") ? atoi(getenv("Q4_TILE")) : 0;
+  if (force == 1) return launch<Tiles<256, 256, 64, 128, 1, 1, kE2m1, kFold>>(p, e, s);
+  if (force == 2) return launch<Tiles<128, 128, 64, 64, 1, 2, kE2m1, kFold>>(p, e, s);
+  if (force == 3) return launch<Tiles<64, 64, 32, 32, 1, 4, kE2m1, kFold>>(p, e, s);
+  if (force == 4) return launch<Tiles<64, 64, 32, 32, 4, 2, kE2m1, kFold>>(p, e, s);
+  if (force == 5) return launch<Tiles<32, 64, 32, 32, 4, 4, kE2m1, kFold>>(p, e, s);
+  if (force == 6) return launch<Tiles<32, 32, 32, 32, 8, 2, kE2m1, kFold>>(p, e, s);
+  if (large >= 192) return launch<Tiles<256, 256, 64, 128, 1, 1, kE2m1, kFold>>(p, e, s);
+  return launch<Tiles<128, 128, 64, 64, 1, 2, kE2m1, kFold>>(p, e, s);
 }
 
 }  // namespace

@@ -29,36 +29,54 @@ __device__ __forceinline__ uint32_t high_halves(float a, float b) {
   return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
 }
 
-// Eight fp32 values as three times eight bf16 values (parts[0] the highest).  The
-// parts are cut off, not rounded: each remainder is exact and has the value's
-// sign, and nothing overflows.  A value that is not finite has itself as its first
-// part and zeros behind it.
+// Eight fp32 values as three times eight bf16 values (parts[0] the highest), each
+// rounded to nearest from what the parts before it leave: the remainders, formed two
+// at a time by the bf16 dot product that adds to an fp32 value, are exact (a part
+// below the smallest normal float counts as zero).  In octets with a value that is
+// not finite, or rounds to infinity, the parts are cut off instead of rounded, and a
+// value that is not finite has itself as its first part and zeros behind it.
 __device__ __forceinline__ void split8(const float (&x)[8], u32x4 (&parts)[3]) {
-  float y[8], h[8];
-  float probe = 0.f;
+  // (-1, 0) and (0, -1), in registers: as an inline constant the instruction takes
+  // -1 for the fp32 bits
+  uint32_t c0 = 0x0000bf80u, c1 = 0xbf800000u;
+  asm("" : "+v"(c0), "+v"(c1));
+  const bf16x2 low = __builtin_bit_cast(bf16x2, c0), high = __builtin_bit_cast(bf16x2, c1);
+  const bf16x2 none = {(__bf16)0.f, (__bf16)0.f};
+  float y[8], probe = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    y[i] = x[i];
-    probe = fmaf(x[i], 0.f, probe);   // NaN if any is not finite
-  }
-  const bool finite = probe == 0.f;
+  for (int i = 0; i < 8; ++i) y[i] = x[i];
 #pragma unroll
   for (int part = 0; part < 3; ++part) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = __uint_as_float(__float_as_uint(y[i]) & 0xffff0000u);
-    if (!finite) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t u = __float_as_uint(x[i]);
-        if ((u & 0x7f800000u) == 0x7f800000u)   // a NaN stays one with its low bits cut off
-          h[i] = part > 0 ? 0.f
-                          : __uint_as_float((u & 0xffff0000u) | ((u & 0x7fffffu) ? 0x400000u : 0u));
+    for (int i = 0; i < 4; ++i) {
+      const f32x2 two = {y[2 * i], y[2 * i + 1]};
+      const bf16x2 h = __builtin_convertvector(two, bf16x2);
+      parts[part][i] = __builtin_bit_cast(uint32_t, h);
+      if (part < 2) {
+        y[2 * i] = __builtin_amdgcn_fdot2_f32_bf16(h, low, y[2 * i], false);
+        y[2 * i + 1] = __builtin_amdgcn_fdot2_f32_bf16(h, high, y[2 * i + 1], false);
+      } else {
+        probe = __builtin_amdgcn_fdot2_f32_bf16(h, none, probe, false);   // NaN there: NaN
       }
     }
+  }
+  if (__builtin_expect(__ballot(probe != 0.f) != 0, 0)) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) parts[part][i] = high_halves(h[2 * i], h[2 * i + 1]);
+    for (int i = 0; i < 8; ++i) {
+      float v = x[i];
+      asm volatile("" : "+v"(v));   // keeps all of this in the branch
+      const uint32_t u = __float_as_uint(v);
+      const bool finite = (u & 0x7f800000u) != 0x7f800000u;
+      // a NaN stays one with its low bits cut off
+      uint32_t h = (u & 0xffff0000u) | (!finite && (u & 0x7fffffu) ? 0x400000u : 0u);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = y[i] - h[i];
+      for (int part = 0; part < 3; ++part) {
+        const uint32_t keep = i & 1 ? 0x0000ffffu : 0xffff0000u;
+        parts[part][i / 2] = (parts[part][i / 2] & keep) | (i & 1 ? h & 0xffff0000u : h >> 16);
+        v = finite ? v - __uint_as_float(h) : 0.f;
+        h = __float_as_uint(v) & 0xffff0000u;
+      }
+    }
   }
 }
 
@@ -94,30 +112,32 @@ __device__ __forceinline__ bf16x8 weights8(uint32_t x, float zero, float scale) 
   return __builtin_bit_cast(bf16x8, w);
 }
 
-// Entry i of the scales, as fp32.  e8m0 is the exponent of a power of two, 255 NaN.
-__device__ __forceinline__ float load_scale(const void* scale, int type, int64_t i) {
-  if (type == kScaleF32) return static_cast<const float*>(scale)[i];
-  if (type == kScaleF16) return (float)static_cast<const _Float16*>(scale)[i];
-  if (type == kScaleBf16)
-    return __uint_as_float((uint32_t) static_cast<const uint16_t*>(scale)[i] << 16);
-  const uint32_t e = static_cast<const uint8_t*>(scale)[i];
-  return __uint_as_float(e == 255 ? 0x7fc00000u : e == 0 ? 0x00400000u : e << 23);
+// Entry i of the scales as it is stored, and its value.  (Loads that are to stay in
+// flight must not be looked at: a conversion beside the load would wait for all.)
+__device__ __forceinline__ uint32_t load_scale(const void* scale, int type, int64_t i) {
+  if (type == kScaleF32) return static_cast<const uint32_t*>(scale)[i];
+  if (type == kScaleE8m0) return static_cast<const uint8_t*>(scale)[i];
+  return static_cast<const uint16_t*>(scale)[i];
+}
+__device__ __forceinline__ float scale_value(uint32_t bits, int type) {
+  if (type == kScaleF32) return __uint_as_float(bits);
+  if (type == kScaleF16) return (float)__builtin_bit_cast(_Float16, (uint16_t)bits);
+  if (type == kScaleBf16) return __uint_as_float(bits << 16);
+  // e8m0, the exponent of a power of two; 255 is NaN
+  return __uint_as_float(bits == 255 ? 0x7fc00000u : bits == 0 ? 0x00400000u : bits << 23);
 }
 
-// 32 consecutive codes of a row from k on (a multiple of 32); those past the last
-// are zeros and their bytes are not read.
-__device__ __forceinline__ u32x4 load_codes(const uint8_t* row, int64_t k, int64_t K) {
+// 32 codes of a row from k on (a multiple of 32) where they may pass its end: those
+// behind it are zeros and their bytes are not read.
+__device__ __forceinline__ u32x4 last_codes(const uint8_t* row, int64_t k, int64_t K) {
+  asm volatile("" ::: "memory");   // keeps these loads apart from whole ones
   u32x4 v = {0u, 0u, 0u, 0u};
-  if (k + 32 <= K) {
-    __builtin_memcpy(&v, row + k / 2, sizeof(v));
-  } else if (k < K) {
-    const int bytes = (int)(K - k + 1) / 2;
-    for (int i = 0; i < bytes; ++i) {
-      const uint32_t b = row[k / 2 + i];
+  const int bytes = k >= K ? 0 : k + 32 <= K ? 16 : (int)(K - k + 1) / 2;
+  for (int i = 0; i < bytes; ++i) {
+    const uint32_t b = row[k / 2 + i];
 #pragma unroll
-      for (int d = 0; d < 4; ++d)
-        if (i >> 2 == d) v[d] |= b << 8 * (i & 3);
-    }
+    for (int d = 0; d < 4; ++d)
+      if (i >> 2 == d) v[d] |= b << 8 * (i & 3);
   }
   return v;
 }
