@@ -197,7 +197,7 @@ int run_q4(int64_t rows, int64_t N, int64_t K, int64_t groups, const int32_t* of
   e.act = activation;
   // few rows in a group: bound by the read of the codes
   static const char* force = getenv("Q4_TILE");
-  const bool few = force ? atoi(force) == 0 : rows <= 24 * std::min(rows, groups);
+  const bool few = K >= 128 && (force ? atoi(force) == 0 : rows <= 24 * std::min(rows, groups));
   hipStream_t s = static_cast<hipStream_t>(stream);
   return launched(few ? gemmf32::launch_q4_few(p, e, s) : gemmf32::launch_q4_tiles(p, e, s));
 }

@@ -1,13 +1,19 @@
-// Products with 4-bit weights for few rows: tiles of up to 10 rows by 16 CT columns,
-// K split over the 8 waves of a workgroup.  Bound by the read of the codes.
+// Products with 4-bit weights for few rows and at least 128 k: tiles of up to 10
+// rows.  Bound by the read of the codes.
 //
 // The rows' three bf16 parts are the rows of the matrix instruction: row r's part
 // p is row 3 r + p, so that up to 5 rows of A take one instruction for 16 columns
-// by 32 k, up to 10 two.  The workgroup splits them once, into LDS
-// in the order of the fragments; each wave then takes every 8th chunk of 128 k of
-// the workgroup's columns, 16 bytes of codes a lane, and the waves' sums are added
-// in LDS in one order.
+// by 32 k, up to 10 two.  A workgroup of 8 waves splits its rows once, into LDS, and
+// goes through strips of columns with them (rows whose parts do not fit take K in
+// passes, for each strip anew).  A wave takes 16 columns and every kw-th chunk of 128
+// k, 16 bytes of codes a lane; the kw waves of a strip add their sums through LDS in
+// one order, and the 8 / kw others have the strips beside it (kw is 8 from five
+// chunks on, so that short K still has work for all waves).  Each wave has the codes
+// and scales of its next two chunks on the way into registers, whichever strip they
+// are of.
 #include "q4_common.h"
+
+#include <algorithm>
 
 namespace gemmf32 {
 namespace {
@@ -17,120 +23,143 @@ using namespace q4;
 constexpr int kWaves = 8, kThreads = kWaves * 64;
 constexpr int kRows = 10;            // rows of a tile, at most
 constexpr int kChunkK = 128;         // k of a chunk: four steps of 32
-// chunks whose parts are in LDS at once, by matrix instructions a step: at most
-// 64 KiB, so that two workgroups share a CU
-template <int RT>
-constexpr int kPass = 16 / RT;
-constexpr int kLdsBytes = 16 * 4 * 1024;
+constexpr int kAhead = 2;            // chunks on the way
+// two workgroups to a CU: the waves' sums (RT KiB a wave; in two buffers, so that a
+// strip takes one barrier, where that leaves the parts of 8 chunks room), then the
+// parts
+constexpr int kLdsBytes = 79 * 1024;
+constexpr int kSumBytes = 2 * kWaves * 1024;
 
-// Fragments of a step of 32 k: RT KiB; row q of the instruction's 16 and octet o of
-// the k are 16 bytes, rotated by the step and octet so that the threads that write
-// octets of one row spread over the banks.
-__device__ __forceinline__ int slot(int q, int octet, int step) {
-  return ((q + 4 * octet + step) & 15) + 16 * octet;
-}
-
-template <int CT, int NS>
-struct Item {   // a wave's chunk of its columns
-  u32x4 codes[CT];
-  uint32_t scale[CT][NS], zero[CT][NS];   // as they are stored
+// kScales: scales of a chunk (1 for groups of 128 and more), of kBytes bytes each.
+template <int kScales, int kBytes>
+struct Item {
+  u32x4 codes;
+  uint32_t scale[(kScales * kBytes + 3) / 4], zero;
 };
 
-// kRest: the chunk that passes the end of K, of which nothing behind a row's end is
-// read.  In whole chunks no branch leaves a load out and nothing looks at what is
-// loaded: they stay in flight while the chunk before is multiplied.
-template <int CT, bool kE2m1, int NS, bool kRest>
-__device__ __forceinline__ void fetch(const Q4Problem& p, const Weights& w, int chunk, int n0,
-                                      int lane, Item<CT, NS>& it) {
-  const int64_t K = p.g.K, k0 = (int64_t)chunk * kChunkK;
-#pragma unroll
-  for (int c = 0; c < CT; ++c) {
+static_assert((kLdsBytes - kSumBytes) / (3 * kRows * 256) >= 8, "8 chunks of a tile");
+
+template <int RT, bool kE2m1, int kScales, int kBytes>
+struct Few {
+  using It = Item<kScales, kBytes>;
+  const Q4Problem& p;
+  const Weights w;
+  const int64_t K, row_bytes, along;   // of a row: bytes of codes, scales
+  const int chunks;
+  const int tid, wave, lane;
+  int kw_log2, kwave, side;            // waves along K; this one's place there, and its strip's
+  int rows, R;                         // of the tile, and of parts
+  int pass;                            // chunks whose parts are in LDS at once
+  char *lds, *parts;
+  int* row_of;
+
+  __device__ __forceinline__ Few(const Q4Problem& p, int group, char* lds, int* row_of)
+      : p(p), w(p, group), K(p.g.K), row_bytes((p.g.K + 1) / 2),
+        along((((int64_t)p.g.K - 1) >> p.group_shift) + 1), chunks((p.g.K + kChunkK - 1) / kChunkK),
+        tid(threadIdx.x), wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)),
+        lane(threadIdx.x & 63), lds(lds), parts(lds + kSumBytes), row_of(row_of) {
+    kw_log2 = chunks > 4 ? 3 : chunks > 2 ? 2 : chunks - 1;
+    kwave = wave & ((1 << kw_log2) - 1);
+    side = wave >> kw_log2;
+  }
+
+  // Chunk `chunk` of the strip's columns into registers.  No branch leaves a load out and
+  // nothing looks at what is loaded: it stays in flight while others are multiplied.
+  // Where the row ends inside the chunk, its last 16 bytes (and last scales) are read,
+  // and moved into place by multiply().
+  __device__ __forceinline__ void fetch(It& it, int strip, int chunk) const {
+    const int64_t k0 = (int64_t)min(chunk, chunks - 1) * kChunkK;
     // columns past the last read the last row: their sums are not stored
-    const int64_t n = min(n0 + 16 * c + (lane & 15), p.g.N - 1);
+    const int64_t n =
+        min((((int64_t)strip << (3 - kw_log2)) + side) * 16 + (lane & 15), (int64_t)p.g.N - 1);
     const uint8_t* row = w.codes + n * p.ldq;
-    if constexpr (kRest)
-      it.codes[c] = last_codes(row, k0 + 32 * (lane >> 4), K);
-    else
-      __builtin_memcpy(&it.codes[c], row + k0 / 2 + 16 * (lane >> 4), sizeof(u32x4));
+    __builtin_memcpy(&it.codes, row + min(k0 / 2 + 16 * (lane >> 4), row_bytes - 16),
+                     sizeof(u32x4));
+    const int64_t at = min(k0 >> p.group_shift, along - kScales);
+    const char* scale = static_cast<const char*>(w.scale) + (w.scale0 + n * p.lds + at) * kBytes;
+    __builtin_memcpy(it.scale, scale, kScales * kBytes);
+    if constexpr (!kE2m1)
+      __builtin_memcpy(&it.zero, w.zero ? w.zero + n * p.ldz + at : row, kScales);
+  }
+
+  // Scale (or zero point) s of a chunk.
+  __device__ __forceinline__ static uint32_t field(const uint32_t* v, int s, int bytes) {
+    const uint32_t x = v[s * bytes / 4];
+    return bytes == 4 ? x : bytes == 2 ? (x >> 16 * (s & 1)) & 0xffffu : (x >> 8 * (s & 3)) & 0xffu;
+  }
+
+  // The last chunk of a K that is no multiple of 128, moved into place: codes and
+  // scales behind the row's last meet parts that are zero.
+  __device__ __forceinline__ void settle(It& it, int64_t k0) const {
+    const int64_t want = k0 / 2 + 16 * (lane >> 4);
+    const int by = (int)(want - min(want, row_bytes - 16));   // bytes, 16 and more: all behind
+    u32x4 v = it.codes;
 #pragma unroll
-    for (int i = 0; i < NS; ++i) {
-      const int64_t at = (kRest ? min(k0 + 32 * i, K - 1) : k0 + 32 * i) >> p.group_shift;
-      it.scale[c][i] = load_scale(w.scale, p.scale_type, w.scale0 + n * p.lds + at);
-      if constexpr (!kE2m1) it.zero[c][i] = w.zero ? w.zero[n * p.ldz + at] : 8;
+    for (int d = 0; d < 4; ++d) {
+      if (by >> 2 > d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = i < 3 ? v[i + 1] : 0u;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      it.codes[i] = __builtin_amdgcn_alignbyte(i < 3 ? v[i + 1] : 0u, v[i], by & 3);
+    if constexpr (kScales > 1) {
+      const int64_t at = k0 >> p.group_shift;
+      const int shift = (int)(at - min(at, along - kScales));
+      uint32_t s[kScales];
+#pragma unroll
+      for (int i = 0; i < kScales; ++i) {
+        s[i] = field(it.scale, kScales - 1, kBytes);
+#pragma unroll
+        for (int j = 0; j < kScales; ++j)
+          if (i + shift == j) s[i] = field(it.scale, j, kBytes);
+      }
+      uint32_t z = 0;
+#pragma unroll
+      for (int i = 0; i < (kScales * kBytes + 3) / 4; ++i) it.scale[i] = 0;
+#pragma unroll
+      for (int i = 0; i < kScales; ++i) {
+        it.scale[i * kBytes / 4] |= s[i] << 8 * (i * kBytes % 4);
+        z |= ((it.zero >> 8 * min(i + shift, kScales - 1)) & 0xffu) << 8 * i;
+      }
+      if constexpr (!kE2m1) it.zero = z;
     }
   }
-}
 
-// One chunk of a wave: parts are those of its first step in LDS.
-template <int RT, int CT, bool kE2m1, int NS>
-__device__ __forceinline__ void multiply(const Q4Problem& p, const Item<CT, NS>& it, int step0,
-                                         const char* lds, int lane, f32x4 (&acc)[RT][CT]) {
-  u32x4 steps[CT];
+  // acc += this wave's chunk, whose parts begin at step step0 of those in LDS.
+  __device__ __forceinline__ void multiply(It it, int chunk, int step0, f32x4 (&acc)[RT]) const {
+    const int64_t k0 = (int64_t)chunk * kChunkK;
+    if (k0 + kChunkK > K) settle(it, k0);
+    const u32x4 codes = by_steps(it.codes);
+    f32x4 sum[RT];
 #pragma unroll
-  for (int c = 0; c < CT; ++c) steps[c] = by_steps(it.codes[c]);
-  f32x4 sum[RT][CT];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    bf16x8 a[RT];
-#pragma unroll
-    for (int t = 0; t < RT; ++t)
-      a[t] = *reinterpret_cast<const bf16x8*>(
-          lds + (((step0 + i) * RT + t) * 64 + slot(lane & 15, lane >> 4, step0 + i)) * 16);
-#pragma unroll
-    for (int c = 0; c < CT; ++c) {
-      const int s = NS == 1 ? 0 : i;
-      const bf16x8 b = weights8<kE2m1, false>(steps[c][i], kE2m1 ? 0.f : (float)it.zero[c][s], 1.f);
+    for (int i = 0; i < 4; ++i) {
+      constexpr int kPer = 4 / kScales;   // steps of a scale
+      const int s = i / kPer;
+      const float zero = kE2m1 ? 0.f : w.zero ? (float)field(&it.zero, s, 1) : 8.f;
+      const bf16x8 b = weights8<kE2m1, false>(codes[i], zero, 1.f);
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
+        // (rows behind the parts' last read that one: their sums are not used)
+        const int q = min(16 * t + (lane & 15), R - 1);
+        const bf16x8 a = *reinterpret_cast<const bf16x8*>(
+            parts + (((step0 + i) * 4 + (lane >> 4)) * R + q) * 16);
         const f32x4 none = {0.f, 0.f, 0.f, 0.f};
-        sum[t][c] = mfma16(a[t], b, NS == 1 && i > 0 ? sum[t][c] : none);
+        sum[t] = mfma16(a, b, i % kPer ? sum[t] : none);
+      }
+      if (i % kPer == kPer - 1) {
+        const float scale = scale_value(field(it.scale, s, kBytes),
+                                        kBytes == 4 ? kScaleF32 : kBytes == 1 ? kScaleE8m0
+                                                                              : p.scale_type);
+#pragma unroll
+        for (int t = 0; t < RT; ++t) acc[t] += sum[t] * scale;
       }
     }
-    if (NS == 4 || i == 3) {
-#pragma unroll
-      for (int c = 0; c < CT; ++c) {
-        const float scale = scale_value(it.scale[c][NS == 1 ? 0 : i], p.scale_type);
-#pragma unroll
-        for (int t = 0; t < RT; ++t) acc[t][c] += sum[t][c] * scale;
-      }
-    }
-    __builtin_amdgcn_sched_barrier(0);   // else all steps' weights are converted first
   }
-}
 
-// One tile of `rows` rows, places first .. first + rows - 1.
-template <int RT, int CT, bool kE2m1, int NS>
-__device__ void tile(const Q4Problem& p, const Epilogue& ep, const Weights& w, int group,
-                     int first, int rows, int n0, char* lds, int* row_of) {
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-  const int64_t K = p.g.K;
-  const int chunks = (int)((K + kChunkK - 1) / kChunkK);
-  if (tid < rows) {
-    const int place = first + tid;
-    const int r = p.g.ia ? p.g.ia[place] : place;
-    row_of[tid] = r >= 0 && r < p.g.rows_a ? r : -1;
-  }
-  f32x4 acc[RT][CT];
-#pragma unroll
-  for (int t = 0; t < RT; ++t)
-#pragma unroll
-    for (int c = 0; c < CT; ++c) acc[t][c] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-  // whole chunks; a part of one behind them is the wave's whose turn it would be
-  const int whole = (int)(K / kChunkK);
-  // chunks on the way into registers: as many as a wave has in a pass
-  constexpr int kAhead = 1;
-  Item<CT, NS> ahead[kAhead];
-  int chunk = wave;
-  if (whole > 0) {
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-      fetch<CT, kE2m1, NS, false>(p, w, min(chunk + i * kWaves, whole - 1), n0, lane, ahead[i]);
-  }
-  const unsigned inverse = (65536 + rows - 1) / rows;   // u / rows for u below 65536 / 16
-  for (int base = 0; base < chunks; base += kPass<RT>) {
-    const int here = min(kPass<RT>, chunks - base);
-    __syncthreads();   // row_of is there; the parts of the pass before are used
+  // The parts of the chunks base .. base + here - 1: octet o, row q at (o R + q) 16.
+  __device__ __forceinline__ void stage(int base, int here) const {
+    const unsigned inverse = (65536 + rows - 1) / rows;   // u / rows for u below 65536 / 16
     for (int u = tid; u < rows * here * (kChunkK / 8); u += kThreads) {
       const int octet = (int)((unsigned)u * inverse >> 16), r = u - octet * rows;
       const int64_t k = (int64_t)base * kChunkK + 8 * octet;
@@ -148,105 +177,172 @@ __device__ void tile(const Q4Problem& p, const Epilogue& ep, const Weights& w, i
             if (k + i < K) x[i] = a[i];
         }
       }
-      u32x4 parts[3];
-      split8(x, parts);
-      const int step = octet >> 2;
+      u32x4 split[3];
+      split8(x, split);
 #pragma unroll
-      for (int part = 0; part < 3; ++part) {
-        const int q = 3 * r + part;
-        *reinterpret_cast<u32x4*>(lds + ((step * RT + (q >> 4)) * 64 +
-                                         slot(q & 15, octet & 3, step)) * 16) = parts[part];
-      }
-    }
-    __syncthreads();
-    const int to = min(base + here, whole);
-    while (chunk < to) {
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        if (chunk >= to) break;
-        multiply<RT, CT, kE2m1, NS>(p, ahead[i], (chunk - base) * 4, lds, lane, acc);
-        fetch<CT, kE2m1, NS, false>(p, w, min(chunk + kAhead * kWaves, whole - 1), n0, lane,
-                                    ahead[i]);
-        chunk += kWaves;
-      }
-    }
-    if (whole < chunks && base + here == chunks && wave == whole % kWaves) {
-      Item<CT, NS> rest;
-      fetch<CT, kE2m1, NS, true>(p, w, whole, n0, lane, rest);
-      multiply<RT, CT, kE2m1, NS>(p, rest, (whole - base) * 4, lds, lane, acc);
+      for (int part = 0; part < 3; ++part)
+        *reinterpret_cast<u32x4*>(parts + (octet * R + 3 * r + part) * 16) = split[part];
     }
   }
-  __syncthreads();
-  // the waves' sums: [wave][row of the instruction][column]
-  float* red = reinterpret_cast<float*>(lds);
+
+  // The waves' sums of a strip added and stored; buffer 0 and 1 in turn.
+  __device__ __forceinline__ void store(const Epilogue& ep, int first, int strip, int buffer,
+                                        f32x4 (&acc)[RT]) const {
+    float* red = reinterpret_cast<float*>(lds) + (RT == 1 ? buffer * (kSumBytes / 8) : 0);
 #pragma unroll
-  for (int t = 0; t < RT; ++t)
-#pragma unroll
-    for (int c = 0; c < CT; ++c)
+    for (int t = 0; t < RT; ++t)
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        red[((wave * RT + t) * 16 + 4 * (lane >> 4) + r) * (16 * CT) + 16 * c + (lane & 15)] =
-            acc[t][c][r];
-  __syncthreads();
-  Epilogue e = ep;
-  if (e.bias) e.bias += group * p.g.sbias;
-  for (int u = tid; u < rows * 16 * CT; u += kThreads) {
-    const int r = u / (16 * CT), n = u % (16 * CT);
-    float v = 0.f;
-    for (int wv = 0; wv < kWaves; ++wv)
+        red[((wave * RT + t) * 16 + 4 * (lane >> 4) + r) * 16 + (lane & 15)] = acc[t][r];
+    __syncthreads();
+    const int kw = 1 << kw_log2, wide = 16 * kWaves >> kw_log2;   // columns of the strip
+    for (int u = tid; u < rows * wide; u += kThreads) {
+      const int r = u / wide, c = u % wide;
+      float v = 0.f;
+      for (int i = 0; i < kw; ++i)
 #pragma unroll
-      for (int part = 0; part < 3; ++part) {
-        v += red[((wv * RT * 16) + 3 * r + part) * (16 * CT) + n];
+        for (int part = 0; part < 3; ++part)
+          v += red[((((c >> 4) << kw_log2) + i) * RT * 16 + 3 * r + part) * 16 + (c & 15)];
+      const int place = first + r;
+      const int to = p.g.ic ? p.g.ic[place] : place;
+      const int64_t n = (int64_t)strip * wide + c;
+      if (n < p.g.N && to >= 0 && to < p.g.rows_c) {
+        float* out = p.g.C + to * p.g.ldc + n;
+        *out = epilogue_apply(ep, row_of[r] >= 0 ? v : 0.f, out, n);
       }
-    const int place = first + r;
-    const int to = p.g.ic ? p.g.ic[place] : place;
-    if (n0 + n < p.g.N && to >= 0 && to < p.g.rows_c) {
-      float* c = p.g.C + to * p.g.ldc + n0 + n;
-      *c = epilogue_apply(e, row_of[r] >= 0 ? v : 0.f, c, n0 + n);
+    }
+    if (RT > 1) __syncthreads();
+  }
+
+  // Places first .. first + rows - 1, every step-th strip from `strip` on.
+  __device__ __forceinline__ void run(const Epilogue& ep, int first, int rows_, int strip,
+                                      int step, int strips) {
+    rows = rows_;
+    R = 3 * rows;
+    __syncthreads();   // the tile before is done with LDS
+    if (tid < rows) {
+      const int place = first + tid;
+      const int r = p.g.ia ? p.g.ia[place] : place;
+      row_of[tid] = r >= 0 && r < p.g.rows_a ? r : -1;
+    }
+    const int kw = 1 << kw_log2;
+    pass = min(chunks, (kLdsBytes - kSumBytes) / (R * 256) & ~7);
+    const int passes = (chunks + pass - 1) / pass;
+    // positions: (strip, first chunk of the pass, this wave's place in it)
+    struct Position {
+      int strip, base, at;
+    };
+    auto advance = [&](Position& x) {
+      x.at += kw;
+      if (x.at >= min(pass, chunks - x.base)) {
+        x.at = 0;
+        x.base += pass;
+        if (x.base >= chunks) {
+          x.base = 0;
+          x.strip += step;
+        }
+      }
+    };
+    It items[kAhead];
+    Position now{strip, 0, 0}, ahead = now;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      fetch(items[i], ahead.strip, ahead.base + ahead.at + kwave);
+      advance(ahead);
+    }
+    f32x4 acc[RT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    bool staged = false;
+    int buffer = 0;
+    for (;;) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (now.at == 0 && !staged) {
+          __syncthreads();   // row_of is there; the pass before is used
+          stage(now.base, min(pass, chunks - now.base));
+          __syncthreads();
+          staged = passes == 1;
+        }
+        const int chunk = now.base + now.at + kwave;
+        if (now.at + kwave < min(pass, chunks - now.base))
+          multiply(items[i], chunk, (now.at + kwave) * 4, acc);
+        fetch(items[i], ahead.strip, ahead.base + ahead.at + kwave);
+        advance(ahead);
+        const int was = now.strip;
+        advance(now);
+        if (now.strip != was) {
+          store(ep, first, was, buffer, acc);
+          buffer ^= 1;
+#pragma unroll
+          for (int t = 0; t < RT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+          if (now.strip >= strips) return;
+        }
+      }
     }
   }
-  __syncthreads();
-}
+};
 
-template <int CT, bool kE2m1, int NS>
+template <bool kE2m1, int kScales, int kBytes>
 __global__ void __launch_bounds__(kThreads, 4) q4_few_kernel(Q4Problem p, Epilogue ep) {
   __shared__ __attribute__((aligned(16))) char lds[kLdsBytes];
   __shared__ int row_of[kRows];
   const int group = blockIdx.y;
   int begin, end;
   group_span(p.g.offsets, group, p.g.rows, begin, end);
-  const Weights w(p, group);
   // row tiles of one size, along the grid's z and, where there are more, in turn
   const int tiles = (end - begin + kRows - 1) / kRows;
-  const int each = tiles > 0 ? (end - begin + tiles - 1) / tiles : 0;
-  for (int64_t n0 = (int64_t)blockIdx.x * 16 * CT; n0 < p.g.N; n0 += (int64_t)gridDim.x * 16 * CT)
-    for (int i = blockIdx.z; i < tiles; i += gridDim.z) {
-      const int first = begin + i * each, rows = min(each, end - first);
-      if (rows <= 0) break;
-      if (rows <= 5)
-        tile<1, CT, kE2m1, NS>(p, ep, w, group, first, rows, (int)n0, lds, row_of);
-      else
-        tile<2, CT, kE2m1, NS>(p, ep, w, group, first, rows, (int)n0, lds, row_of);
+  if (tiles == 0) return;
+  const int each = (end - begin + tiles - 1) / tiles;
+  if (ep.bias) ep.bias += group * p.g.sbias;
+  for (int i = blockIdx.z; i < tiles; i += gridDim.z) {
+    const int first = begin + i * each, rows = min(each, end - first);
+    if (rows <= 0) break;
+    if (rows <= 5) {
+      Few<1, kE2m1, kScales, kBytes> few(p, group, lds, row_of);
+      const int wide = 16 * kWaves >> few.kw_log2;
+      few.run(ep, first, rows, blockIdx.x, gridDim.x, (int)(((int64_t)p.g.N + wide - 1) / wide));
+    } else {
+      Few<2, kE2m1, kScales, kBytes> few(p, group, lds, row_of);
+      const int wide = 16 * kWaves >> few.kw_log2;
+      few.run(ep, first, rows, blockIdx.x, gridDim.x, (int)(((int64_t)p.g.N + wide - 1) / wide));
     }
+  }
 }
 
-template <int CT, bool kE2m1>
+template <bool kE2m1, int kScales, int kBytes>
 hipError_t launch(const Q4Problem& p, const Epilogue& e, hipStream_t s) {
   const int tiles = p.g.offsets ? 1 : (p.g.rows + kRows - 1) / kRows;
-  const int strips = (p.g.N + 16 * CT - 1) / (16 * CT);
-  const dim3 grid((unsigned)(strips < kGridX ? strips : kGridX), (unsigned)p.g.groups,
+  const int chunks = (p.g.K + kChunkK - 1) / kChunkK;
+  const int wide = 16 * (chunks > 4 ? 1 : chunks > 2 ? 2 : 8 >> (chunks - 1));
+  const int64_t strips = ((int64_t)p.g.N + wide - 1) / wide;
+  // two workgroups a CU, each with strips enough
+  const int64_t most = std::max((int64_t)1, 512 / ((int64_t)p.g.groups * tiles));
+  const int64_t each = (strips + most - 1) / most;
+  const dim3 grid((unsigned)((strips + each - 1) / each), (unsigned)p.g.groups,
                   (unsigned)(tiles < 1024 ? tiles : 1024));
-  if (p.group_shift >= 7)
-    q4_few_kernel<CT, kE2m1, 1><<<grid, kThreads, 0, s>>>(p, e);
-  else
-    q4_few_kernel<CT, kE2m1, 4><<<grid, kThreads, 0, s>>>(p, e);
+  q4_few_kernel<kE2m1, kScales, kBytes><<<grid, kThreads, 0, s>>>(p, e);
   return hipGetLastError();
+}
+
+template <bool kE2m1, int kScales>
+hipError_t by_type(const Q4Problem& p, const Epilogue& e, hipStream_t s) {
+  if (p.scale_type == kScaleF32) return launch<kE2m1, kScales, 4>(p, e, s);
+  if (p.scale_type == kScaleE8m0) return launch<kE2m1, kScales, 1>(p, e, s);
+  return launch<kE2m1, kScales, 2>(p, e, s);
+}
+template <bool kE2m1>
+hipError_t by_group(const Q4Problem& p, const Epilogue& e, hipStream_t s) {
+  if (p.group_shift == 5) return by_type<kE2m1, 4>(p, e, s);
+  if (p.group_shift == 6) return by_type<kE2m1, 2>(p, e, s);
+  return by_type<kE2m1, 1>(p, e, s);
 }
 
 }  // namespace
 
 hipError_t launch_q4_few(const Q4Problem& p, const Epilogue& e, hipStream_t s) {
-  return p.e2m1 ? launch<2, true>(p, e, s) : launch<2, false>(p, e, s);
+  if (p.g.K < kChunkK) return hipErrorInvalidValue;
+  return p.e2m1 ? by_group<true>(p, e, s) : by_group<false>(p, e, s);
 }
 
 }  // namespace gemmf32
