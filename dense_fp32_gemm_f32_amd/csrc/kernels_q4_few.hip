@@ -20,14 +20,14 @@ namespace {
 
 using namespace q4;
 
-constexpr int kWaves = 8, kThreads = kWaves * 64;
-constexpr int kRows = 10;            // rows of a tile, at most
+constexpr int kWaves = 16, kWavesLog2 = 4, kThreads = kWaves * 64;
+constexpr int kRows = 8;             // rows of a tile, at most
 constexpr int kChunkK = 128;         // k of a chunk: four steps of 32
 constexpr int kAhead = 2;            // chunks on the way
 // two workgroups to a CU: the waves' sums (RT KiB a wave; in two buffers, so that a
 // strip takes one barrier, where that leaves the parts of 8 chunks room), then the
 // parts
-constexpr int kLdsBytes = 79 * 1024;
+constexpr int kLdsBytes = 158 * 1024;
 constexpr int kSumBytes = 2 * kWaves * 1024;
 
 // kScales: scales of a chunk (1 for groups of 128 and more), of kBytes bytes each.
@@ -37,49 +37,72 @@ struct Item {
   uint32_t scale[(kScales * kBytes + 3) / 4], zero;
 };
 
-static_assert((kLdsBytes - kSumBytes) / (3 * kRows * 256) >= 8, "8 chunks of a tile");
+static_assert((kLdsBytes - kSumBytes) / (3 * kRows * 256) >= kWaves, "a chunk for every wave");
+
+// Waves along K, as a power of two: so many that a workgroup on each CU has columns
+// for its waves, and no more than there are chunks.
+__host__ __device__ inline int waves_along_k(const Q4Problem& p) {
+  const int64_t chunks = ((int64_t)p.g.K + kChunkK - 1) / kChunkK;
+  const int64_t columns = ((int64_t)p.g.N + 15) / 16 * p.g.groups;
+  int log2 = 0;
+  while (log2 < kWavesLog2 && (columns << log2) < 256 * kWaves && (INT64_C(1) << log2) < chunks)
+    ++log2;
+  return log2;
+}
 
 template <int RT, bool kE2m1, int kScales, int kBytes>
 struct Few {
   using It = Item<kScales, kBytes>;
   const Q4Problem& p;
   const Weights w;
-  const int64_t K, row_bytes, along;   // of a row: bytes of codes, scales
-  const int chunks;
+  const int64_t K;
+  const int row_bytes, along, chunks;   // of a row: bytes of codes, scales, chunks
   const int tid, wave, lane;
   int kw_log2, kwave, side;            // waves along K; this one's place there, and its strip's
   int rows, R;                         // of the tile, and of parts
   int pass;                            // chunks whose parts are in LDS at once
   char *lds, *parts;
-  int* row_of;
+  int *row_of, *row_to;   // rows of A and C, -1: none
 
   __device__ __forceinline__ Few(const Q4Problem& p, int group, char* lds, int* row_of)
-      : p(p), w(p, group), K(p.g.K), row_bytes((p.g.K + 1) / 2),
-        along((((int64_t)p.g.K - 1) >> p.group_shift) + 1), chunks((p.g.K + kChunkK - 1) / kChunkK),
+      : p(p), w(p, group), K(p.g.K), row_bytes((int)(((int64_t)p.g.K + 1) / 2)),
+        along((int)(((int64_t)p.g.K - 1) >> p.group_shift) + 1),
+        chunks((int)(((int64_t)p.g.K + kChunkK - 1) / kChunkK)),
         tid(threadIdx.x), wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)),
-        lane(threadIdx.x & 63), lds(lds), parts(lds + kSumBytes), row_of(row_of) {
-    kw_log2 = chunks > 4 ? 3 : chunks > 2 ? 2 : chunks - 1;
+        lane(threadIdx.x & 63), lds(lds), parts(lds + kSumBytes), row_of(row_of), row_to(row_of + kRows) {
+    kw_log2 = waves_along_k(p);
     kwave = wave & ((1 << kw_log2) - 1);
     side = wave >> kw_log2;
   }
 
-  // Chunk `chunk` of the strip's columns into registers.  No branch leaves a load out and
-  // nothing looks at what is loaded: it stays in flight while others are multiplied.
-  // Where the row ends inside the chunk, its last 16 bytes (and last scales) are read,
-  // and moved into place by multiply().
-  __device__ __forceinline__ void fetch(It& it, int strip, int chunk) const {
-    const int64_t k0 = (int64_t)min(chunk, chunks - 1) * kChunkK;
+  // Where a lane's column of a strip begins: its codes, scales and zero points.
+  struct Row {
+    const uint8_t *codes, *zero;
+    const char* scale;
+  };
+  __device__ __forceinline__ Row row(int strip) const {
     // columns past the last read the last row: their sums are not stored
     const int64_t n =
-        min((((int64_t)strip << (3 - kw_log2)) + side) * 16 + (lane & 15), (int64_t)p.g.N - 1);
-    const uint8_t* row = w.codes + n * p.ldq;
-    __builtin_memcpy(&it.codes, row + min(k0 / 2 + 16 * (lane >> 4), row_bytes - 16),
-                     sizeof(u32x4));
-    const int64_t at = min(k0 >> p.group_shift, along - kScales);
-    const char* scale = static_cast<const char*>(w.scale) + (w.scale0 + n * p.lds + at) * kBytes;
-    __builtin_memcpy(it.scale, scale, kScales * kBytes);
-    if constexpr (!kE2m1)
-      __builtin_memcpy(&it.zero, w.zero ? w.zero + n * p.ldz + at : row, kScales);
+        min((((int64_t)strip << (kWavesLog2 - kw_log2)) + side) * 16 + (lane & 15),
+            (int64_t)p.g.N - 1);
+    Row r;
+    r.codes = w.codes + n * p.ldq;
+    r.scale = static_cast<const char*>(w.scale) + (w.scale0 + n * p.lds) * kBytes;
+    r.zero = w.zero ? w.zero + n * p.ldz : r.codes;   // bytes that are there, for none
+    return r;
+  }
+
+  // A chunk into registers.  No branch leaves a load out and nothing looks at what is
+  // loaded: it stays in flight while others are multiplied.  Where the row ends inside
+  // the chunk, its last 16 bytes (and last scales) are read, and moved into place by
+  // multiply().
+  __device__ __forceinline__ void fetch(It& it, const Row& r, int chunk) const {
+    chunk = min(chunk, chunks - 1);
+    const int at = min(chunk * (kChunkK / 32) >> (p.group_shift - 5), along - kScales);
+    __builtin_memcpy(&it.codes, r.codes + min(chunk * (kChunkK / 2) + 16 * (lane >> 4),
+                                              row_bytes - 16), sizeof(u32x4));
+    __builtin_memcpy(it.scale, r.scale + (int64_t)at * kBytes, kScales * kBytes);
+    if constexpr (!kE2m1) __builtin_memcpy(&it.zero, r.zero + at, kScales);
   }
 
   // Scale (or zero point) s of a chunk.
@@ -92,7 +115,7 @@ struct Few {
   // scales behind the row's last meet parts that are zero.
   __device__ __forceinline__ void settle(It& it, int64_t k0) const {
     const int64_t want = k0 / 2 + 16 * (lane >> 4);
-    const int by = (int)(want - min(want, row_bytes - 16));   // bytes, 16 and more: all behind
+    const int by = (int)(want - min(want, (int64_t)row_bytes - 16));   // bytes, 16 and more: all behind
     u32x4 v = it.codes;
 #pragma unroll
     for (int d = 0; d < 4; ++d) {
@@ -105,7 +128,7 @@ struct Few {
       it.codes[i] = __builtin_amdgcn_alignbyte(i < 3 ? v[i + 1] : 0u, v[i], by & 3);
     if constexpr (kScales > 1) {
       const int64_t at = k0 >> p.group_shift;
-      const int shift = (int)(at - min(at, along - kScales));
+      const int shift = (int)(at - min(at, (int64_t)along - kScales));
       uint32_t s[kScales];
 #pragma unroll
       for (int i = 0; i < kScales; ++i) {
@@ -186,8 +209,10 @@ struct Few {
   }
 
   // The waves' sums of a strip added and stored; buffer 0 and 1 in turn.
-  __device__ __forceinline__ void store(const Epilogue& ep, int first, int strip, int buffer,
+  __device__ __forceinline__ void store(const Epilogue& ep, int strip, int buffer,
                                         f32x4 (&acc)[RT]) const {
+    const int kw = 1 << kw_log2, wide = 16 * kWaves >> kw_log2;   // columns of the strip
+    const int64_t n0 = (int64_t)strip * wide + tid % wide;   // this thread's column
     float* red = reinterpret_cast<float*>(lds) + (RT == 1 ? buffer * (kSumBytes / 8) : 0);
 #pragma unroll
     for (int t = 0; t < RT; ++t)
@@ -195,22 +220,19 @@ struct Few {
       for (int r = 0; r < 4; ++r)
         red[((wave * RT + t) * 16 + 4 * (lane >> 4) + r) * 16 + (lane & 15)] = acc[t][r];
     __syncthreads();
-    const int kw = 1 << kw_log2, wide = 16 * kWaves >> kw_log2;   // columns of the strip
-    for (int u = tid; u < rows * wide; u += kThreads) {
-      const int r = u / wide, c = u % wide;
-      float v = 0.f;
-      for (int i = 0; i < kw; ++i)
+    if (n0 < p.g.N)
+      for (int r = tid / wide; r < rows; r += kThreads / wide) {
+        const int c = tid % wide, to = row_to[r];
+        float v = 0.f;
+        for (int i = 0; i < kw; ++i)
 #pragma unroll
-        for (int part = 0; part < 3; ++part)
-          v += red[((((c >> 4) << kw_log2) + i) * RT * 16 + 3 * r + part) * 16 + (c & 15)];
-      const int place = first + r;
-      const int to = p.g.ic ? p.g.ic[place] : place;
-      const int64_t n = (int64_t)strip * wide + c;
-      if (n < p.g.N && to >= 0 && to < p.g.rows_c) {
-        float* out = p.g.C + to * p.g.ldc + n;
-        *out = epilogue_apply(ep, row_of[r] >= 0 ? v : 0.f, out, n);
+          for (int part = 0; part < 3; ++part)
+            v += red[((((c >> 4) << kw_log2) + i) * RT * 16 + 3 * r + part) * 16 + (c & 15)];
+        if (to >= 0) {
+          float* out = p.g.C + to * p.g.ldc + n0;
+          *out = epilogue_apply(ep, row_of[r] >= 0 ? v : 0.f, out, n0);
+        }
       }
-    }
     if (RT > 1) __syncthreads();
   }
 
@@ -224,9 +246,11 @@ struct Few {
       const int place = first + tid;
       const int r = p.g.ia ? p.g.ia[place] : place;
       row_of[tid] = r >= 0 && r < p.g.rows_a ? r : -1;
+      const int to = p.g.ic ? p.g.ic[place] : place;
+      row_to[tid] = to >= 0 && to < p.g.rows_c ? to : -1;
     }
     const int kw = 1 << kw_log2;
-    pass = min(chunks, (kLdsBytes - kSumBytes) / (R * 256) & ~7);
+    pass = min(chunks, (kLdsBytes - kSumBytes) / (R * 256) & -kWaves);
     const int passes = (chunks + pass - 1) / pass;
     // positions: (strip, first chunk of the pass, this wave's place in it)
     struct Position {
@@ -245,11 +269,15 @@ struct Few {
     };
     It items[kAhead];
     Position now{strip, 0, 0}, ahead = now;
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      fetch(items[i], ahead.strip, ahead.base + ahead.at + kwave);
+    Row row_ahead = row(strip);
+    auto fetch_next = [&](It& it) {
+      fetch(it, row_ahead, ahead.base + ahead.at + kwave);
+      const int was = ahead.strip;
       advance(ahead);
-    }
+      if (ahead.strip != was) row_ahead = row(ahead.strip);
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) fetch_next(items[i]);
     f32x4 acc[RT];
 #pragma unroll
     for (int t = 0; t < RT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -267,12 +295,11 @@ struct Few {
         const int chunk = now.base + now.at + kwave;
         if (now.at + kwave < min(pass, chunks - now.base))
           multiply(items[i], chunk, (now.at + kwave) * 4, acc);
-        fetch(items[i], ahead.strip, ahead.base + ahead.at + kwave);
-        advance(ahead);
+        fetch_next(items[i]);
         const int was = now.strip;
         advance(now);
         if (now.strip != was) {
-          store(ep, first, was, buffer, acc);
+          store(ep, was, buffer, acc);
           buffer ^= 1;
 #pragma unroll
           for (int t = 0; t < RT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -286,7 +313,7 @@ struct Few {
 template <bool kE2m1, int kScales, int kBytes>
 __global__ void __launch_bounds__(kThreads, 4) q4_few_kernel(Q4Problem p, Epilogue ep) {
   __shared__ __attribute__((aligned(16))) char lds[kLdsBytes];
-  __shared__ int row_of[kRows];
+  __shared__ int row_of[2 * kRows];
   const int group = blockIdx.y;
   int begin, end;
   group_span(p.g.offsets, group, p.g.rows, begin, end);
@@ -313,11 +340,10 @@ __global__ void __launch_bounds__(kThreads, 4) q4_few_kernel(Q4Problem p, Epilog
 template <bool kE2m1, int kScales, int kBytes>
 hipError_t launch(const Q4Problem& p, const Epilogue& e, hipStream_t s) {
   const int tiles = p.g.offsets ? 1 : (p.g.rows + kRows - 1) / kRows;
-  const int chunks = (p.g.K + kChunkK - 1) / kChunkK;
-  const int wide = 16 * (chunks > 4 ? 1 : chunks > 2 ? 2 : 8 >> (chunks - 1));
+  const int wide = 16 * kWaves >> waves_along_k(p);
   const int64_t strips = ((int64_t)p.g.N + wide - 1) / wide;
-  // two workgroups a CU, each with strips enough
-  const int64_t most = std::max((int64_t)1, 512 / ((int64_t)p.g.groups * tiles));
+  // a workgroup a CU, each with as many strips
+  const int64_t most = std::max((int64_t)1, 256 / ((int64_t)p.g.groups * tiles));
   const int64_t each = (strips + most - 1) / most;
   const dim3 grid((unsigned)((strips + each - 1) / each), (unsigned)p.g.groups,
                   (unsigned)(tiles < 1024 ? tiles : 1024));
