@@ -8,12 +8,12 @@
 
 #include <algorithm>
 #include <cmath>
-#include <cstdlib>
 #include <new>
 #include <vector>
 
 #include "experts_internal.h"
 #include "host_checks.h"
+#include "q4_routes.h"
 
 using gemmf32::Epilogue;
 using gemmf32::JoinProblem;
@@ -195,11 +195,9 @@ int run_q4(int64_t rows, int64_t N, int64_t K, int64_t groups, const int32_t* of
   e.beta = beta;
   e.bias = bias;
   e.act = activation;
-  // few rows in a group: bound by the read of the codes
-  static const char* force = getenv("Q4_TILE");
-  const bool few = K >= 128 && (force ? atoi(force) == 0 : rows <= 24 * std::min(rows, groups));
   hipStream_t s = static_cast<hipStream_t>(stream);
-  return launched(few ? gemmf32::launch_q4_few(p, e, s) : gemmf32::launch_q4_tiles(p, e, s));
+  return launched(gemmf32::q4_few(p) ? gemmf32::launch_q4_few(p, e, s)
+                                     : gemmf32::launch_q4_tiles(p, e, s));
 }
 
 }  // namespace

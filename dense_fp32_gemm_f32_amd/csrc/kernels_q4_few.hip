@@ -1,17 +1,20 @@
-// Products with 4-bit weights for few rows and at least 128 k: tiles of up to 10
-// rows.  Bound by the read of the codes.
+// Products with 4-bit weights for few rows (q4_routes.h) and at least 128 k: tiles of up
+// to 8 rows.  Bound by the read of the codes: one row of 8192 x 8192 takes 16 us (33.5 MB
+// of codes, 2.2 TB/s), 28672 x 8192 38 us (3.1 TB/s), where loads alone in the same order
+// take 33 us.
 //
 // The rows' three bf16 parts are the rows of the matrix instruction: row r's part
 // p is row 3 r + p, so that up to 5 rows of A take one instruction for 16 columns
-// by 32 k, up to 10 two.  A workgroup of 8 waves splits its rows once, into LDS, and
-// goes through strips of columns with them (rows whose parts do not fit take K in
-// passes, for each strip anew).  A wave takes 16 columns and every kw-th chunk of 128
-// k, 16 bytes of codes a lane; the kw waves of a strip add their sums through LDS in
-// one order, and the 8 / kw others have the strips beside it (kw is 8 from five
-// chunks on, so that short K still has work for all waves).  Each wave has the codes
-// and scales of its next two chunks on the way into registers, whichever strip they
-// are of.
+// by 32 k, up to 8 two.  A workgroup splits its rows once, into LDS, and goes through
+// strips of columns with them (rows whose parts do not fit take K in passes, for each
+// strip anew).  A wave takes 16 columns and every kw-th chunk of 128 k, 16 bytes of
+// codes a lane; the kw waves of a strip add their sums through LDS in one order, and
+// the 16 / kw others have the strips beside it.  Each wave has the codes and scales
+// of its next two chunks on the way into registers, whichever strip they are of
+// (four chunks were no faster).  With 8 waves a workgroup 8192 x 8192 took 19 us, as
+// fewer loads are on the way.
 #include "q4_common.h"
+#include "q4_routes.h"
 
 #include <algorithm>
 
@@ -24,9 +27,8 @@ constexpr int kWaves = 16, kWavesLog2 = 4, kThreads = kWaves * 64;
 constexpr int kRows = 8;             // rows of a tile, at most
 constexpr int kChunkK = 128;         // k of a chunk: four steps of 32
 constexpr int kAhead = 2;            // chunks on the way
-// two workgroups to a CU: the waves' sums (RT KiB a wave; in two buffers, so that a
-// strip takes one barrier, where that leaves the parts of 8 chunks room), then the
-// parts
+// the waves' sums (1 KiB a wave and 16 rows of parts), then the parts; one workgroup to
+// a CU
 constexpr int kLdsBytes = 158 * 1024;
 constexpr int kSumBytes = 2 * kWaves * 1024;
 
@@ -50,7 +52,7 @@ __host__ __device__ inline int waves_along_k(const Q4Problem& p) {
   return log2;
 }
 
-template <int RT, bool kE2m1, int kScales, int kBytes>
+template <int RT, int kForm, int kScales, int kBytes>
 struct Few {
   using It = Item<kScales, kBytes>;
   const Q4Problem& p;
@@ -88,7 +90,7 @@ struct Few {
     Row r;
     r.codes = w.codes + n * p.ldq;
     r.scale = static_cast<const char*>(w.scale) + (w.scale0 + n * p.lds) * kBytes;
-    r.zero = w.zero ? w.zero + n * p.ldz : r.codes;   // bytes that are there, for none
+    if constexpr (kForm == kIntZeros) r.zero = w.zero + n * p.ldz;
     return r;
   }
 
@@ -102,7 +104,7 @@ struct Few {
     __builtin_memcpy(&it.codes, r.codes + min(chunk * (kChunkK / 2) + 16 * (lane >> 4),
                                               row_bytes - 16), sizeof(u32x4));
     __builtin_memcpy(it.scale, r.scale + (int64_t)at * kBytes, kScales * kBytes);
-    if constexpr (!kE2m1) __builtin_memcpy(&it.zero, r.zero + at, kScales);
+    if constexpr (kForm == kIntZeros) __builtin_memcpy(&it.zero, r.zero + at, kScales);
   }
 
   // Scale (or zero point) s of a chunk.
@@ -143,24 +145,25 @@ struct Few {
 #pragma unroll
       for (int i = 0; i < kScales; ++i) {
         it.scale[i * kBytes / 4] |= s[i] << 8 * (i * kBytes % 4);
-        z |= ((it.zero >> 8 * min(i + shift, kScales - 1)) & 0xffu) << 8 * i;
+        if constexpr (kForm == kIntZeros)
+          z |= ((it.zero >> 8 * min(i + shift, kScales - 1)) & 0xffu) << 8 * i;
       }
-      if constexpr (!kE2m1) it.zero = z;
+      if constexpr (kForm == kIntZeros) it.zero = z;
     }
   }
 
   // acc += this wave's chunk, whose parts begin at step step0 of those in LDS.
   __device__ __forceinline__ void multiply(It it, int chunk, int step0, f32x4 (&acc)[RT]) const {
     const int64_t k0 = (int64_t)chunk * kChunkK;
-    if (k0 + kChunkK > K) settle(it, k0);
+    if (__builtin_expect(k0 + kChunkK > K, 0)) settle(it, k0);
     const u32x4 codes = by_steps(it.codes);
     f32x4 sum[RT];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       constexpr int kPer = 4 / kScales;   // steps of a scale
       const int s = i / kPer;
-      const float zero = kE2m1 ? 0.f : w.zero ? (float)field(&it.zero, s, 1) : 8.f;
-      const bf16x8 b = weights8<kE2m1, false>(codes[i], zero, 1.f);
+      const float zero = kForm == kIntZeros ? (float)field(&it.zero, s, 1) : 8.f;
+      const bf16x8 b = weights8<kForm, false>(codes[i], zero, 1.f);
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
         // (rows behind the parts' last read that one: their sums are not used)
@@ -310,7 +313,7 @@ struct Few {
   }
 };
 
-template <bool kE2m1, int kScales, int kBytes>
+template <int kForm, int kScales, int kBytes>
 __global__ void __launch_bounds__(kThreads, 4) q4_few_kernel(Q4Problem p, Epilogue ep) {
   __shared__ __attribute__((aligned(16))) char lds[kLdsBytes];
   __shared__ int row_of[2 * kRows];
@@ -326,18 +329,18 @@ __global__ void __launch_bounds__(kThreads, 4) q4_few_kernel(Q4Problem p, Epilog
     const int first = begin + i * each, rows = min(each, end - first);
     if (rows <= 0) break;
     if (rows <= 5) {
-      Few<1, kE2m1, kScales, kBytes> few(p, group, lds, row_of);
+      Few<1, kForm, kScales, kBytes> few(p, group, lds, row_of);
       const int wide = 16 * kWaves >> few.kw_log2;
       few.run(ep, first, rows, blockIdx.x, gridDim.x, (int)(((int64_t)p.g.N + wide - 1) / wide));
     } else {
-      Few<2, kE2m1, kScales, kBytes> few(p, group, lds, row_of);
+      Few<2, kForm, kScales, kBytes> few(p, group, lds, row_of);
       const int wide = 16 * kWaves >> few.kw_log2;
       few.run(ep, first, rows, blockIdx.x, gridDim.x, (int)(((int64_t)p.g.N + wide - 1) / wide));
     }
   }
 }
 
-template <bool kE2m1, int kScales, int kBytes>
+template <int kForm, int kScales, int kBytes>
 hipError_t launch(const Q4Problem& p, const Epilogue& e, hipStream_t s) {
   const int tiles = p.g.offsets ? 1 : (p.g.rows + kRows - 1) / kRows;
   const int wide = 16 * kWaves >> waves_along_k(p);
@@ -347,28 +350,30 @@ hipError_t launch(const Q4Problem& p, const Epilogue& e, hipStream_t s) {
   const int64_t each = (strips + most - 1) / most;
   const dim3 grid((unsigned)((strips + each - 1) / each), (unsigned)p.g.groups,
                   (unsigned)(tiles < 1024 ? tiles : 1024));
-  q4_few_kernel<kE2m1, kScales, kBytes><<<grid, kThreads, 0, s>>>(p, e);
+  q4_few_kernel<kForm, kScales, kBytes><<<grid, kThreads, 0, s>>>(p, e);
   return hipGetLastError();
 }
 
-template <bool kE2m1, int kScales>
+template <int kForm, int kScales>
 hipError_t by_type(const Q4Problem& p, const Epilogue& e, hipStream_t s) {
-  if (p.scale_type == kScaleF32) return launch<kE2m1, kScales, 4>(p, e, s);
-  if (p.scale_type == kScaleE8m0) return launch<kE2m1, kScales, 1>(p, e, s);
-  return launch<kE2m1, kScales, 2>(p, e, s);
+  if (p.scale_type == kScaleF32) return launch<kForm, kScales, 4>(p, e, s);
+  if (p.scale_type == kScaleE8m0) return launch<kForm, kScales, 1>(p, e, s);
+  return launch<kForm, kScales, 2>(p, e, s);
 }
-template <bool kE2m1>
+template <int kForm>
 hipError_t by_group(const Q4Problem& p, const Epilogue& e, hipStream_t s) {
-  if (p.group_shift == 5) return by_type<kE2m1, 4>(p, e, s);
-  if (p.group_shift == 6) return by_type<kE2m1, 2>(p, e, s);
-  return by_type<kE2m1, 1>(p, e, s);
+  if (p.group_shift == 5) return by_type<kForm, 4>(p, e, s);
+  if (p.group_shift == 6) return by_type<kForm, 2>(p, e, s);
+  return by_type<kForm, 1>(p, e, s);
 }
 
 }  // namespace
 
 hipError_t launch_q4_few(const Q4Problem& p, const Epilogue& e, hipStream_t s) {
+  static_assert(kQ4FewK == kChunkK, "a chunk at least");
   if (p.g.K < kChunkK) return hipErrorInvalidValue;
-  return p.e2m1 ? by_group<true>(p, e, s) : by_group<false>(p, e, s);
+  return p.e2m1 ? by_group<kE2m1>(p, e, s)
+                : p.zero ? by_group<kIntZeros>(p, e, s) : by_group<kInt8>(p, e, s);
 }
 
 }  // namespace gemmf32

@@ -13,7 +13,7 @@
 // column's scale.  A scale that is a power of two is put into the weights instead,
 // which stay bf16 values exactly, and the sums go straight on.
 #include "q4_common.h"
-#include <cstdlib>
+#include "q4_routes.h"
 #include <type_traits>
 
 namespace gemmf32 {
@@ -31,7 +31,7 @@ __device__ __forceinline__ int fragment(int r, int o) {
 // D: steps whose values are on the way into registers.
 // KS: groups of waves, each with every KS-th step and buffers of its own; the first
 // adds the others' sums to its own in order.
-template <int BM, int BN, int WM, int WN, int KS, int D, bool kE2m1, bool kFold>
+template <int BM, int BN, int WM, int WN, int KS, int D, int kForm, bool kFold>
 struct Tiles {
   static constexpr int kWavesN = BN / WN, kWaves = BM / WM * kWavesN, kThreads = 64 * kWaves;
   static constexpr int kBM = BM, kBN = BN, kAllThreads = KS * kThreads;
@@ -90,26 +90,31 @@ struct Tiles {
                                           : static_cast<const uint16_t*>(w.scale)[i];
     else
       v.scale = static_cast<const uint8_t*>(w.scale)[i];
-    if constexpr (!kE2m1) v.zero = zeros[at];
+    if constexpr (kForm == kIntZeros) v.zero = zeros[at];
   }
 
-  // The same for the part of K behind the whole steps: nothing behind a row's end is
-  // read.
+  // The same for the part of K behind the whole steps: k past the end reads the last
+  // one, and settle_rest() then makes A's values there zeros.
   __device__ __forceinline__ void load_rest(Values& v, int step) {
-    const int64_t k0 = ((int64_t)step * KS + part_k) * 32, left = K - k0;
+    const int64_t k0 = ((int64_t)step * KS + part_k) * 32, ka = k0 + 8 * (tid & 3),
+                  kw = k0 + 16 * (tid & 1);
 #pragma unroll
     for (int i = 0; i < kOctets; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int k = 8 * (tid & 3) + j;
-        v.x[i][j] = k < left ? a[i][k0 + j] : 0.f;
-      }
-    uint64_t u = 0;
-    for (int i = 0; i < 8 && 16 * (tid & 1) + 2 * i < left; ++i)
-      u |= (uint64_t)codes[k0 / 2 + i] << 8 * i;
-    v.c[0] = (uint32_t)u;
-    v.c[1] = (uint32_t)(u >> 32);
+      for (int j = 0; j < 8; ++j) v.x[i][j] = a[i][min(ka + j, K - 1) - 8 * (tid & 3)];
+    uint8_t bytes[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) bytes[i] = codes[min(kw + 2 * i, K - 1) / 2 - 8 * (tid & 1)];
+    __builtin_memcpy(v.c, bytes, sizeof(v.c));
     load_scales(v, min(k0, K - 1));
+  }
+  __device__ __forceinline__ void settle_rest(Values& v, int step) {
+    const int64_t ka = ((int64_t)step * KS + part_k) * 32 + 8 * (tid & 3);
+#pragma unroll
+    for (int i = 0; i < kOctets; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (ka + j >= K) v.x[i][j] = 0.f;
   }
 
   // The registers' values into a buffer.
@@ -128,12 +133,12 @@ struct Tiles {
     if (BN * 2 == kThreads || tid < BN * 2) {
       const int col = tid >> 1;
       const float scale = scale_value(v.scale, kFold ? p.scale_type : kScaleE8m0);
-      const float zero = kE2m1 ? 0.f : w.zero ? (float)v.zero : 8.f;
+      const float zero = kForm == kIntZeros ? (float)v.zero : 8.f;
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         *reinterpret_cast<bf16x8*>(to + kBytesA + (col >> 4) * 1024 +
                                    fragment(col & 15, 2 * (tid & 1) + h)) =
-            weights8<kE2m1, !kFold>(v.c[h], zero, scale);
+            weights8<kForm, !kFold>(v.c[h], zero, scale);
       if constexpr (kFold)
         if ((tid & 1) == 0) reinterpret_cast<float*>(to + kBytesA + kBytesW)[col] = scale;
     }
@@ -225,7 +230,7 @@ struct Tiles {
     // columns past the last are not stored; threads without a column load one too
     n = min(n0 + (tid >> 1) % BN, p.g.N - 1);
     codes = w.codes + n * p.ldq + 8 * (tid & 1);
-    zeros = w.zero ? w.zero + n * p.ldz : codes;   // a byte that is there, for none
+    if constexpr (kForm == kIntZeros) zeros = w.zero + n * p.ldz;
     // whole steps of each group; none where A has no row at all
     const int steps = p.g.rows_a > 0 ? (int)(K / (32 * KS)) : 0;
     // Waves w and w + 4 share a SIMD.  One of them refills before it multiplies: its
@@ -233,6 +238,10 @@ struct Tiles {
     // run one loop and no path through it leaves loads out.
     const int first = (__builtin_amdgcn_readfirstlane(threadIdx.x) >> 8 & 1) ^ 1;
     const int last = steps - 1;
+    // what is left of K; its loads go out before all others where there are registers
+    const bool rest = p.g.rows_a > 0 && K % (32 * KS) != 0;
+    Values behind;
+    if (D > 1 && rest) load_rest(behind, steps);
     if (steps > 0) {
       Values v0, v1;
       load(v0, 0);
@@ -266,9 +275,10 @@ struct Tiles {
     done:
       __syncthreads();
     }
-    if (p.g.rows_a > 0 && K % (32 * KS) != 0) {
-      load_rest(v[0], steps);
-      convert(v[0], 0);
+    if (rest) {
+      if constexpr (D == 1) load_rest(v[0], steps);
+      settle_rest(D > 1 ? behind : v[0], steps);
+      convert(D > 1 ? behind : v[0], 0);
       __syncthreads();
       multiply(0);
       __syncthreads();
@@ -338,26 +348,26 @@ hipError_t launch(const Q4Problem& p, const Epilogue& e, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <bool kE2m1, bool kFold>
+template <int kForm, bool kFold>
 hipError_t by_tile(const Q4Problem& p, const Epilogue& e, hipStream_t s) {
-  const int64_t large = ((int64_t)p.g.rows / 256 + p.g.groups / 2) * ((p.g.N + 255) / 256);
-  static const int force = getenv("Q4_TILE") ? atoi(getenv("Q4_TILE")) : 0;
-  if (force == 1) return launch<Tiles<256, 256, 64, 128, 1, 1, kE2m1, kFold>>(p, e, s);
-  if (force == 2) return launch<Tiles<128, 128, 64, 64, 1, 2, kE2m1, kFold>>(p, e, s);
-  if (force == 3) return launch<Tiles<64, 64, 32, 32, 1, 4, kE2m1, kFold>>(p, e, s);
-  if (force == 4) return launch<Tiles<64, 64, 32, 32, 4, 2, kE2m1, kFold>>(p, e, s);
-  if (force == 5) return launch<Tiles<32, 64, 32, 32, 4, 4, kE2m1, kFold>>(p, e, s);
-  if (force == 6) return launch<Tiles<32, 32, 32, 32, 8, 2, kE2m1, kFold>>(p, e, s);
-  if (large >= 192) return launch<Tiles<256, 256, 64, 128, 1, 1, kE2m1, kFold>>(p, e, s);
-  return launch<Tiles<128, 128, 64, 64, 1, 2, kE2m1, kFold>>(p, e, s);
+  switch (q4_tile(p)) {
+    case kTile256: return launch<Tiles<256, 256, 64, 128, 1, 1, kForm, kFold>>(p, e, s);
+    case kTile128: return launch<Tiles<128, 128, 64, 64, 2, 1, kForm, kFold>>(p, e, s);
+    case kTile64x128: return launch<Tiles<64, 128, 32, 64, 2, 2, kForm, kFold>>(p, e, s);
+    case kTile64: return launch<Tiles<64, 64, 32, 32, 4, 2, kForm, kFold>>(p, e, s);
+    case kTile32x64: return launch<Tiles<32, 64, 32, 32, 4, 4, kForm, kFold>>(p, e, s);
+    default: return launch<Tiles<32, 32, 32, 32, 8, 2, kForm, kFold>>(p, e, s);
+  }
 }
 
 }  // namespace
 
 hipError_t launch_q4_tiles(const Q4Problem& p, const Epilogue& e, hipStream_t s) {
   const bool fold = p.scale_type != kScaleE8m0;
-  if (p.e2m1) return fold ? by_tile<true, true>(p, e, s) : by_tile<true, false>(p, e, s);
-  return fold ? by_tile<false, true>(p, e, s) : by_tile<false, false>(p, e, s);
+  if (p.e2m1) return fold ? by_tile<kE2m1, true>(p, e, s) : by_tile<kE2m1, false>(p, e, s);
+  if (p.zero)
+    return fold ? by_tile<kIntZeros, true>(p, e, s) : by_tile<kIntZeros, false>(p, e, s);
+  return fold ? by_tile<kInt8, true>(p, e, s) : by_tile<kInt8, false>(p, e, s);
 }
 
 }  // namespace gemmf32

@@ -80,16 +80,19 @@ __device__ __forceinline__ void split8(const float (&x)[8], u32x4 (&parts)[3]) {
   }
 }
 
+// What codes stand for: int with the zero point 8, int with zero points, e2m1.
+enum Form { kInt8, kIntZeros, kE2m1 };
+
 // Eight weights from a dword of codes (the first k in its low bits), without their
 // scale, or with a scale that is a power of two (kScaled): bf16 values exactly.  int
 // codes: read as e4m3 with a scale of 2^9, the bytes 0 .. 15 are the values 0 .. 15
 // (the format is linear there), so that one instruction converts two; minus the
 // zero point they are whole numbers of at most 8 bits.
-template <bool kE2m1, bool kScaled>
+template <int kForm, bool kScaled>
 __device__ __forceinline__ bf16x8 weights8(uint32_t x, float zero, float scale) {
   u32x4 w;
   const float by = kScaled ? scale : 1.f;
-  if constexpr (kE2m1) {
+  if constexpr (kForm == kE2m1) {
     bf16x2 v[4];
     v[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, by, 0);
     v[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, by, 1);
@@ -125,21 +128,6 @@ __device__ __forceinline__ float scale_value(uint32_t bits, int type) {
   if (type == kScaleBf16) return __uint_as_float(bits << 16);
   // e8m0, the exponent of a power of two; 255 is NaN
   return __uint_as_float(bits == 255 ? 0x7fc00000u : bits == 0 ? 0x00400000u : bits << 23);
-}
-
-// 32 codes of a row from k on (a multiple of 32) where they may pass its end: those
-// behind it are zeros and their bytes are not read.
-__device__ __forceinline__ u32x4 last_codes(const uint8_t* row, int64_t k, int64_t K) {
-  asm volatile("" ::: "memory");   // keeps these loads apart from whole ones
-  u32x4 v = {0u, 0u, 0u, 0u};
-  const int bytes = k >= K ? 0 : k + 32 <= K ? 16 : (int)(K - k + 1) / 2;
-  for (int i = 0; i < bytes; ++i) {
-    const uint32_t b = row[k / 2 + i];
-#pragma unroll
-    for (int d = 0; d < 4; ++d)
-      if (i >> 2 == d) v[d] |= b << 8 * (i & 3);
-  }
-  return v;
 }
 
 // Lane group g (16 lanes) has dwords 0 .. 3 of codes 32 g + 0 .. 31; afterwards

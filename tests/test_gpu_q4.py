@@ -225,6 +225,23 @@ def test_large_and_small_values(gpu_lib):
         assert torch.equal(got[:5].cpu(), x[:, None].expand(5, 6))
 
 
+# rows x columns that reach each kernel (test_q4_routes_host.py asks the rules)
+KERNELS = {"few": (10, 1000), "32x32": (60, 4000), "32x64": (126, 4090), "64x64": (250, 4090),
+           "64x128": (500, 4090), "128x128": (1000, 4090), "256x256": (4000, 4090)}
+
+
+@pytest.mark.parametrize("kernel", list(KERNELS))
+@pytest.mark.parametrize("form", ["symmetric", "zeros", "e2m1"])
+@pytest.mark.parametrize("kind", ["f32", "e8m0"])
+def test_every_kernel(gpu_lib, kernel, form, kind):
+    """Sums exact, K with whole steps for all, some and none of the waves that share it,
+    and a rest."""
+    M, N = KERNELS[kernel]
+    for K in ((160, 131) if kernel == "few" else (1, 32, 203)):
+        dense(M, N, K, form, kind, group=32, integer=True)
+    dense(M, N, 160, form, kind, group=64, pad=3, shift=1, beta=0.5, bias=True, act=1)
+
+
 GROUPS = {"one": [1], "few": [0, 3, 0, 1, 17, 0], "even": [16, 16, 16, 16],
           "skewed": [0, 130, 1, 64, 65, 0, 300, 7], "many": [(7 * i) % 5 for i in range(150)],
           "long": [400, 500, 333]}
@@ -259,15 +276,18 @@ def grouped(counts, K, N, form, kind="f32", group=64, integer=True, spare=0, gat
     want, mag = c0.double().clone(), torch.zeros(rows_c, N, dtype=torch.float64)
     o = offsets.tolist()
     for e in range(G):
-        for i in range(o[e], o[e + 1]):
-            if not 0 <= ic[i] < rows_c:
-                continue
-            x = a[ia[i]].double() if 0 <= ia[i] < rows_a else torch.zeros(K, dtype=torch.float64)
-            old = c0[ic[i]].double()
-            v = W[e] @ x + beta * old + (bv[e].double() if bias else 0)
-            mag[ic[i]] = W[e].abs() @ x.abs() + abs(beta) * old.abs() + \
-                (bv[e].double().abs() if bias else 0)
-            want[ic[i]] = v.clamp_min(0) if act else v
+        places = torch.arange(o[e], o[e + 1])
+        places = places[(ic[places] >= 0) & (ic[places] < rows_c)]
+        if not len(places):
+            continue
+        read, to = ia[places], ic[places]
+        x = a[read.clamp(0, rows_a - 1)].double()
+        x[(read < 0) | (read >= rows_a)] = 0
+        old = c0[to].double()
+        v = x @ W[e].t() + beta * old + (bv[e].double() if bias else 0)
+        mag[to] = x.abs() @ W[e].abs().t() + abs(beta) * old.abs() + \
+            (bv[e].double().abs() if bias else 0)
+        want[to] = v.clamp_min(0) if act else v
     check(got, want, mag, K, group, integer, str(counts[:9]))
     if pad:
         flat = torch.as_strided(got, (rows_c, N + pad), (N + pad, 1), shift).cpu()
@@ -281,6 +301,20 @@ def test_grouped(gpu_lib, name, form, K, N):
     grouped(GROUPS[name], K, N, form, spare=4)
     grouped(GROUPS[name], K, N, form, group=32, integer=False, gather=False, scatter=False,
             bias=False, act=0)
+
+
+# uneven groups whose sizes reach each tile: (counts, N)
+WIDE = {"few": ([3, 0, 9, 21, 1, 8], 700), "32x32": ([40, 7, 0, 33], 1000),
+        "32x64": ([70, 33, 0, 20], 2000), "64x64": ([130, 64, 0, 40], 2900),
+        "64x128": ([300, 65, 7, 64], 4000), "128x128": ([500, 129, 3, 128], 4000),
+        "256x256": ([1500, 257, 3, 2000], 4000)}
+
+
+@pytest.mark.parametrize("kernel", list(WIDE))
+@pytest.mark.parametrize("form,kind", [("symmetric", "bf16"), ("e2m1", "e8m0")])
+def test_grouped_in_every_kernel(gpu_lib, kernel, form, kind):
+    counts, N = WIDE[kernel]
+    grouped(counts, 160 if kernel == "few" else 67, N, form, kind, group=32, spare=3)
 
 
 @pytest.mark.parametrize("pad,shift", [(3, 1), (8, 4)])
