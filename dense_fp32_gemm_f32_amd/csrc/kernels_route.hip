@@ -1,42 +1,90 @@
-// Routing to experts and its gradient, one wave a token, logits in registers
-// (expert i 64 + lane in register i).
+// Routing to experts and its gradient, one wave a token, the logits in registers:
+// lane l has experts l E to l E + E - 1, so that the lowest lane is the lowest expert.
 //
-// Which experts are chosen is decided in 64 bits: scores that 32 bits would round
-// onto each other, or exchange, go by their real order.  The weights and the
-// gradient are fp32; renormalised softmax weights are the softmax of the chosen
-// logits alone, so they hold where the chosen scores would underflow.
+// Which experts are chosen is decided as if in 64 bits: scores that 32 bits would round
+// onto each other, or exchange, go by their real order.  Without a bias the logits
+// themselves have that order.  With one (or sums of scores for groups) the scores are
+// formed in 32 bits first; where two that decide something lie within the error of
+// that, the token is done again in 64 bits.  The weights and the gradient are fp32;
+// renormalised softmax weights are the softmax of the chosen logits alone, so they
+// hold where the chosen scores would underflow.
 #include "experts_internal.h"
 
 #include <cfloat>
+#include <climits>
 
 namespace gemmf32 {
 namespace {
 
 constexpr int kWaves = 4, kThreads = kWaves * 64;
 
-__device__ __forceinline__ float wave_max(float x) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor(x, d));
-  return x;
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+// x of the lane that kCtrl names; none's in rows of 16 outside kRows.
+template <int kCtrl, int kRows, class T>
+__device__ __forceinline__ T dpp(T none, T x) {
+  return __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, none),
+                                                           __builtin_bit_cast(int, x), kCtrl,
+                                                           kRows, 0xf, false));
 }
-template <class T>
-__device__ __forceinline__ T wave_sum(T x) {
+
+// op over the wave's values, none being its neutral one: lanes 1, 2, then (as fours,
+// and then eights, agree by now) the mirrored half row and row, then row 0 (2) into
+// row 1 (3), and both into row 3, whose last lane has it.
+template <class T, class Op>
+__device__ __forceinline__ T wave_all(T x, T none, Op op) {
+  x = op(x, dpp<0xb1, 0xf>(none, x));
+  x = op(x, dpp<0x4e, 0xf>(none, x));
+  x = op(x, dpp<0x141, 0xf>(none, x));
+  x = op(x, dpp<0x140, 0xf>(none, x));
+  x = op(x, dpp<0x142, 0xa>(none, x));
+  x = op(x, dpp<0x143, 0xc>(none, x));
+  return __builtin_bit_cast(T, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 63));
+}
+__device__ __forceinline__ int wave_max(int x) {
+  return wave_all(x, INT_MIN, [](int a, int b) { return a > b ? a : b; });
+}
+__device__ __forceinline__ float wave_sum(float x) {
+  return wave_all(x, 0.f, [](float a, float b) { return a + b; });
+}
+
+__device__ __forceinline__ double wave_sum(double x) {
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) x += __shfl_xor(x, d);
   return x;
 }
 
-// The largest of the wave's 64 E values and its number i 64 + lane, the lowest of
-// equal ones; -1 where all are -infinity.
+// Floats that are not NaN as integers of the same order, 0 and -0 alike; kNone for what
+// is not to be chosen, -infinity too.
+constexpr int kNone = INT_MIN;
+__device__ __forceinline__ int key_of(float x) {
+  const int i = __float_as_int(x + 0.f);
+  return x > -INFINITY ? i ^ (i >> 31 & 0x7fffffff) : kNone;
+}
+__device__ __forceinline__ float of_key(int k) {
+  return k == kNone ? -INFINITY : __int_as_float(k ^ (k >> 31 & 0x7fffffff));
+}
+__device__ __forceinline__ float wave_max(float x) { return of_key(wave_max(key_of(x))); }
+
+// mask (0 or -1) ? a : b, in one instruction; of array elements a conditional would
+// become a choice of their index.
+__device__ __forceinline__ int pick(int mask, int a, int b) { return (a & mask) | (b & ~mask); }
+
+__device__ __forceinline__ float lane_value(float x, int lane) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), lane));
+}
+
+// The largest of the wave's 64 E values and its number, the lowest of equal ones; -1
+// where all are -infinity.
 template <int E>
-__device__ __forceinline__ int wave_best(const double (&v)[E], int lane, double& best) {
+__device__ __forceinline__ int wave_best(const double (&v)[E], int lane) {
   double x = v[0];
-  int at = lane;
+  int at = lane * E;
 #pragma unroll
   for (int i = 1; i < E; ++i)
     if (v[i] > x) {
       x = v[i];
-      at = i * 64 + lane;
+      at = lane * E + i;
     }
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) {
@@ -47,7 +95,6 @@ __device__ __forceinline__ int wave_best(const double (&v)[E], int lane, double&
       at = yat;
     }
   }
-  best = x;
   return x > -INFINITY ? at : -1;
 }
 
@@ -57,90 +104,336 @@ __device__ __forceinline__ void wave_fence() {
   __builtin_amdgcn_wave_barrier();
 }
 
+// A lane's share of a row of n values, E from lane E on; past the end what is given.
+// (Loads without a branch: past the end they read the last values.)
+template <int E>
+__device__ __forceinline__ void load_row(const float* row, int n, int lane, float past,
+                                         float (&v)[E]) {
+  const int first = lane * E;
+  if (E >= 4 && n % 4 == 0 && n > 0 && reinterpret_cast<uintptr_t>(row) % 16 == 0) {
+#pragma unroll
+    for (int i = 0; i < E; i += 4) {
+      const f32x4 x = *reinterpret_cast<const f32x4*>(row + min(first + i, n - 4));
+#pragma unroll
+      for (int k = 0; k < 4 && i + k < E; ++k) v[i + k] = first + i < n ? x[k] : past;
+    }
+  } else if (n > 0) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const float x = row[min(first + i, n - 1)];
+      v[i] = first + i < n ? x : past;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < E; ++i) v[i] = past;
+  }
+}
+
+template <int E>
+__device__ __forceinline__ void store_row(float* row, int n, int lane, const float (&v)[E]) {
+  const int first = lane * E;
+  if constexpr (E >= 4) {
+    if (n % 4 == 0 && reinterpret_cast<uintptr_t>(row) % 16 == 0) {
+#pragma unroll
+      for (int i = 0; i < E; i += 4)
+        if (first + i < n)
+          *reinterpret_cast<f32x4*>(row + first + i) = f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < E; ++i)
+    if (first + i < n) row[first + i] = v[i];
+}
+
 // A token's logits: NaN and -infinity (and what is past the end) as -infinity,
 // +infinity as the largest finite value.
 template <int E>
 __device__ __forceinline__ void load_logits(const RouteProblem& p, int64_t t, int lane,
                                             float (&l)[E]) {
-  const float* row = p.logits + t * p.ldl;
+  load_row<E>(p.logits + t * p.ldl, p.experts, lane, -INFINITY, l);
 #pragma unroll
-  for (int i = 0; i < E; ++i) {
-    const int e = i * 64 + lane;
-    const float x = e < p.experts ? row[e] : -INFINITY;
-    l[i] = x > -INFINITY ? fminf(x, FLT_MAX) : -INFINITY;
-  }
+  for (int i = 0; i < E; ++i) l[i] = l[i] > -INFINITY ? fminf(l[i], FLT_MAX) : -INFINITY;
 }
 
-// Softmax of the wave's logits into s; all -infinity gives zeros.
 template <int E>
-__device__ __forceinline__ void softmax(const float (&l)[E], float (&s)[E]) {
+__device__ __forceinline__ float largest(const float (&l)[E]) {
   float m = l[0];
 #pragma unroll
   for (int i = 1; i < E; ++i) m = fmaxf(m, l[i]);
-  m = wave_max(m);
-  float sum = 0.f;
-#pragma unroll
-  for (int i = 0; i < E; ++i) {
-    s[i] = l[i] > -INFINITY ? expf(l[i] - m) : 0.f;
-    sum += s[i];
-  }
-  sum = wave_sum(sum);
-#pragma unroll
-  for (int i = 0; i < E; ++i) s[i] = sum > 0.f ? s[i] / sum : 0.f;
+  return wave_max(m);
 }
 
-// The choices in 64 bits: lane j gets the expert of choice j (-1: none).
+// The sum of exp(l - m), m the largest; all -infinity gives 0.
 template <int E>
-__device__ __forceinline__ int choose(const RouteProblem& p, const float (&l)[E], int lane,
-                                      double* lds) {
-  double s[E], v[E];
-  const bool grouped = p.group_top < p.groups;
-  if (p.bias || (grouped && p.group_best == 2)) {
-    if (p.sigmoid) {
+__device__ __forceinline__ float exp_sum(const float (&l)[E], float m) {
+  float sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < E; ++i) s[i] = 1.0 / (1.0 + exp(-(double)l[i]));
-    } else {
-      float m = l[0];
+  for (int i = 0; i < E; ++i) sum += l[i] > -INFINITY ? expf(l[i] - m) : 0.f;
+  return wave_sum(sum);
+}
+
+// Keys and their numbers from the largest down, the lower number first of equal ones
+// (an odd-even merge sort).
+template <int E>
+__device__ __forceinline__ void sort_down(int (&v)[E], int (&at)[E]) {
 #pragma unroll
-      for (int i = 1; i < E; ++i) m = fmaxf(m, l[i]);
-      m = wave_max(m);
-      double sum = 0;
+  for (int p = 1; p < E; p *= 2)
 #pragma unroll
-      for (int i = 0; i < E; ++i) {
-        s[i] = l[i] > -INFINITY ? exp((double)l[i] - (double)m) : 0.0;
-        sum += s[i];
-      }
-      sum = wave_sum(sum);
+    for (int k = p; k >= 1; k /= 2)
 #pragma unroll
-      for (int i = 0; i < E; ++i) s[i] = sum > 0 ? s[i] / sum : 0.0;
-    }
+      for (int j = k % p; j + k < E; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; ++i) {
+          const int x = i + j, y = i + j + k;
+          if (y < E && x / (2 * p) == y / (2 * p)) {
+            const int vx = v[x], vy = v[y], ax = at[x], ay = at[y];
+            const int swap = -(int)((vy > vx) | ((vy == vx) & (ay < ax)));
+            v[x] = max(vx, vy);
+            v[y] = min(vx, vy);
+            at[x] = pick(swap, ay, ax);
+            at[y] = pick(swap, ax, ay);
+          }
+        }
+}
+
+// What 32-bit scores s + bias have to differ by for their order to be the real one.
+// A sigmoid is off by less than 2^-22: 0.45 2^-23 by the exponential (one unit of its
+// last place, and 2^-23 of its argument x, where x s (1 - s) < 0.23), half a unit by the
+// sum, one by the reciprocal.  A softmax's scores share the sum's error: 21 roundings of
+// half a unit, and the exponentials' mean one (below 7 units: the mean of |x| is below
+// 4.5 for 1024 experts); with 3 units of their own, two differ rightly to within 2^-18
+// of the largest score.  The addition of the bias rounds once.
+struct Margin {
+  float score;   // of the difference of two scores
+  __device__ __forceinline__ bool apart(float above, float below, float terms) const {
+    return above - below > terms * (score + 0x1p-22f * fmaxf(fabsf(above), fabsf(below)));
   }
+};
+
+// A token's scores in 64 bits.
+template <int E>
+struct Exact {
+  const RouteProblem& p;
+  double m = 0, sum = 1;   // of a softmax
+  __device__ __forceinline__ Exact(const RouteProblem& p, const float (&l)[E]) : p(p) {
+    if (p.sigmoid) return;
+    m = largest<E>(l);
+    sum = 0;
+#pragma unroll
+    for (int i = 0; i < E; ++i) sum += l[i] > -INFINITY ? exp(l[i] - m) : 0.0;
+    sum = wave_sum(sum);
+  }
+  __device__ __forceinline__ double score(double l) const {
+    return p.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - m) / sum;
+  }
+  // With the bias, of a logit above -infinity; one that is not to be chosen -infinity.
+  __device__ __forceinline__ double biased(double l, float b) const {
+    const double x = score(l) + (double)(b > FLT_MAX ? FLT_MAX : b);   // NaN stays NaN
+    return x > -INFINITY ? x : -INFINITY;
+  }
+};
+
+// Whether the group that lane g has the score of is above this lane's, by lane g.
+__device__ __forceinline__ bool above(double other, double mine, int g, int lane) {
+  return (other > mine) | ((other == mine) & (g < lane));
+}
+__device__ __forceinline__ double lane_value(double x, int lane) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_readlane((int)u, lane);
+  const uint32_t hi = __builtin_amdgcn_readlane((int)(u >> 32), lane);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// Whether lane g's group is among the best, by scores in 64 bits: as choose_fast finds it.
+template <int E>
+__device__ __forceinline__ bool in_best_groups(const RouteProblem& p, const float (&l)[E],
+                                               int lanes, int lane, double* lds) {
+  const Exact<E> exact(p, l);
+  float bias[E];
+  if (p.bias) load_row<E>(p.bias, p.experts, lane, 0.f, bias);
+  double a = -INFINITY, b = -INFINITY;
 #pragma unroll
   for (int i = 0; i < E; ++i) {
-    v[i] = l[i];   // without a bias the scores have the logits' order
-    if (p.bias && l[i] > -INFINITY) {
-      const float b = p.bias[i * 64 + lane];
-      const double x = s[i] + (double)(b > FLT_MAX ? FLT_MAX : b);   // NaN stays NaN
-      v[i] = x > -INFINITY ? x : -INFINITY;
+    double x = -INFINITY;
+    if (l[i] > -INFINITY) x = p.bias ? exact.biased(l[i], bias[i]) : exact.score(l[i]);
+    b = fmax(b, fmin(a, x));
+    a = fmax(a, x);
+  }
+  wave_fence();
+  lds[2 * lane] = a;
+  lds[2 * lane + 1] = b;
+  wave_fence();
+  a = b = -INFINITY;
+  if (lane < p.groups)
+    for (int k = 0; k < lanes; ++k) {
+      const double x = lds[2 * (lane * lanes + k)], y = lds[2 * (lane * lanes + k) + 1];
+      b = fmax(fmax(b, y), fmin(a, x));
+      a = fmax(a, x);
+    }
+  const double score = p.group_best == 2 && b > -INFINITY ? a + b : a;
+  int rank = 0;
+  for (int g = 0; g < p.groups; ++g) rank += above(lane_value(score, g), score, g, lane);
+  return rank < p.group_top;
+}
+
+// The choices by 32-bit scores: lane j gets the expert of choice j (-1: none).  False
+// where these do not decide them.
+template <int E>
+__device__ __forceinline__ bool choose_fast(const RouteProblem& p, const float* row,
+                                            const float (&l)[E], int lane, double* lds,
+                                            int& mine) {
+  const bool grouped = p.group_top < p.groups, sums = p.group_best == 2;
+  const bool scores = p.bias || (grouped && sums);
+  float s[E];
+  int v[E];
+  Margin margin = {0x1.8p-21f};
+  if (scores) {
+    constexpr float kLog2e = 1.44269504f;
+    if (p.sigmoid) {
+#pragma unroll
+      for (int i = 0; i < E; ++i)
+        s[i] = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(l[i] * -kLog2e));
+    } else {
+      const float m = largest<E>(l);
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        s[i] = l[i] > -INFINITY ? __builtin_amdgcn_exp2f((l[i] - m) * kLog2e) : 0.f;
+        sum += s[i];
+      }
+      const float r = __builtin_amdgcn_rcpf(wave_sum(sum));
+      margin.score = 0x1p-18f * r;
+#pragma unroll
+      for (int i = 0; i < E; ++i) s[i] *= r;
     }
   }
-  if (grouped) {
-    // a group's score by one lane each, then the best groups, marked in LDS
-    const int size = p.experts / p.groups;
-    const bool sums = p.group_best == 2;
-#pragma unroll
-    for (int i = 0; i < E; ++i)
-      if (i * 64 + lane < p.experts)
-        lds[i * 64 + lane] = sums && !p.bias ? (v[i] > -INFINITY ? s[i] : -INFINITY) : v[i];
-    wave_fence();
-    double gs[E];
+  if (p.bias) {
+    float b[E];
+    load_row<E>(p.bias, p.experts, lane, 0.f, b);
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-      const int g = i * 64 + lane;
+      const float x = s[i] + fminf(b[i], FLT_MAX);
+      v[i] = ((l[i] > -INFINITY) & (b[i] > -INFINITY)) ? key_of(x) : kNone;   // NaN: neither
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < E; ++i) v[i] = key_of(l[i]);
+  }
+  if (grouped) {
+    // whole lanes to a group: each lane's best two, then those of a group by one lane
+    const int size = p.experts / p.groups, lanes = size / E;
+    if (lanes * E != size) return false;
+    int a = kNone, b = kNone;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      int x = v[i];
+      if (sums && !p.bias) x = x != kNone ? key_of(s[i]) : kNone;
+      b = max(b, min(a, x));
+      a = max(a, x);
+    }
+    int* const best = reinterpret_cast<int*>(lds);
+    best[2 * lane] = a;
+    best[2 * lane + 1] = b;
+    wave_fence();
+    a = b = kNone;
+    if (lane < p.groups)
+      for (int k = 0; k < lanes; ++k) {
+        const int x = best[2 * (lane * lanes + k)], y = best[2 * (lane * lanes + k) + 1];
+        b = max(max(b, y), min(a, x));
+        a = max(a, x);
+      }
+    const int score = sums && b != kNone ? key_of(of_key(a) + of_key(b)) : a;
+    int rank = 0;   // groups above this lane's
+    for (int g = 0; g < p.groups; ++g) {
+      const int other = __builtin_amdgcn_readlane(score, g);
+      rank += (other > score) | ((other == score) & (g < lane));
+    }
+    bool in = rank < p.group_top;
+    if (scores) {
+      // the least of those in, as the largest of the others' complement
+      const int least = ~wave_max(in ? ~score : kNone), next = wave_max(in ? kNone : score);
+      if (next != kNone && !margin.apart(of_key(least), of_key(next), 2.f))
+        in = in_best_groups<E>(p, l, lanes, lane, lds);
+    }
+    const uint64_t chosen = __builtin_amdgcn_ballot_w64(in);
+    const int out = (int)(chosen >> (lane / lanes & 63) & 1) - 1;
+#pragma unroll
+    for (int i = 0; i < E; ++i) v[i] = pick(out, kNone, v[i]);
+  }
+  int at[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) at[i] = lane * E + i;
+  sort_down<E>(v, at);
+  mine = -1;
+  // lane j has the key of choice j; those behind the last are chosen too until one is
+  // apart, so that the real choices are among them
+  int key = kNone, last = kNone, n = 0;
+  bool known = true;
+  for (;; ++n) {
+    const int best = wave_max(v[0]);
+    if (best == kNone) break;
+    if (n >= p.top && (!p.bias || margin.apart(of_key(last), of_key(best), 1.f))) break;
+    known = n < 64;
+    if (!known) break;
+    last = best;
+    const int w = __builtin_ctzll(__builtin_amdgcn_ballot_w64(v[0] == best));
+    const int e = __builtin_amdgcn_readlane(at[0], w);
+    const int here = -(int)(lane == n), pop = -(int)(lane == w);
+    mine = pick(here, e, mine);
+    key = pick(here, best, key);
+#pragma unroll
+    for (int i = 0; i + 1 < E; ++i) {
+      v[i] = pick(pop, v[i + 1], v[i]);
+      at[i] = pick(pop, at[i + 1], at[i]);
+    }
+    v[E - 1] = pick(pop, kNone, v[E - 1]);
+  }
+  if (!known) return false;
+  if (p.bias) {
+    const int next = __shfl_down(key, 1);
+    const bool close = lane + 1 < n && !margin.apart(of_key(key), of_key(next), 1.f);
+    if (__builtin_amdgcn_ballot_w64(close)) {
+      // their order in 64 bits
+      const Exact<E> exact(p, l);
+      double x = -INFINITY;
+      if (lane < n) x = exact.biased(fminf(row[mine], FLT_MAX), p.bias[mine]);
+      int rank = lane < n ? 0 : lane;
+      for (int j = 0; j < n; ++j) {
+        const double y = lane_value(x, j);
+        const int e = __builtin_amdgcn_readlane(mine, j);
+        rank += lane < n && ((y > x) | ((y == x) & (e < mine)));
+      }
+      mine = __builtin_amdgcn_ds_permute(rank * 4, mine);
+    }
+  }
+  if (lane >= p.top) mine = -1;
+  return true;
+}
+
+// The choices in 64 bits from the start, the scores in LDS: for groups that share lanes
+// and for more than 64 scores too close to each other.
+template <int E>
+__device__ __forceinline__ int choose(const RouteProblem& p, const float (&l)[E], int lane,
+                                      double* v) {
+  const Exact<E> exact(p, l);
+  float bias[E];
+  if (p.bias) load_row<E>(p.bias, p.experts, lane, 0.f, bias);
+#pragma unroll
+  for (int i = 0; i < E; ++i)   // without a bias the scores have the logits' order
+    v[lane * E + i] = p.bias && l[i] > -INFINITY ? exact.biased(l[i], bias[i]) : l[i];
+  wave_fence();
+  if (p.group_top < p.groups) {
+    const int size = p.experts / p.groups;
+    const bool sums = p.group_best == 2;
+    double gs[E];   // of groups lane E + i
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const int g = lane * E + i;
       double a = -INFINITY, b = -INFINITY;
       if (g < p.groups)
         for (int k = 0; k < size; ++k) {
-          const double x = lds[g * size + k];
+          const double x = v[g * size + k];
           if (x > a) {
             b = a;
             a = x;
@@ -148,35 +441,47 @@ __device__ __forceinline__ int choose(const RouteProblem& p, const float (&l)[E]
             b = x;
           }
         }
+      if (sums && !p.bias) {
+        a = a > -INFINITY ? exact.score(a) : a;
+        b = b > -INFINITY ? exact.score(b) : b;
+      }
       gs[i] = sums && b > -INFINITY ? a + b : a;
     }
     wave_fence();
-#pragma unroll
-    for (int i = 0; i < E; ++i)
-      if (i * 64 + lane < p.groups) lds[i * 64 + lane] = 0;
+    uint32_t in = 0;
     for (int j = 0; j < p.group_top; ++j) {
-      double best;
-      const int g = wave_best<E>(gs, lane, best);
+      const int g = wave_best<E>(gs, lane);
       if (g < 0) break;
-      if (lane == 0) lds[g] = 1;
 #pragma unroll
       for (int i = 0; i < E; ++i)
-        if (i * 64 + lane == g) gs[i] = -INFINITY;
+        if (lane * E + i == g) {
+          gs[i] = -INFINITY;
+          in |= 1u << i;
+        }
+    }
+#pragma unroll 1
+    for (int i = 0; i < E; ++i) {
+      const int g = lane * E + i;
+      if (g < p.groups && !(in >> i & 1))
+        for (int k = 0; k < size; ++k) v[g * size + k] = -INFINITY;
     }
     wave_fence();
-#pragma unroll
-    for (int i = 0; i < E; ++i)
-      if (i * 64 + lane < p.experts && lds[(i * 64 + lane) / size] == 0) v[i] = -INFINITY;
   }
   int mine = -1;
   for (int j = 0; j < p.top; ++j) {
-    double best;
-    const int e = wave_best<E>(v, lane, best);
-    if (e < 0) break;
-    if (lane == j) mine = e;
-#pragma unroll
+    double x[1] = {-INFINITY};
+    int at = 0;
+#pragma unroll 1
     for (int i = 0; i < E; ++i)
-      if (i * 64 + lane == e) v[i] = -INFINITY;
+      if (v[lane * E + i] > x[0]) {
+        x[0] = v[lane * E + i];
+        at = i;
+      }
+    const int w = wave_best<1>(x, lane);
+    if (w < 0) break;
+    const int e = w * E + __builtin_amdgcn_readlane(at, __builtin_amdgcn_readfirstlane(w));
+    if (lane == j) mine = e;
+    if (lane == w) v[e] = -INFINITY;
   }
   return mine;
 }
@@ -201,13 +506,17 @@ __device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + expf(-x)
 
 template <int E>
 __global__ void __launch_bounds__(kThreads) route_kernel(RouteProblem p) {
-  __shared__ double lds[kWaves][64 * E];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  __shared__ double lds[kWaves][64 * (E > 1 ? E : 2)];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int64_t t = (int64_t)tile_id() * kWaves + wave;
   if (t >= p.tokens) return;
   float l[E];
   load_logits<E>(p, t, lane, l);
-  const int e = choose<E>(p, l, lane, lds[wave]);
+  int e;
+  if (!choose_fast<E>(p, p.logits + t * p.ldl, l, lane, lds[wave], e)) {
+    wave_fence();
+    e = choose<E>(p, l, lane, lds[wave]);
+  }
   const bool there = e >= 0;
   float x = 0.f, w;   // this lane's chosen logit
   if (there) x = fminf(p.logits[t * p.ldl + e], FLT_MAX);
@@ -217,14 +526,8 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteProblem p) {
   } else if (p.renorm) {
     w = share_of_chosen(x, there);
   } else {
-    float s[E];
-    softmax<E>(l, s);
-    w = 0.f;
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const float y = __shfl(s[i], e & 63);
-      if (there && e >> 6 == i) w = y;
-    }
+    const float m = largest<E>(l), sum = exp_sum<E>(l, m);
+    w = there ? expf(x - m) / sum : 0.f;
   }
   if (lane < p.top) {
     p.choice[t * p.top + lane] = e;
@@ -241,7 +544,7 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteProblem p) {
 // by choice, so an expert named twice gets both.
 template <int E>
 __global__ void __launch_bounds__(kThreads) route_grad_kernel(RouteProblem p) {
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int64_t t = (int64_t)tile_id() * kWaves + wave;
   if (t >= p.tokens) return;
   const float* row = p.logits + t * p.ldl;
@@ -255,19 +558,19 @@ __global__ void __launch_bounds__(kThreads) route_grad_kernel(RouteProblem p) {
   for (int i = 0; i < E; ++i) d[i] = 0.f;
   float mine;
   if (!p.sigmoid && !p.renorm) {
-    float l[E], s[E];
+    float l[E], sum = 0.f;
     load_logits<E>(p, t, lane, l);
-    softmax<E>(l, s);
-    mine = 0.f;
+    const float m = largest<E>(l);
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-      const float y = __shfl(s[i], e & 63);
-      if (there && e >> 6 == i) mine = y;
+      d[i] = l[i] > -INFINITY ? expf(l[i] - m) : 0.f;
+      sum += d[i];
     }
-    mine *= g;
+    sum = wave_sum(sum);
+    mine = there ? expf(x - m) / sum * g : 0.f;
     const float dot = wave_sum(mine);
 #pragma unroll
-    for (int i = 0; i < E; ++i) d[i] = l[i] > -INFINITY ? -s[i] * dot : 0.f;
+    for (int i = 0; i < E; ++i) d[i] = sum > 0.f ? -(d[i] / sum * dot) : 0.f;
   } else {
     const float s = p.sigmoid && there ? sigmoid(x) : 0.f;
     if (p.renorm) {
@@ -279,16 +582,14 @@ __global__ void __launch_bounds__(kThreads) route_grad_kernel(RouteProblem p) {
   }
   for (int j = 0; j < p.top; ++j) {
     const int to = __builtin_amdgcn_readlane(there ? e : -1, j);
-    const float y = __shfl(mine, j);
+    const float y = lane_value(mine, j);
     if (to < 0) continue;
 #pragma unroll
     for (int i = 0; i < E; ++i)
-      if (i * 64 + lane == to) d[i] += y;
+      if (lane * E + i == to) d[i] += y;
   }
   float* out = p.dlogits + t * p.lddl;
-#pragma unroll
-  for (int i = 0; i < E; ++i)
-    if (i * 64 + lane < p.experts) out[i * 64 + lane] = d[i];
+  store_row<E>(out, p.experts, lane, d);
 }
 
 template <template <int> class K>

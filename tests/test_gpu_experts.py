@@ -174,6 +174,25 @@ def test_route_scores_that_32_bits_cannot_tell_apart(gpu_lib):
                 group_best=2, what="groups")
 
 
+@pytest.mark.parametrize("E,groups,group_top", [(64, 1, 1), (100, 1, 1), (256, 8, 3), (250, 10, 4),
+                                                (384, 12, 5), (1000, 1, 1), (1000, 8, 2)])
+@pytest.mark.parametrize("score", [SOFTMAX, SIGMOID])
+def test_route_close_scores(gpu_lib, E, groups, group_top, score):
+    """Clusters of scores that differ by about a step of 32 bits or not at all, at the
+    last choice and the last group too."""
+    g = gen(3 * E + groups)
+    H.say(f"route close scores E={E} groups={groups} score={score}")
+    for levels, steps in ((E // 5, 3), (2, 40), (1, 2)):
+        logits = torch.randint(0, levels, (24, E), generator=g) * (2.0 / levels)
+        logits = logits.float() + torch.randint(0, steps, (24, E), generator=g) * 2.0 ** -22
+        bias = torch.randint(0, 2, (E,), generator=g) * 0.125
+        logits[7, 3:] = -INF
+        for best in (1, 2):
+            check_route(logits, 8, bias=bias, score=score, groups=groups, group_top=group_top,
+                        group_best=best, renorm=True, what=f"{levels} levels, best={best}")
+        check_route(logits, 64, bias=bias, score=score, what=f"{levels} levels, 64 choices")
+
+
 def test_route_masks_and_values_that_are_not_finite(gpu_lib):
     H.say("route masks")
     g = gen(7)
