@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from array import array
 from pathlib import Path
 
 PKG = Path(__file__).resolve().parent
@@ -981,17 +982,19 @@ def gemm_q4_grouped(A, codes, scale, offsets, C=None, *, zero=None, group=128, f
 
 
 def _arrays(tensors, name, device):
-    """Host tables of the pointers and sizes of contiguous float32 tensors."""
+    """Host tables of the pointers and sizes of contiguous float32 tensors.  (There may
+    be hundreds: each property is read by one map, without a Python frame for each.)"""
     import torch
-    f32 = torch.float32
-    for t in tensors:
-        if t.dtype is not f32 or not t.is_contiguous():
-            raise TypeError(f"{name} must hold contiguous float32 tensors")
-        if t.device != device:
-            raise ValueError(f"{name} must be on {device} (got {t.device})")
-    n = len(tensors)
-    return ((ctypes.c_void_p * n)(*[t.data_ptr() for t in tensors]),
-            (ctypes.c_int64 * n)(*[t.numel() for t in tensors]))
+    T = torch.Tensor
+    for t in set(map(type, tensors)):
+        if not issubclass(t, T):
+            raise TypeError(f"{name} must hold tensors")
+    if set(map(T.get_device, tensors)) != {device.index}:
+        raise ValueError(f"{name} must be on {device}")
+    if (set(map(T.dtype.__get__, tensors)) != {torch.float32}
+            or not all(map(T.is_contiguous, tensors))):
+        raise TypeError(f"{name} must hold contiguous float32 tensors")
+    return (array("Q", map(T.data_ptr, tensors)), array("q", map(T.numel, tensors)))
 
 
 def _norm_of(tensors, out, max_norm, norm):
@@ -1005,15 +1008,17 @@ def _norm_of(tensors, out, max_norm, norm):
     if out is not None:
         out = list(out)
         y, m = _arrays(out, "out", dev)
-        if len(out) != len(tensors) or m[:] != n[:]:
+        if m != n:
             raise ValueError("out must hold a tensor of the same size for each")
     if norm is None:
         norm = torch.empty(1, dtype=torch.float32, device=dev)
     ptr = _vector(norm, "norm", dev, 1)
     if max_norm is None:
-        rc, what = _on(tensors[0], gemm_f32_norm, len(tensors), x, n, ptr), "gemm_f32_norm"
+        rc, what = (_on(tensors[0], gemm_f32_norm, len(tensors), x.buffer_info()[0],
+                        n.buffer_info()[0], ptr), "gemm_f32_norm")
     else:
-        rc, what = (_on(tensors[0], gemm_f32_clip, len(tensors), x, n, y, max_norm, ptr),
+        rc, what = (_on(tensors[0], gemm_f32_clip, len(tensors), x.buffer_info()[0],
+                        n.buffer_info()[0], y and y.buffer_info()[0], max_norm, ptr),
                     "gemm_f32_clip")
     if rc != GEMM_F32_OK:
         raise GemmError(rc, what)
