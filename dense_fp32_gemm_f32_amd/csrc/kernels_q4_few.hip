@@ -1,11 +1,11 @@
 // Products with 4-bit weights for few rows (q4_routes.h) and at least 128 k: tiles of up
-// to 8 rows.  Bound by the read of the codes: one row of 8192 x 8192 takes 16 us (33.5 MB
+// to 16 rows.  Bound by the read of the codes: one row of 8192 x 8192 takes 16 us (33.5 MB
 // of codes, 2.2 TB/s), 28672 x 8192 38 us (3.1 TB/s), where loads alone in the same order
 // take 33 us.
 //
 // The rows' three bf16 parts are the rows of the matrix instruction: row r's part
 // p is row 3 r + p, so that up to 5 rows of A take one instruction for 16 columns
-// by 32 k, up to 8 two.  A workgroup splits its rows once, into LDS, and goes through
+// by 32 k, up to 10 two.  A workgroup splits its rows once, into LDS, and goes through
 // strips of columns with them (rows whose parts do not fit take K in passes, for each
 // strip anew).  A wave takes 16 columns and every kw-th chunk of 128 k, 16 bytes of
 // codes a lane; the kw waves of a strip add their sums through LDS in one order, and
@@ -23,14 +23,13 @@ namespace {
 
 using namespace q4;
 
-constexpr int kWaves = 16, kWavesLog2 = 4, kThreads = kWaves * 64;
-constexpr int kRows = 8;             // rows of a tile, at most
+constexpr int kWavesLog2 = kQ4FewWavesLog2, kWaves = 1 << kWavesLog2, kThreads = kWaves * 64;
 constexpr int kChunkK = 128;         // k of a chunk: four steps of 32
 constexpr int kAhead = 2;            // chunks on the way
-// the waves' sums (1 KiB a wave and 16 rows of parts), then the parts; one workgroup to
-// a CU
+// the waves' sums (1 KiB a wave and 16 rows of parts; two buffers of them, so that a
+// strip takes one barrier, for 16 rows), then the parts; one workgroup to a CU
 constexpr int kLdsBytes = 158 * 1024;
-constexpr int kSumBytes = 2 * kWaves * 1024;
+constexpr int sum_bytes(int rt) { return (rt < 2 ? 2 : rt) * kWaves * 1024; }
 
 // kScales: scales of a chunk (1 for groups of 128 and more), of kBytes bytes each.
 template <int kScales, int kBytes>
@@ -39,18 +38,10 @@ struct Item {
   uint32_t scale[(kScales * kBytes + 3) / 4], zero;
 };
 
-static_assert((kLdsBytes - kSumBytes) / (3 * kRows * 256) >= kWaves, "a chunk for every wave");
-
-// Waves along K, as a power of two: so many that a workgroup on each CU has columns
-// for its waves, and no more than there are chunks.
-__host__ __device__ inline int waves_along_k(const Q4Problem& p) {
-  const int64_t chunks = ((int64_t)p.g.K + kChunkK - 1) / kChunkK;
-  const int64_t columns = ((int64_t)p.g.N + 15) / 16 * p.g.groups;
-  int log2 = 0;
-  while (log2 < kWavesLog2 && (columns << log2) < 256 * kWaves && (INT64_C(1) << log2) < chunks)
-    ++log2;
-  return log2;
-}
+// a chunk for every wave along K
+static_assert((kLdsBytes - sum_bytes(2)) / (3 * kQ4FewRowsDeep * 256) >= kWaves &&
+              (kLdsBytes - sum_bytes(3)) / (3 * kQ4FewRows * 256) >= kWaves / 2, "room for parts");
+static_assert(kWaves == 1 << kQ4FewWavesLog2 && kChunkK == kQ4FewK, "as the rules count them");
 
 template <int RT, int kForm, int kScales, int kBytes>
 struct Few {
@@ -71,8 +62,8 @@ struct Few {
         along((int)(((int64_t)p.g.K - 1) >> p.group_shift) + 1),
         chunks((int)(((int64_t)p.g.K + kChunkK - 1) / kChunkK)),
         tid(threadIdx.x), wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)),
-        lane(threadIdx.x & 63), lds(lds), parts(lds + kSumBytes), row_of(row_of), row_to(row_of + kRows) {
-    kw_log2 = waves_along_k(p);
+        lane(threadIdx.x & 63), lds(lds), parts(lds + sum_bytes(RT)), row_of(row_of), row_to(row_of + kQ4FewRows) {
+    kw_log2 = q4_waves_along_k(p);
     kwave = wave & ((1 << kw_log2) - 1);
     side = wave >> kw_log2;
   }
@@ -216,7 +207,7 @@ struct Few {
                                         f32x4 (&acc)[RT]) const {
     const int kw = 1 << kw_log2, wide = 16 * kWaves >> kw_log2;   // columns of the strip
     const int64_t n0 = (int64_t)strip * wide + tid % wide;   // this thread's column
-    float* red = reinterpret_cast<float*>(lds) + (RT == 1 ? buffer * (kSumBytes / 8) : 0);
+    float* red = reinterpret_cast<float*>(lds) + (RT == 1 ? buffer * (sum_bytes(1) / 8) : 0);
 #pragma unroll
     for (int t = 0; t < RT; ++t)
 #pragma unroll
@@ -227,10 +218,11 @@ struct Few {
       for (int r = tid / wide; r < rows; r += kThreads / wide) {
         const int c = tid % wide, to = row_to[r];
         float v = 0.f;
+        const float* from = red + ((((c >> 4) << kw_log2) * RT * 16 + 3 * r) * 16 + (c & 15));
+#pragma unroll 4
         for (int i = 0; i < kw; ++i)
 #pragma unroll
-          for (int part = 0; part < 3; ++part)
-            v += red[((((c >> 4) << kw_log2) + i) * RT * 16 + 3 * r + part) * 16 + (c & 15)];
+          for (int part = 0; part < 3; ++part) v += from[(i * RT * 16 + part) * 16];
         if (to >= 0) {
           float* out = p.g.C + to * p.g.ldc + n0;
           *out = epilogue_apply(ep, row_of[r] >= 0 ? v : 0.f, out, n0);
@@ -253,7 +245,7 @@ struct Few {
       row_to[tid] = to >= 0 && to < p.g.rows_c ? to : -1;
     }
     const int kw = 1 << kw_log2;
-    pass = min(chunks, (kLdsBytes - kSumBytes) / (R * 256) & -kWaves);
+    pass = min(chunks, (kLdsBytes - sum_bytes(RT)) / (R * 256) & -kw);
     const int passes = (chunks + pass - 1) / pass;
     // positions: (strip, first chunk of the pass, this wave's place in it)
     struct Position {
@@ -316,34 +308,35 @@ struct Few {
 template <int kForm, int kScales, int kBytes>
 __global__ void __launch_bounds__(kThreads, 4) q4_few_kernel(Q4Problem p, Epilogue ep) {
   __shared__ __attribute__((aligned(16))) char lds[kLdsBytes];
-  __shared__ int row_of[2 * kRows];
+  __shared__ int row_of[2 * kQ4FewRows];
   const int group = blockIdx.y;
   int begin, end;
   group_span(p.g.offsets, group, p.g.rows, begin, end);
   // row tiles of one size, along the grid's z and, where there are more, in turn
-  const int tiles = (end - begin + kRows - 1) / kRows;
+  const int most = q4_few_rows(p), tiles = (end - begin + most - 1) / most;
   if (tiles == 0) return;
   const int each = (end - begin + tiles - 1) / tiles;
   if (ep.bias) ep.bias += group * p.g.sbias;
   for (int i = blockIdx.z; i < tiles; i += gridDim.z) {
     const int first = begin + i * each, rows = min(each, end - first);
     if (rows <= 0) break;
-    if (rows <= 5) {
-      Few<1, kForm, kScales, kBytes> few(p, group, lds, row_of);
+    auto run = [&](auto few) {
       const int wide = 16 * kWaves >> few.kw_log2;
       few.run(ep, first, rows, blockIdx.x, gridDim.x, (int)(((int64_t)p.g.N + wide - 1) / wide));
-    } else {
-      Few<2, kForm, kScales, kBytes> few(p, group, lds, row_of);
-      const int wide = 16 * kWaves >> few.kw_log2;
-      few.run(ep, first, rows, blockIdx.x, gridDim.x, (int)(((int64_t)p.g.N + wide - 1) / wide));
-    }
+    };
+    if (rows <= 5)
+      run(Few<1, kForm, kScales, kBytes>(p, group, lds, row_of));
+    else if (rows <= 10)
+      run(Few<2, kForm, kScales, kBytes>(p, group, lds, row_of));
+    else
+      run(Few<3, kForm, kScales, kBytes>(p, group, lds, row_of));
   }
 }
 
 template <int kForm, int kScales, int kBytes>
 hipError_t launch(const Q4Problem& p, const Epilogue& e, hipStream_t s) {
-  const int tiles = p.g.offsets ? 1 : (p.g.rows + kRows - 1) / kRows;
-  const int wide = 16 * kWaves >> waves_along_k(p);
+  const int tiles = p.g.offsets ? 1 : (p.g.rows + q4_few_rows(p) - 1) / q4_few_rows(p);
+  const int wide = 16 * kWaves >> q4_waves_along_k(p);
   const int64_t strips = ((int64_t)p.g.N + wide - 1) / wide;
   // a workgroup a CU, each with as many strips
   const int64_t most = std::max((int64_t)1, 256 / ((int64_t)p.g.groups * tiles));
@@ -370,7 +363,6 @@ hipError_t by_group(const Q4Problem& p, const Epilogue& e, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_q4_few(const Q4Problem& p, const Epilogue& e, hipStream_t s) {
-  static_assert(kQ4FewK == kChunkK, "a chunk at least");
   if (p.g.K < kChunkK) return hipErrorInvalidValue;
   return p.e2m1 ? by_group<kE2m1>(p, e, s)
                 : p.zero ? by_group<kIntZeros>(p, e, s) : by_group<kInt8>(p, e, s);

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 
 #include "experts_internal.h"
@@ -43,27 +44,57 @@ inline Q4Tile q4_tile(const Q4Problem& p) {
   return (Q4Tile)best;
 }
 
-// The kernel for few rows (kernels_q4_few.hip), whose row tiles have up to 8, in the same
-// unit: with c columns of 16 for each CU, a row tile takes as long as (0.3 + 0.12 c)
-// rounds of kTile32; where columns are fewer than CUs, row tiles go beside each other.
-// (e8m0 scales, 4096 x 4096: 8 rows 14 us against 24 us for the tiles, 16 rows 23 against
-// 24, 24 rows 39 against 24; 8192 x 8192: 8 rows 25 against 40, 16 rows 44 against 40;
-// 2048 x 1024 in 32 groups: 192 rows 17 against 48, 700 rows 42 against 51, 1000 rows 54
-// against 53.)
-inline int64_t q4_few_cost(const Q4Problem& p) {
-  const int64_t columns = ((int64_t)p.g.N + 15) / 16 * p.g.groups;   // 256 to a round
-  // row tiles of a group, in quarters; of uneven groups a little more than their average
-  const int64_t tiles = p.g.groups == 1
-                            ? ((int64_t)p.g.rows + 7) / 8 * 4
-                            : std::max((int64_t)4, (int64_t)p.g.rows / (2 * p.g.groups) + 1);
-  if (columns < 256) return 30 + 25 * columns * tiles / (4 * 256);
-  return tiles * (30 + 12 * columns / 256) / 4;
+constexpr int kQ4FewK = 128;   // the least K that the kernel for few rows takes, and its chunk
+constexpr int kQ4FewWavesLog2 = 4;
+constexpr int kQ4FewRows = 16, kQ4FewRowsDeep = 10;
+
+#if defined(__HIP__)
+#define GEMM_F32_BOTH __host__ __device__
+#else
+#define GEMM_F32_BOTH
+#endif
+
+// Its waves along K, as a power of two: so many that a workgroup on each CU has columns
+// for its waves, and no more than there are chunks.
+GEMM_F32_BOTH inline int q4_waves_along_k(const Q4Problem& p) {
+  const int64_t chunks = ((int64_t)p.g.K + kQ4FewK - 1) / kQ4FewK;
+  const int64_t columns = ((int64_t)p.g.N + 15) / 16 * p.g.groups;
+  int log2 = 0;
+  while (log2 < kQ4FewWavesLog2 && (columns << log2) < (256 << kQ4FewWavesLog2) &&
+         (INT64_C(1) << log2) < chunks)
+    ++log2;
+  return log2;
 }
 
-constexpr int kQ4FewK = 128;   // the least K it takes
+// Rows of its row tiles, at most: those whose parts of a chunk for each wave along K fit
+// into LDS.
+GEMM_F32_BOTH inline int q4_few_rows(const Q4Problem& p) {
+  return q4_waves_along_k(p) < kQ4FewWavesLog2 ? kQ4FewRows : kQ4FewRowsDeep;
+}
 
+// Whether the kernel for few rows (kernels_q4_few.hip) is the faster one, by its time in
+// the tiles' unit: with e strips of columns for each workgroup, c columns of 16 in them,
+// and r rows a row tile takes 12 + 2 r + c (9 + 0.8 r), and 18 for each strip where all
+// waves go along K.  Row tiles of one matrix go beside each other, those of a group one
+// after another; uneven groups are counted half as long again as their average.
+// (Few against tiles in us, e8m0 scales.  4096 x 4096: 8 rows 14 against 24, 16 rows 22
+// against 23, 24 rows 39 against 24; 8192 x 8192: 8 rows 25 against 40, 16 rows 41 against
+// 40, 24 rows 63 against 41; 28672 x 8192: 16 rows 95 against 104, 17 rows 117 against 104;
+// 2048 x 1024 in 32 groups: 6 rows each 17 against 48, 20 rows 32 against 48.)
 inline bool q4_few(const Q4Problem& p) {
-  return p.g.K >= kQ4FewK && q4_few_cost(p) < q4_tile_cost(p, q4_tile(p));
+  if (p.g.K < kQ4FewK) return false;
+  const int waves = 1 << kQ4FewWavesLog2, wide = waves >> q4_waves_along_k(p);
+  const auto up = [](double x, double by) { return std::ceil(x / by); };
+  const bool one = p.g.groups == 1;
+  const double strips = up(p.g.N, 16 * wide), groups = p.g.groups;
+  const double rows = one ? p.g.rows : 1.5 * p.g.rows / groups + 1;
+  const double tiles = up(rows, q4_few_rows(p)), r = up(rows, tiles);
+  const double beside = groups * (one ? tiles : 1.0), turns = one ? 1.0 : tiles;
+  const double e = up(strips, std::max(1.0, std::floor(256 / beside)));
+  const double rounds = up(beside * up(strips, e), 256);
+  const double time =
+      12 + 2 * r + e * wide * (9 + 0.8 * r) + (wide == 1 ? 18 * e : 0.0);
+  return time * rounds * turns < 0.9 * (double)q4_tile_cost(p, q4_tile(p));
 }
 
 }  // namespace gemmf32

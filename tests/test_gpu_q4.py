@@ -237,9 +237,23 @@ def test_every_kernel(gpu_lib, kernel, form, kind):
     """Sums exact, K with whole steps for all, some and none of the waves that share it,
     and a rest."""
     M, N = KERNELS[kernel]
-    for K in ((160, 131) if kernel == "few" else (1, 32, 203)):
+    for K in ((640, 515) if kernel == "few" else (1, 32, 203)):
         dense(M, N, K, form, kind, group=32, integer=True)
-    dense(M, N, 160, form, kind, group=64, pad=3, shift=1, beta=0.5, bias=True, act=1)
+    dense(M, N, 640 if kernel == "few" else 160, form, kind, group=64, pad=3, shift=1, beta=0.5,
+          bias=True, act=1)
+
+
+# rows, columns, K of the kernel for few rows: its row tiles of each size, one and more of
+# them, all and some of its waves along K, K in one pass and in several
+FEW = [(M, N, K) for M in (1, 5, 6, 10, 11, 16) for N, K in ((1000, 2100), (8192, 1031),
+                                                             (33, 16400), (28672, 1031))]
+FEW += [(17, 1000, 2100), (33, 1000, 640), (40, 300, 2100), (150, 16, 4096)]
+
+
+@pytest.mark.parametrize("M,N,K", FEW)
+def test_few_rows(gpu_lib, M, N, K):
+    dense(M, N, K, "zeros", "f16", group=128)
+    dense(M, N, K, "e2m1", "e8m0", group=32, beta=0.5, bias=True, pad=5, shift=3)
 
 
 GROUPS = {"one": [1], "few": [0, 3, 0, 1, 17, 0], "even": [16, 16, 16, 16],
@@ -314,7 +328,7 @@ WIDE = {"few": ([3, 0, 9, 21, 1, 8], 700), "32x32": ([40, 7, 0, 33], 1000),
 @pytest.mark.parametrize("form,kind", [("symmetric", "bf16"), ("e2m1", "e8m0")])
 def test_grouped_in_every_kernel(gpu_lib, kernel, form, kind):
     counts, N = WIDE[kernel]
-    grouped(counts, 160 if kernel == "few" else 67, N, form, kind, group=32, spare=3)
+    grouped(counts, 515 if kernel == "few" else 67, N, form, kind, group=32, spare=3)
 
 
 @pytest.mark.parametrize("pad,shift", [(3, 1), (8, 4)])

@@ -29,14 +29,19 @@ def route(tmp_path_factory):
 @pytest.mark.parametrize("kernel", list(q4.KERNELS))
 def test_cases_reach_their_kernel(route, kernel):
     M, N = q4.KERNELS[kernel]
-    for K in ((160, 131) if kernel == "few" else (1, 32, 160, 203)):
+    for K in ((640, 515) if kernel == "few" else (1, 32, 160, 203)):
         assert route(M, N, K, 1) == kernel
+
+
+@pytest.mark.parametrize("M,N,K", q4.FEW)
+def test_few_rows_reach_their_kernel(route, M, N, K):
+    assert route(M, N, K, 1) == "few"
 
 
 @pytest.mark.parametrize("kernel", list(q4.WIDE))
 def test_grouped_cases_reach_their_kernel(route, kernel):
     counts, N = q4.WIDE[kernel]
-    assert route(sum(counts) + 3, N, 160 if kernel == "few" else 67, len(counts)) == kernel
+    assert route(sum(counts) + 3, N, 515 if kernel == "few" else 67, len(counts)) == kernel
 
 
 @pytest.mark.parametrize("rows,N,K,groups,want", [
