@@ -352,6 +352,8 @@ template <int kForm, bool kFold>
 hipError_t by_tile(const Q4Problem& p, const Epilogue& e, hipStream_t s) {
   switch (q4_tile(p)) {
     case kTile256: return launch<Tiles<256, 256, 64, 128, 1, 1, kForm, kFold>>(p, e, s);
+    case kTile256x192: return launch<Tiles<256, 192, 64, 96, 1, 1, kForm, kFold>>(p, e, s);
+    case kTile256x128: return launch<Tiles<256, 128, 64, 64, 1, 1, kForm, kFold>>(p, e, s);
     case kTile128: return launch<Tiles<128, 128, 64, 64, 2, 1, kForm, kFold>>(p, e, s);
     case kTile64x128: return launch<Tiles<64, 128, 32, 64, 2, 2, kForm, kFold>>(p, e, s);
     case kTile64: return launch<Tiles<64, 64, 32, 32, 4, 2, kForm, kFold>>(p, e, s);

@@ -10,7 +10,9 @@
 
 namespace gemmf32 {
 
-enum Q4Tile { kTile256, kTile128, kTile64x128, kTile64, kTile32x64, kTile32 };
+enum Q4Tile {
+  kTile256, kTile256x192, kTile256x128, kTile128, kTile64x128, kTile64, kTile32x64, kTile32
+};
 
 struct Q4TileCost {
   int rows, cols;
@@ -19,10 +21,11 @@ struct Q4TileCost {
 
 // A CU holds one workgroup of each tile, so a product takes as long as the rounds its
 // workgroups make, times the round's time, which grows with K alike for all of them
-// (measured at K = 4096 with e8m0 scales: 24, 31, 45, 68, 104 and 275 us; with fp16 scales
-// 27, 37, 53, 78, 126 and 333 us).
-constexpr Q4TileCost kQ4Tiles[] = {{256, 256, 1150}, {128, 128, 435}, {64, 128, 285},
-                                   {64, 64, 190},    {32, 64, 132},   {32, 32, 100}};
+// (measured at K = 4096 in the table's order, with e8m0 scales: 281, 232, 199, 104, 68, 45, 31
+// and 24 us; with fp16 or bf16 scales 339, 289, 223, 126, 78, 53, 37 and 27 us).
+constexpr Q4TileCost kQ4Tiles[] = {{256, 256, 1170}, {256, 192, 990}, {256, 128, 825},
+                                   {128, 128, 435},  {64, 128, 285},  {64, 64, 190},
+                                   {32, 64, 132},    {32, 32, 100}};
 
 // Rounds of a tile: the groups' last row tiles are counted half full.
 inline int64_t q4_rounds(const Q4Problem& p, const Q4TileCost& t) {

@@ -227,7 +227,8 @@ def test_large_and_small_values(gpu_lib):
 
 # rows x columns that reach each kernel (test_q4_routes_host.py asks the rules)
 KERNELS = {"few": (10, 1000), "32x32": (60, 4000), "32x64": (126, 4090), "64x64": (250, 4090),
-           "64x128": (500, 4090), "128x128": (1000, 4090), "256x256": (4000, 4090)}
+           "64x128": (500, 4090), "128x128": (1000, 4090), "256x128": (2000, 4090),
+           "256x192": (4000, 2990), "256x256": (4000, 4090)}
 
 
 @pytest.mark.parametrize("kernel", list(KERNELS))
@@ -321,6 +322,8 @@ def test_grouped(gpu_lib, name, form, K, N):
 WIDE = {"few": ([3, 0, 9, 21, 1, 8], 700), "32x32": ([40, 7, 0, 33], 1000),
         "32x64": ([70, 33, 0, 20], 2000), "64x64": ([130, 64, 0, 40], 2900),
         "64x128": ([300, 65, 7, 64], 4000), "128x128": ([500, 129, 3, 128], 4000),
+        "256x128": ([1100, 257, 3, 400], 4000),
+        "256x192": ([1500, 300, 0, 1100, 900, 1400, 7, 2900], 1000),
         "256x256": ([1500, 257, 3, 2000], 4000)}
 
 

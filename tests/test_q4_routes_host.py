@@ -47,7 +47,8 @@ def test_grouped_cases_reach_their_kernel(route, kernel):
 @pytest.mark.parametrize("rows,N,K,groups,want", [
     (1, 8192, 8192, 1, "few"), (1, 8192, 127, 1, "32x32"), (8, 28672, 8192, 1, "few"),
     (24, 4096, 4096, 1, "32x32"), (32, 1024, 4096, 1, "few"), (4096, 4096, 4096, 1, "256x256"),
-    (192, 2048, 1024, 32, "few"), (8192, 1024, 2048, 8, "256x256"),
+    (192, 2048, 1024, 32, "few"), (8192, 1024, 2048, 8, "256x192"),
+    (2048, 4096, 4096, 1, "256x128"),
     (1000, 4096, 64, 1, "128x128"), (2147418112, 2147418112, 1, 1, "256x256"),
     (2147418112, 1000, 4096, 1024, "256x256")])
 def test_choices(route, rows, N, K, groups, want):
