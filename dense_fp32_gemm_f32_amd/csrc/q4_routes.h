@@ -21,11 +21,11 @@ struct Q4TileCost {
 
 // A CU holds one workgroup of each tile, so a product takes as long as the rounds its
 // workgroups make, times the round's time, which grows with K alike for all of them
-// (measured at K = 4096 in the table's order, with e8m0 scales: 281, 232, 199, 104, 68, 45, 31
-// and 24 us; with fp16 or bf16 scales 339, 289, 223, 126, 78, 53, 37 and 27 us).
-constexpr Q4TileCost kQ4Tiles[] = {{256, 256, 1170}, {256, 192, 990}, {256, 128, 825},
-                                   {128, 128, 435},  {64, 128, 285},  {64, 64, 190},
-                                   {32, 64, 132},    {32, 32, 100}};
+// (measured at K = 4096 in the table's order, with e8m0 scales: 292, 238, 189, 107, 70, 47, 33
+// and 26 us; with fp16 scales 343, 284, 220, 130, 75, 51, 38 and 28 us).
+constexpr Q4TileCost kQ4Tiles[] = {{256, 256, 1180}, {256, 192, 970}, {256, 128, 760},
+                                   {128, 128, 440},  {64, 128, 270},  {64, 64, 185},
+                                   {32, 64, 130},    {32, 32, 100}};
 
 // Rounds of a tile: the groups' last row tiles are counted half full.
 inline int64_t q4_rounds(const Q4Problem& p, const Q4TileCost& t) {
