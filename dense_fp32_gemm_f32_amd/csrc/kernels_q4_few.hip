@@ -43,8 +43,9 @@ static_assert((kLdsBytes - sum_bytes(2)) / (3 * kQ4FewRowsDeep * 256) >= kWaves 
               (kLdsBytes - sum_bytes(3)) / (3 * kQ4FewRows * 256) >= kWaves / 2, "room for parts");
 static_assert(kWaves == 1 << kQ4FewWavesLog2 && kChunkK == kQ4FewK, "as the rules count them");
 
-template <int RT, int kForm, int kScales, int kBytes>
+template <int RT, int kForm, int kScales, int kType>
 struct Few {
+  static constexpr int kBytes = kType == kScaleF32 ? 4 : kType == kScaleE8m0 ? 1 : 2;
   using It = Item<kScales, kBytes>;
   const Q4Problem& p;
   const Weights w;
@@ -55,6 +56,7 @@ struct Few {
   int rows, R;                         // of the tile, and of parts
   int pass;                            // chunks whose parts are in LDS at once
   char *lds, *parts;
+  const char* own[RT];   // this lane's parts of the first step
   int *row_of, *row_to;   // rows of A and C, -1: none
 
   __device__ __forceinline__ Few(const Q4Problem& p, int group, char* lds, int* row_of)
@@ -157,17 +159,12 @@ struct Few {
       const bf16x8 b = weights8<kForm, false>(codes[i], zero, 1.f);
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
-        // (rows behind the parts' last read that one: their sums are not used)
-        const int q = min(16 * t + (lane & 15), R - 1);
-        const bf16x8 a = *reinterpret_cast<const bf16x8*>(
-            parts + (((step0 + i) * 4 + (lane >> 4)) * R + q) * 16);
+        const bf16x8 a = *reinterpret_cast<const bf16x8*>(own[t] + (step0 + i) * 64 * R);
         const f32x4 none = {0.f, 0.f, 0.f, 0.f};
         sum[t] = mfma16(a, b, i % kPer ? sum[t] : none);
       }
       if (i % kPer == kPer - 1) {
-        const float scale = scale_value(field(it.scale, s, kBytes),
-                                        kBytes == 4 ? kScaleF32 : kBytes == 1 ? kScaleE8m0
-                                                                              : p.scale_type);
+        const float scale = scale_value(field(it.scale, s, kBytes), kType);
 #pragma unroll
         for (int t = 0; t < RT; ++t) acc[t] += sum[t] * scale;
       }
@@ -236,6 +233,10 @@ struct Few {
                                       int step, int strips) {
     rows = rows_;
     R = 3 * rows;
+    // (rows behind the parts' last read that one: their sums are not used)
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+      own[t] = parts + ((lane >> 4) * R + min(16 * t + (lane & 15), R - 1)) * 16;
     __syncthreads();   // the tile before is done with LDS
     if (tid < rows) {
       const int place = first + tid;
@@ -305,7 +306,7 @@ struct Few {
   }
 };
 
-template <int kForm, int kScales, int kBytes>
+template <int kForm, int kScales, int kType>
 __global__ void __launch_bounds__(kThreads, 4) q4_few_kernel(Q4Problem p, Epilogue ep) {
   __shared__ __attribute__((aligned(16))) char lds[kLdsBytes];
   __shared__ int row_of[2 * kQ4FewRows];
@@ -325,15 +326,15 @@ __global__ void __launch_bounds__(kThreads, 4) q4_few_kernel(Q4Problem p, Epilog
       few.run(ep, first, rows, blockIdx.x, gridDim.x, (int)(((int64_t)p.g.N + wide - 1) / wide));
     };
     if (rows <= 5)
-      run(Few<1, kForm, kScales, kBytes>(p, group, lds, row_of));
+      run(Few<1, kForm, kScales, kType>(p, group, lds, row_of));
     else if (rows <= 10)
-      run(Few<2, kForm, kScales, kBytes>(p, group, lds, row_of));
+      run(Few<2, kForm, kScales, kType>(p, group, lds, row_of));
     else
-      run(Few<3, kForm, kScales, kBytes>(p, group, lds, row_of));
+      run(Few<3, kForm, kScales, kType>(p, group, lds, row_of));
   }
 }
 
-template <int kForm, int kScales, int kBytes>
+template <int kForm, int kScales, int kType>
 hipError_t launch(const Q4Problem& p, const Epilogue& e, hipStream_t s) {
   const int tiles = p.g.offsets ? 1 : (p.g.rows + q4_few_rows(p) - 1) / q4_few_rows(p);
   const int wide = 16 * kWaves >> q4_waves_along_k(p);
@@ -343,15 +344,16 @@ hipError_t launch(const Q4Problem& p, const Epilogue& e, hipStream_t s) {
   const int64_t each = (strips + most - 1) / most;
   const dim3 grid((unsigned)((strips + each - 1) / each), (unsigned)p.g.groups,
                   (unsigned)(tiles < 1024 ? tiles : 1024));
-  q4_few_kernel<kForm, kScales, kBytes><<<grid, kThreads, 0, s>>>(p, e);
+  q4_few_kernel<kForm, kScales, kType><<<grid, kThreads, 0, s>>>(p, e);
   return hipGetLastError();
 }
 
 template <int kForm, int kScales>
 hipError_t by_type(const Q4Problem& p, const Epilogue& e, hipStream_t s) {
-  if (p.scale_type == kScaleF32) return launch<kForm, kScales, 4>(p, e, s);
-  if (p.scale_type == kScaleE8m0) return launch<kForm, kScales, 1>(p, e, s);
-  return launch<kForm, kScales, 2>(p, e, s);
+  if (p.scale_type == kScaleF32) return launch<kForm, kScales, kScaleF32>(p, e, s);
+  if (p.scale_type == kScaleE8m0) return launch<kForm, kScales, kScaleE8m0>(p, e, s);
+  if (p.scale_type == kScaleBf16) return launch<kForm, kScales, kScaleBf16>(p, e, s);
+  return launch<kForm, kScales, kScaleF16>(p, e, s);
 }
 template <int kForm>
 hipError_t by_group(const Q4Problem& p, const Epilogue& e, hipStream_t s) {
