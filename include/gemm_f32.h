@@ -470,8 +470,10 @@ int gemm_f32_join_rows_grad(int64_t tokens, int64_t top, int64_t N,
  * split into three bf16 values exactly, a weight without its scale is one exactly,
  * and their products are summed in fp32, a group's sum first, then times its scale.
  * (So a group's sum of a * code must not pass the largest float, also where the
- * scale would bring it back.)  Values that are not finite give what the formula
- * gives.
+ * scale would bring it back.  e8m0 scales may go into the weights first: a weight
+ * that passes the largest float, as 6 * 2^127 does, gives a result that is not
+ * finite.  Of an a below 2^-110 the lowest bits may be lost.)  Values that are not
+ * finite give what the formula gives.
  *
  * Errors as gemm_f32_fused; an unknown format or scale type, a group that is no
  * power of two or below 32, zero points with e2m1 GEMM_F32_ERR_INVALID_ARG; ldq

@@ -244,6 +244,25 @@ def test_every_kernel(gpu_lib, kernel, form, kind):
           bias=True, act=1)
 
 
+@pytest.mark.parametrize("kernel", list(KERNELS))
+def test_smallest_and_largest_powers(gpu_lib, kernel):
+    """e8m0 scales from the subnormal 2^-127 to the last that keeps every weight finite."""
+    M, N = KERNELS[kernel]
+    K = 640 if kernel == "few" else 64
+    g = gen(M)
+    a = torch.randint(-2, 3, (M, K), generator=g).float()
+    packed = torch.randint(0, 256, (N, K // 2), generator=g, dtype=torch.uint8)
+    for fmt, most in ((INT, 251), (E2M1, 252)):
+        ones = torch.full((N, K // 32), 127, dtype=torch.uint8)
+        W = q4.dequantize(packed, ones, K, group=32, format=fmt).double()
+        want = a.double() @ W.t()
+        for e, size in ((0, 2.0 ** 100), (1, 2.0 ** 100), (127, 1.0), (most, 2.0 ** -40)):
+            H.say(f"q4 powers {kernel} format={fmt} e={e}")
+            got = binding.gemm_q4((a * size).cuda(), packed.cuda(),
+                                  torch.full_like(ones, e).cuda(), group=32, format=fmt)
+            assert torch.equal(got.cpu().double(), want * size * 2.0 ** (e - 127))
+
+
 # rows, columns, K of the kernel for few rows: its row tiles of each size, one and more of
 # them, all and some of its waves along K, K in one pass and in several
 FEW = [(M, N, K) for M in (1, 5, 6, 10, 11, 16) for N, K in ((1000, 2100), (8192, 1031),
