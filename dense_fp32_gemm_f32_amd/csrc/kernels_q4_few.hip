@@ -1,18 +1,21 @@
 // Products with 4-bit weights for few rows (q4_routes.h) and at least 128 k: tiles of up
-// to 16 rows.  Bound by the read of the codes: one row of 8192 x 8192 takes 16 us (33.5 MB
-// of codes, 2.2 TB/s), 28672 x 8192 38 us (3.1 TB/s), where loads alone in the same order
-// take 33 us.
+// to 20 rows.  Bound by the conversion of the codes (95 vector instructions for 2048 of
+// them) beside their read: one row of 8192 x 8192 takes 17.5 us from HBM (33.5 MB of codes,
+// 2.0 TB/s; 15.0 us from the last-level cache), one of 28672 x 8192 45 us (2.7 TB/s), where
+// loads alone in the same order take 33 us.
 //
-// The rows' three bf16 parts are the rows of the matrix instruction: row r's part
-// p is row 3 r + p, so that up to 5 rows of A take one instruction for 16 columns
-// by 32 k, up to 10 two.  A workgroup splits its rows once, into LDS, and goes through
-// strips of columns with them (rows whose parts do not fit take K in passes, for each
-// strip anew).  A wave takes 16 columns and every kw-th chunk of 128 k, 16 bytes of
-// codes a lane; the kw waves of a strip add their sums through LDS in one order, and
-// the 16 / kw others have the strips beside it.  Each wave has the codes and scales
-// of its next two chunks on the way into registers, whichever strip they are of
-// (four chunks were no faster).  With 8 waves a workgroup 8192 x 8192 took 19 us, as
-// fewer loads are on the way.
+// The rows' three bf16 parts are rows of the matrix instruction: a row has four of its
+// 16, of which the last is not used, so that a lane gets the sums of one row's parts and
+// adds them by itself; 4 rows of A take one instruction for 16 columns by 32 k.  (With
+// all 16 in use, 5 rows and a third, the sums went through LDS whole, three times as
+// many.)  A workgroup splits its rows once, into LDS, and goes through strips
+// of columns with them (rows whose parts do not fit take K in passes, for each strip
+// anew).  A wave takes 16 columns and every kw-th chunk of 128 k, 16 bytes of codes a
+// lane; the kw waves of a strip add their sums through LDS in one order, and the 16 / kw
+// others have the strips beside it.  Each wave has the codes and scales of its next two
+// chunks on the way into registers, whichever strip they are of (four chunks were no
+// faster, nor were two chunks of one line of codes in turn).  With 8 waves a workgroup
+// the row of 8192 x 8192 took 19 us where it took 16, as fewer loads are on the way.
 #include "q4_common.h"
 #include "q4_routes.h"
 
@@ -26,10 +29,12 @@ using namespace q4;
 constexpr int kWavesLog2 = kQ4FewWavesLog2, kWaves = 1 << kWavesLog2, kThreads = kWaves * 64;
 constexpr int kChunkK = 128;         // k of a chunk: four steps of 32
 constexpr int kAhead = 2;            // chunks on the way
-// the waves' sums (1 KiB a wave and 16 rows of parts; two buffers of them, so that a
-// strip takes one barrier, for 16 rows), then the parts; one workgroup to a CU
+constexpr int kRowsT = 4;            // rows of an instruction
+// the waves' sums (of rt instructions, 4 bytes a lane; two buffers, so that a strip takes
+// one barrier, where that leaves the parts room), then the parts; one workgroup to a CU
 constexpr int kLdsBytes = 158 * 1024;
-constexpr int sum_bytes(int rt) { return (rt < 2 ? 2 : rt) * kWaves * 1024; }
+constexpr int buffers(int rt) { return rt <= 2 ? 2 : 1; }
+constexpr int sum_bytes(int rt) { return buffers(rt) * rt * kThreads * 4; }
 
 // kScales: scales of a chunk (1 for groups of 128 and more), of kBytes bytes each.
 template <int kScales, int kBytes>
@@ -39,8 +44,12 @@ struct Item {
 };
 
 // a chunk for every wave along K
-static_assert((kLdsBytes - sum_bytes(2)) / (3 * kQ4FewRowsDeep * 256) >= kWaves &&
-              (kLdsBytes - sum_bytes(3)) / (3 * kQ4FewRows * 256) >= kWaves / 2, "room for parts");
+constexpr int chunks_in_lds(int rt, int rows) {
+  return (kLdsBytes - sum_bytes(rt)) / (3 * rows * 256);
+}
+static_assert(chunks_in_lds(3, kQ4FewRowsDeep) >= kWaves &&
+              chunks_in_lds(5, kQ4FewRows) >= kWaves / 2, "room for parts");
+static_assert(kQ4FewRowsDeep == 3 * kRowsT && kQ4FewRows == 5 * kRowsT, "as launched");
 static_assert(kWaves == 1 << kQ4FewWavesLog2 && kChunkK == kQ4FewK, "as the rules count them");
 
 template <int RT, int kForm, int kScales, int kType>
@@ -199,33 +208,45 @@ struct Few {
     }
   }
 
-  // The waves' sums of a strip added and stored; buffer 0 and 1 in turn.
+  __device__ __forceinline__ void put(const Epilogue& ep, int row, int64_t n, float v) const {
+    const int to = row_to[row];
+    if (n >= p.g.N || to < 0) return;
+    float* out = p.g.C + to * p.g.ldc + n;
+    *out = epilogue_apply(ep, row_of[row] >= 0 ? v : 0.f, out, n);
+  }
+
+  // The sums of a strip stored, those of the waves along K added: a lane has the three
+  // parts' of row lane / 16 of each instruction.  Buffer 0 and 1 in turn.
   __device__ __forceinline__ void store(const Epilogue& ep, int strip, int buffer,
                                         f32x4 (&acc)[RT]) const {
     const int kw = 1 << kw_log2, wide = 16 * kWaves >> kw_log2;   // columns of the strip
-    const int64_t n0 = (int64_t)strip * wide + tid % wide;   // this thread's column
-    float* red = reinterpret_cast<float*>(lds) + (RT == 1 ? buffer * (sum_bytes(1) / 8) : 0);
+    const int64_t n0 = (int64_t)strip * wide;
+    float v[RT];
 #pragma unroll
-    for (int t = 0; t < RT; ++t)
+    for (int t = 0; t < RT; ++t) v[t] = acc[t][0] + acc[t][1] + acc[t][2];
+    if (kw == 1) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        red[((wave * RT + t) * 16 + 4 * (lane >> 4) + r) * 16 + (lane & 15)] = acc[t][r];
-    __syncthreads();
-    if (n0 < p.g.N)
-      for (int r = tid / wide; r < rows; r += kThreads / wide) {
-        const int c = tid % wide, to = row_to[r];
-        float v = 0.f;
-        const float* from = red + ((((c >> 4) << kw_log2) * RT * 16 + 3 * r) * 16 + (c & 15));
-#pragma unroll 4
-        for (int i = 0; i < kw; ++i)
-#pragma unroll
-          for (int part = 0; part < 3; ++part) v += from[(i * RT * 16 + part) * 16];
-        if (to >= 0) {
-          float* out = p.g.C + to * p.g.ldc + n0;
-          *out = epilogue_apply(ep, row_of[r] >= 0 ? v : 0.f, out, n0);
-        }
+      for (int t = 0; t < RT; ++t) {
+        const int row = kRowsT * t + (lane >> 4);
+        if (row < rows) put(ep, row, n0 + 16 * wave + (lane & 15), v[t]);
       }
-    if (RT > 1) __syncthreads();
+      return;
+    }
+    // row r of wave w at (r / 4 * kWaves + w) 64 + r % 4 * 16
+    float* red = reinterpret_cast<float*>(lds) + (buffers(RT) == 2 ? buffer * RT * kThreads : 0);
+#pragma unroll
+    for (int t = 0; t < RT; ++t) red[t * kThreads + tid] = v[t];
+    __syncthreads();
+    const int c = tid % wide;
+    for (int r = tid / wide; r < rows; r += kThreads / wide) {
+      const float* from = red + (r / kRowsT * kWaves + (c >> 4 << kw_log2)) * 64 +
+                          r % kRowsT * 16 + (c & 15);
+      float sum = 0.f;
+#pragma unroll 8
+      for (int i = 0; i < kw; ++i) sum += from[i * 64];
+      put(ep, r, n0 + c, sum);
+    }
+    if (buffers(RT) == 1) __syncthreads();
   }
 
   // Places first .. first + rows - 1, every step-th strip from `strip` on.
@@ -233,10 +254,13 @@ struct Few {
                                       int step, int strips) {
     rows = rows_;
     R = 3 * rows;
-    // (rows behind the parts' last read that one: their sums are not used)
+    // (the fourth of a row, and rows behind the last, read another part: their sums are
+    // not used)
 #pragma unroll
-    for (int t = 0; t < RT; ++t)
-      own[t] = parts + ((lane >> 4) * R + min(16 * t + (lane & 15), R - 1)) * 16;
+    for (int t = 0; t < RT; ++t) {
+      const int q = 3 * (kRowsT * t + (lane >> 2 & 3)) + min(lane & 3, 2);
+      own[t] = parts + ((lane >> 4) * R + min(q, R - 1)) * 16;
+    }
     __syncthreads();   // the tile before is done with LDS
     if (tid < rows) {
       const int place = first + tid;
@@ -325,12 +349,16 @@ __global__ void __launch_bounds__(kThreads, 4) q4_few_kernel(Q4Problem p, Epilog
       const int wide = 16 * kWaves >> few.kw_log2;
       few.run(ep, first, rows, blockIdx.x, gridDim.x, (int)(((int64_t)p.g.N + wide - 1) / wide));
     };
-    if (rows <= 5)
+    if (rows <= kRowsT)
       run(Few<1, kForm, kScales, kType>(p, group, lds, row_of));
-    else if (rows <= 10)
+    else if (rows <= 2 * kRowsT)
       run(Few<2, kForm, kScales, kType>(p, group, lds, row_of));
-    else
+    else if (rows <= 3 * kRowsT)
       run(Few<3, kForm, kScales, kType>(p, group, lds, row_of));
+    else if (rows <= 4 * kRowsT)
+      run(Few<4, kForm, kScales, kType>(p, group, lds, row_of));
+    else
+      run(Few<5, kForm, kScales, kType>(p, group, lds, row_of));
   }
 }
 

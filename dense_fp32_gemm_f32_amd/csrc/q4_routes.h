@@ -49,7 +49,7 @@ inline Q4Tile q4_tile(const Q4Problem& p) {
 
 constexpr int kQ4FewK = 128;   // the least K that the kernel for few rows takes, and its chunk
 constexpr int kQ4FewWavesLog2 = 4;
-constexpr int kQ4FewRows = 16, kQ4FewRowsDeep = 10;
+constexpr int kQ4FewRows = 20, kQ4FewRowsDeep = 12;
 
 #if defined(__HIP__)
 #define GEMM_F32_BOTH __host__ __device__
@@ -77,13 +77,14 @@ GEMM_F32_BOTH inline int q4_few_rows(const Q4Problem& p) {
 
 // Whether the kernel for few rows (kernels_q4_few.hip) is the faster one, by its time in
 // the tiles' unit: with e strips of columns for each workgroup, c columns of 16 in them,
-// and r rows a row tile takes 12 + 2 r + c (9 + 0.8 r), and 18 for each strip where all
+// and r rows a row tile takes 12 + 2 r + c (9 + 0.8 r), and 14 for each strip where all
 // waves go along K.  Row tiles of one matrix go beside each other, those of a group one
 // after another; uneven groups are counted half as long again as their average.
-// (Few against tiles in us, e8m0 scales.  4096 x 4096: 8 rows 14 against 24, 16 rows 22
-// against 23, 24 rows 39 against 24; 8192 x 8192: 8 rows 25 against 40, 16 rows 41 against
-// 40, 24 rows 63 against 41; 28672 x 8192: 16 rows 95 against 104, 17 rows 117 against 104;
-// 2048 x 1024 in 32 groups: 6 rows each 17 against 48, 20 rows 32 against 48.)
+// (Few against tiles in us, e8m0 scales.  4096 x 4096: 8 rows 14 against 26, 16 rows 22
+// against 26, 24 rows 28 against 26; 8192 x 8192: 8 rows 26 against 40, 12 rows 32 against
+// 40, 16 rows 42 against 40, 24 rows 57 against 41; 28672 x 8192: 16 rows 99 against 104,
+// 24 rows 148 against 106; 2048 x 1024 in 32 groups: 6 rows each 17 against 47, 32 rows 42
+// against 48.)
 inline bool q4_few(const Q4Problem& p) {
   if (p.g.K < kQ4FewK) return false;
   const int waves = 1 << kQ4FewWavesLog2, wide = waves >> q4_waves_along_k(p);
@@ -96,7 +97,7 @@ inline bool q4_few(const Q4Problem& p) {
   const double e = up(strips, std::max(1.0, std::floor(256 / beside)));
   const double rounds = up(beside * up(strips, e), 256);
   const double time =
-      12 + 2 * r + e * wide * (9 + 0.8 * r) + (wide == 1 ? 18 * e : 0.0);
+      12 + 2 * r + e * wide * (9 + 0.8 * r) + (wide == 1 ? 14 * e : 0.0);
   return time * rounds * turns < 0.9 * (double)q4_tile_cost(p, q4_tile(p));
 }
 

@@ -265,9 +265,9 @@ def test_smallest_and_largest_powers(gpu_lib, kernel):
 
 # rows, columns, K of the kernel for few rows: its row tiles of each size, one and more of
 # them, all and some of its waves along K, K in one pass and in several
-FEW = [(M, N, K) for M in (1, 5, 6, 10, 11, 16) for N, K in ((1000, 2100), (8192, 1031),
-                                                             (33, 16400), (28672, 1031))]
-FEW += [(17, 1000, 2100), (33, 1000, 640), (40, 300, 2100), (150, 16, 4096)]
+FEW = [(M, N, K) for M in (1, 4, 5, 8, 9, 12, 13, 16) for N, K in ((1000, 2100), (8192, 1031),
+                                                                   (33, 16400), (28672, 1031))]
+FEW += [(17, 28672, 515), (17, 1000, 2100), (30, 1000, 640), (40, 300, 2100), (150, 16, 4096)]
 
 
 @pytest.mark.parametrize("M,N,K", FEW)
@@ -338,7 +338,7 @@ def test_grouped(gpu_lib, name, form, K, N):
 
 
 # uneven groups whose sizes reach each tile: (counts, N)
-WIDE = {"few": ([3, 0, 9, 21, 1, 8], 700), "32x32": ([40, 7, 0, 33], 1000),
+WIDE = {"few": ([3, 0, 9, 20, 1, 8], 700), "32x32": ([40, 7, 0, 33], 1000),
         "32x64": ([70, 33, 0, 20], 2000), "64x64": ([130, 64, 0, 40], 2900),
         "64x128": ([300, 65, 7, 64], 4000), "128x128": ([500, 129, 3, 128], 4000),
         "256x128": ([1100, 257, 3, 400], 4000),
