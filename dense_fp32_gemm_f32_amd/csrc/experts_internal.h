@@ -23,7 +23,7 @@ struct RouteProblem {
   const float* bias = nullptr;       // NULL: none
   int64_t ldl = 0;
   int tokens = 0, experts = 0, top = 0;
-  int groups = 1, group_top = 1, group_best = 1;
+  int groups = 1, group_size = 0, group_top = 1, group_best = 1;   // experts = groups group_size
   bool sigmoid = false, renorm = false;
   float scale = 1.f;
   int* choice = nullptr;             // tokens x top

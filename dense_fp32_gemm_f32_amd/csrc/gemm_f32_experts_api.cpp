@@ -234,6 +234,7 @@ int gemm_f32_route(int64_t tokens, int64_t experts, int64_t top, const float* lo
   p.experts = (int)experts;
   p.top = (int)top;
   p.groups = (int)groups;
+  p.group_size = (int)(experts / groups);
   p.group_top = (int)group_top;
   p.group_best = group_best;
   p.sigmoid = score == GEMM_F32_SCORE_SIGMOID;
