@@ -1,14 +1,14 @@
 // The norm of many arrays, sqrt(sum of squares), and the arrays scaled so that it
 // is at most a limit.
 //
-// The arrays are cut into chunks, a workgroup takes every grid-th chunk, and its sum of squares goes to the workspace; the next launch
-// adds all of them, each of its workgroups alone and in one order, so nothing is
-// counted or waited for and the result depends on the sizes only.  Squares are
-// added in 64 bits, which no float's square leaves: the sum neither overflows nor
-// loses small arrays beside large ones, and at 8 bytes of arithmetic for 4 of
-// memory costs nothing beside the read.  Bound by HBM: one read for the norm, and
-// a read and a write for the scaled arrays: those 264 M floats' norm takes 187 us (5.6 TB/s),
-// the norm and the scaled arrays 585 us (5.4 TB/s).
+// The arrays are cut into chunks, a workgroup takes every grid-th chunk, and its sum of
+// squares goes to the workspace; the next launch adds all of them, each of its
+// workgroups alone and in one order, so nothing is counted or waited for and the result
+// depends on the sizes only.  Squares are added in 64 bits, which no float's square
+// leaves: the sum neither overflows nor loses small arrays beside large ones, and at 8
+// bytes of arithmetic for 4 of memory costs nothing beside the read.  Bound by HBM: one
+// read for the norm, and a read and a write for the scaled arrays.  264 M floats' norm
+// takes 187 us (5.6 TB/s), the norm and the scaled arrays 585 us (5.4 TB/s).
 #include "experts_internal.h"
 
 namespace gemmf32 {

@@ -73,7 +73,8 @@ struct Few {
         along((int)(((int64_t)p.g.K - 1) >> p.group_shift) + 1),
         chunks((int)(((int64_t)p.g.K + kChunkK - 1) / kChunkK)),
         tid(threadIdx.x), wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)),
-        lane(threadIdx.x & 63), lds(lds), parts(lds + sum_bytes(RT)), row_of(row_of), row_to(row_of + kQ4FewRows) {
+        lane(threadIdx.x & 63), lds(lds), parts(lds + sum_bytes(RT)), row_of(row_of),
+        row_to(row_of + kQ4FewRows) {
     kw_log2 = q4_waves_along_k(p);
     kwave = wave & ((1 << kw_log2) - 1);
     side = wave >> kw_log2;
@@ -119,7 +120,8 @@ struct Few {
   // scales behind the row's last meet parts that are zero.
   __device__ __forceinline__ void settle(It& it, int64_t k0) const {
     const int64_t want = k0 / 2 + 16 * (lane >> 4);
-    const int by = (int)(want - min(want, (int64_t)row_bytes - 16));   // bytes, 16 and more: all behind
+    // bytes, 16 and more: all behind
+    const int by = (int)(want - min(want, (int64_t)row_bytes - 16));
     u32x4 v = it.codes;
 #pragma unroll
     for (int d = 0; d < 4; ++d) {

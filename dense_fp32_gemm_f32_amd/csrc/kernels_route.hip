@@ -11,8 +11,8 @@
 //
 // Each lane sorts its keys once; a choice is then the largest head of 64 lists, six DPP
 // steps and a pop.  Bound by the vector instructions: 16384 x 256, 8 choices, take 11 us
-// without a bias (two passes over the row in 64 bits took 50), 14 with one, 19 with the
-// best 4 of 8 groups; the read of the logits alone would take 3.5.
+// without a bias, 14 with one, 19 with the best 4 of 8 groups (54 where every choice was
+// made in 64 bits); the read of the logits alone would take 3.5.
 #include "experts_internal.h"
 
 #include <cfloat>

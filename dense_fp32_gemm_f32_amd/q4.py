@@ -65,8 +65,9 @@ def quantize(W, *, group=128, format=Q4_INT, symmetric=True, scale_dtype=torch.f
     if scale_dtype == torch.uint8:
         scale = (torch.ceil(torch.log2(size)) + 127).clamp(0, 254).to(torch.uint8)
     else:
-        scale = size.to(scale_dtype)
+        scale = size.clamp_max(torch.finfo(scale_dtype).max).to(scale_dtype)
     by = scale_values(scale).unsqueeze(-1)
+    by = torch.where(by > 0, by, torch.ones_like(by))   # too small for the type: zeros
     if format == Q4_E2M1:
         steps = torch.tensor(E2M1[:8], device=W.device)
         x = (w / by).abs()

@@ -290,6 +290,17 @@ def test_quantize_stays_within_half_a_step(kind, form, group, K):
     assert torch.equal(back[0, 0], torch.zeros(K, dtype=torch.float64))
 
 
+@pytest.mark.parametrize("size", [1e-9, 1e30])
+@pytest.mark.parametrize("symmetric", [True, False])
+def test_quantize_past_the_scale_type(size, symmetric):
+    """Groups whose scale fp16 cannot hold: zeros below, the largest scale above."""
+    W = torch.linspace(-1, 1, 64).view(2, 32) * size
+    codes, scale, zero = q4.quantize(W, group=32, symmetric=symmetric, scale_dtype=torch.float16)
+    back = q4.dequantize(codes, scale, 32, zero=zero, group=32)
+    assert bool(scale.isfinite().all()) and bool(back.isfinite().all())
+    assert bool((back.abs() <= W.abs().max()).all())
+
+
 def test_dequantize_by_hand():
     codes = q4.pack(torch.tensor([[0, 15, 8, 3]]))
     scale = torch.tensor([[0.5]])
