@@ -564,6 +564,42 @@ def test_captured_calls_replay(gpu_lib):
             stream.synchronize()
 
 
+def test_calls_on_streams_at_once(gpu_lib):
+    """The calls in turn on four streams, each with its inputs: as one after another."""
+    H.say("calls on streams at once")
+    T, E, top, N, K = 300, 64, 4, 520, 384
+    streams = [torch.cuda.Stream() for _ in range(4)]
+
+    def inputs(seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        draw = lambda *s: torch.randn(*s, generator=g, device="cuda")
+        codes = torch.randint(0, 256, (N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+        return dict(logits=draw(T, E), bias=draw(E), h=draw(T * top, N), a=draw(T, K),
+                    codes=codes, scale=draw(N, K // 32).abs(),
+                    grads=[draw(n) for n in (70001, 3, 200000)])
+
+    def calls(x):
+        choice, weight = binding.route(x["logits"], top, bias=x["bias"], score=SIGMOID)
+        y = binding.join_rows(x["h"], weight, choice, groups=E)
+        few = binding.gemm_q4(x["a"][:3], x["codes"], x["scale"], group=32)
+        many = binding.gemm_q4(x["a"], x["codes"], x["scale"], group=32)
+        outs = [torch.empty_like(t) for t in x["grads"]]
+        return [choice, weight, y, few, many, binding.clip_norm(x["grads"], 5.0, out=outs), *outs]
+
+    sets = [inputs(seed) for seed in range(4)]
+    want = [calls(x) for x in sets]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for stream, x in zip(streams, sets):
+            with torch.cuda.stream(stream):
+                got.append(calls(x))
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            for u, v in zip(a, b):
+                assert torch.equal(u, v)
+
+
 def test_clip_needs_its_workspace_before_capture(gpu_lib):
     H.say("clip captured without a workspace")
     x = [torch.ones(1000, device="cuda")]
