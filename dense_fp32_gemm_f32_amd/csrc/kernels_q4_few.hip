@@ -1,8 +1,8 @@
 // Products with 4-bit weights for few rows (q4_routes.h) and at least 128 k: tiles of up
 // to 20 rows.  Bound by the conversion of the codes (95 vector instructions for 2048 of
-// them) beside their read: one row of 8192 x 8192 takes 17.5 us from HBM (33.5 MB of codes,
-// 2.0 TB/s; 15.0 us from the last-level cache), one of 28672 x 8192 45 us (2.7 TB/s), where
-// loads alone in the same order take 33 us.
+// them) beside their read: one row of 8192 x 8192 takes 16.6 us from HBM (33.5 MB of codes,
+// 2.1 TB/s), one of 28672 x 8192 43 us (2.8 TB/s), where loads alone in the same order
+// take 33 us.
 //
 // The rows' three bf16 parts are rows of the matrix instruction: a row has four of its
 // 16, of which the last is not used, so that a lane gets the sums of one row's parts and
@@ -280,7 +280,7 @@ struct Few {
     };
     auto advance = [&](Position& x) {
       x.at += kw;
-      if (x.at >= min(pass, chunks - x.base)) {
+      if ((x.at >> kw_log2) % kAhead == 0 && x.at >= min(pass, chunks - x.base)) {
         x.at = 0;
         x.base += pass;
         if (x.base >= chunks) {
@@ -299,36 +299,42 @@ struct Few {
       if (ahead.strip != was) row_ahead = row(ahead.strip);
     };
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) fetch_next(items[i]);
+    for (int i = 0; i < kAhead; ++i) {
+      fetch_next(items[i]);
+      // (out of order here, the first would be waited for behind the others in the loop)
+      __builtin_amdgcn_sched_barrier(0);
+    }
     f32x4 acc[RT];
 #pragma unroll
     for (int t = 0; t < RT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
     bool staged = false;
     int buffer = 0;
-    for (;;) {
+    // kAhead steps in turn, those behind a pass's chunks empty, so that staging and
+    // storing, and the way out, stand here once: the code is fetched anew by each CU (by
+    // the step they stand in it cost up to 1 us of 17; so do four steps).
+    do {
+      if (now.at == 0 && !staged) {
+        __syncthreads();   // row_of is there; the pass before is used
+        stage(now.base, min(pass, chunks - now.base));
+        __syncthreads();
+        staged = passes == 1;
+      }
+      const int was = now.strip;
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
-        if (now.at == 0 && !staged) {
-          __syncthreads();   // row_of is there; the pass before is used
-          stage(now.base, min(pass, chunks - now.base));
-          __syncthreads();
-          staged = passes == 1;
-        }
         const int chunk = now.base + now.at + kwave;
         if (now.at + kwave < min(pass, chunks - now.base))
           multiply(items[i], chunk, (now.at + kwave) * 4, acc);
         fetch_next(items[i]);
-        const int was = now.strip;
         advance(now);
-        if (now.strip != was) {
-          store(ep, was, buffer, acc);
-          buffer ^= 1;
-#pragma unroll
-          for (int t = 0; t < RT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-          if (now.strip >= strips) return;
-        }
       }
-    }
+      if (now.strip != was) {
+        store(ep, was, buffer, acc);
+        buffer ^= 1;
+#pragma unroll
+        for (int t = 0; t < RT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+      }
+    } while (now.strip < strips);
   }
 };
 

@@ -70,9 +70,13 @@ GEMM_F32_BOTH inline int q4_waves_along_k(const Q4Problem& p) {
 }
 
 // Rows of its row tiles, at most: those whose parts of a chunk for each wave along K fit
-// into LDS.
+// into LDS, of two chunks where K takes several passes over 8 waves (8192 x 8192, 16 rows:
+// 47 us with one).
 GEMM_F32_BOTH inline int q4_few_rows(const Q4Problem& p) {
-  return q4_waves_along_k(p) < kQ4FewWavesLog2 ? kQ4FewRows : kQ4FewRowsDeep;
+  const int log2 = q4_waves_along_k(p);
+  const bool deep = log2 == kQ4FewWavesLog2 ||
+                    (log2 == kQ4FewWavesLog2 - 1 && p.g.K > kQ4FewK << log2);
+  return deep ? kQ4FewRowsDeep : kQ4FewRows;
 }
 
 // Whether the kernel for few rows (kernels_q4_few.hip) is the faster one, by its time in
@@ -80,11 +84,10 @@ GEMM_F32_BOTH inline int q4_few_rows(const Q4Problem& p) {
 // and r rows a row tile takes 12 + 2 r + c (9 + 0.8 r), and 14 for each strip where all
 // waves go along K.  Row tiles of one matrix go beside each other, those of a group one
 // after another; uneven groups are counted half as long again as their average.
-// (Few against tiles in us, e8m0 scales.  4096 x 4096: 8 rows 14 against 26, 16 rows 22
-// against 26, 24 rows 28 against 26; 8192 x 8192: 8 rows 26 against 40, 12 rows 32 against
-// 40, 16 rows 42 against 40, 24 rows 57 against 41; 28672 x 8192: 16 rows 99 against 104,
-// 24 rows 148 against 106; 2048 x 1024 in 32 groups: 6 rows each 17 against 47, 32 rows 42
-// against 48.)
+// (Few against tiles in us, e8m0 scales.  4096 x 4096: 8 rows 15 against 23, 12 rows 18
+// against 23, 16 rows 24 against 23; 8192 x 8192: 8 rows 25 against 39, 12 rows 32 against
+// 39, 16 rows 42 against 39; 28672 x 8192: 16 rows 97 against 97, 24 rows 148 against 96;
+// 2048 x 1024 in 32 groups: 6 rows each 17 against 47, 32 rows 42 against 48.)
 inline bool q4_few(const Q4Problem& p) {
   if (p.g.K < kQ4FewK) return false;
   const int waves = 1 << kQ4FewWavesLog2, wide = waves >> q4_waves_along_k(p);
@@ -98,7 +101,7 @@ inline bool q4_few(const Q4Problem& p) {
   const double rounds = up(beside * up(strips, e), 256);
   const double time =
       12 + 2 * r + e * wide * (9 + 0.8 * r) + (wide == 1 ? 14 * e : 0.0);
-  return time * rounds * turns < 0.9 * (double)q4_tile_cost(p, q4_tile(p));
+  return time * rounds * turns < 0.88 * (double)q4_tile_cost(p, q4_tile(p));
 }
 
 }  // namespace gemmf32

@@ -265,8 +265,9 @@ def test_smallest_and_largest_powers(gpu_lib, kernel):
 
 # rows, columns, K of the kernel for few rows: its row tiles of each size, one and more of
 # them, all and some of its waves along K, K in one pass and in several
-FEW = [(M, N, K) for M in (1, 4, 5, 8, 9, 12, 13, 16) for N, K in ((1000, 2100), (8192, 1031),
-                                                                   (33, 16400), (28672, 1031))]
+FEW = [(M, N, K) for M in (1, 4, 5, 8, 9, 12) for N, K in ((1000, 2100), (8192, 1031),
+                                                           (33, 16400), (28672, 1031))]
+FEW += [(M, N, K) for M in (13, 16) for N, K in ((1000, 2100), (4096, 1000), (28672, 1031))]
 FEW += [(17, 28672, 515), (17, 1000, 2100), (30, 1000, 640), (40, 300, 2100), (150, 16, 4096)]
 
 
