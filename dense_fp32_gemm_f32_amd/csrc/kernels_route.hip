@@ -211,8 +211,14 @@ __device__ __forceinline__ void sort_down(int (&v)[E], int (&at)[E]) {
 // of the largest score.  The addition of the bias rounds once.
 struct Margin {
   float score;   // of the difference of two scores
-  __device__ __forceinline__ bool apart(float above, float below, float terms) const {
-    return above - below > terms * (score + 0x1p-22f * fmaxf(fabsf(above), fabsf(below)));
+  __device__ __forceinline__ bool apart(float above, float below) const {
+    return above - below > score + 0x1p-22f * fmaxf(fabsf(above), fabsf(below));
+  }
+  // What a group's score a + b is off by: the additions of the bias by 2^-24 of |a| and of
+  // |b|, which the sum may be far below, their own by 2^-24 of that; as much again covers
+  // the rounding of what it is added to.  Of two groups' four scores' errors, half.
+  __device__ __forceinline__ float of_group(float a, float b) const {
+    return score + 0x1p-22f * (fabsf(a) + fabsf(b));
   }
 };
 
@@ -348,7 +354,8 @@ __device__ __forceinline__ bool choose_fast(const RouteProblem& p, const float* 
         b = max(max(b, y), min(a, x));
         a = max(a, x);
       }
-    const int score = sums && b != kNone ? key_of(of_key(a) + of_key(b)) : a;
+    const bool both = sums && b != kNone;
+    const int score = both ? key_of(of_key(a) + of_key(b)) : a;
     int rank = 0;   // groups above this lane's
     for (int g = 0; g < p.groups; ++g) {
       const int other = __builtin_amdgcn_readlane(score, g);
@@ -356,10 +363,13 @@ __device__ __forceinline__ bool choose_fast(const RouteProblem& p, const float* 
     }
     bool in = rank < p.group_top;
     if (scores) {
-      // the least of those in, as the largest of the others' complement
-      const int least = ~wave_max(in ? ~score : kNone), next = wave_max(in ? kNone : score);
-      if (next != kNone && !margin.apart(of_key(least), of_key(next), 2.f))
-        in = in_best_groups<E>(p, l, lanes, lane, lds);
+      // each group's score lies within `off` of it: the least that one in may have (as the
+      // largest of the complements), and the most that one of the others may have
+      const float x = of_key(score);
+      const float off = margin.of_group(of_key(a), both ? of_key(b) : 0.f);
+      const int low = key_of(x - off), high = score == kNone ? kNone : key_of(x + off);
+      const int least = ~wave_max(in ? ~low : kNone), next = wave_max(in ? kNone : high);
+      if (next != kNone && least <= next) in = in_best_groups<E>(p, l, lanes, lane, lds);
     }
     const uint64_t chosen = __builtin_amdgcn_ballot_w64(in);
     // lane / lanes (the quotient is at least half a 64th from a whole number)
@@ -380,7 +390,7 @@ __device__ __forceinline__ bool choose_fast(const RouteProblem& p, const float* 
   for (;; ++n) {
     const int best = wave_max(v[0]);
     if (best == kNone) break;
-    if (n >= p.top && (!p.bias || margin.apart(of_key(last), of_key(best), 1.f))) break;
+    if (n >= p.top && (!p.bias || margin.apart(of_key(last), of_key(best)))) break;
     known = n < 64;
     if (!known) break;
     last = best;
@@ -399,7 +409,7 @@ __device__ __forceinline__ bool choose_fast(const RouteProblem& p, const float* 
   if (!known) return false;
   if (p.bias) {
     const int next = __shfl_down(key, 1);
-    const bool close = lane + 1 < n && !margin.apart(of_key(key), of_key(next), 1.f);
+    const bool close = lane + 1 < n && !margin.apart(of_key(key), of_key(next));
     if (__builtin_amdgcn_ballot_w64(close)) {
       // their order in 64 bits
       const Exact<E> exact(p, l);
