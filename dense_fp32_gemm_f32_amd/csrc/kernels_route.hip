@@ -354,8 +354,11 @@ __device__ __forceinline__ bool choose_fast(const RouteProblem& p, const float* 
         b = max(max(b, y), min(a, x));
         a = max(a, x);
       }
+    // (a sum that passes the largest float stays above kNone: a group of the lowest biases
+    // comes before one without an expert; which of such sums is above, 64 bits decide)
     const bool both = sums && b != kNone;
-    const int score = both ? key_of(of_key(a) + of_key(b)) : a;
+    const float sum = fminf(fmaxf(of_key(a) + of_key(b), -FLT_MAX), FLT_MAX);
+    const int score = both ? key_of(sum) : a;
     int rank = 0;   // groups above this lane's
     for (int g = 0; g < p.groups; ++g) {
       const int other = __builtin_amdgcn_readlane(score, g);
