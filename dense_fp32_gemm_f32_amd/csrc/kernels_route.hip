@@ -592,12 +592,13 @@ __global__ void __launch_bounds__(kThreads) route_grad_kernel(RouteProblem p) {
 #pragma unroll
     for (int i = 0; i < E; ++i) d[i] = sum > 0.f ? -(d[i] / sum * dot) : 0.f;
   } else {
-    const float s = p.sigmoid && there ? sigmoid(x) : 0.f;
+    // 1 - s is the sigmoid of -x: taken from s it would have no bits left above x = 17
+    const float s = p.sigmoid && there ? sigmoid(x) : 0.f, rest = p.sigmoid ? sigmoid(-x) : 1.f;
     if (p.renorm) {
       const float q = p.sigmoid ? share_of_sigmoid(x, s, there) : share_of_chosen(x, there);
-      mine = q * (g - wave_sum(there ? q * g : 0.f)) * (1.f - s);
+      mine = q * (g - wave_sum(there ? q * g : 0.f)) * rest;
     } else {
-      mine = s * (1.f - s) * g;
+      mine = s * rest * g;
     }
   }
   for (int j = 0; j < p.top; ++j) {

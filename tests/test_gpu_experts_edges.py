@@ -5,6 +5,7 @@ import math
 import pytest
 import torch
 
+from dense_fp32_gemm_f32_amd import binding
 from tests import gpu_helpers as H
 from tests.test_gpu_experts import SIGMOID, SOFTMAX, check_route
 from tests.test_gpu_grouped import gen
@@ -61,3 +62,67 @@ def test_route_groups_of_lowest_biases(gpu_lib, E, groups, score):
                     group_best=2, what="two sums")
         check_route(logits, 2, bias=-bias.reshape(-1), score=score, groups=groups, group_top=top,
                     group_best=2, what="highest")
+
+
+# ---- the gradient of routing ----------------------------------------------------------
+
+def centred(share, g):
+    """sum_k share_k (g_i - g_k), the formula's g_i - sum share_k g_k (shares add up to
+    one, or are all zero), and the sum of magnitudes without i = k."""
+    by = g[:, :, None] - g[:, None, :]
+    return (share[:, None, :] * by).sum(2), \
+        (share[:, None, :] * (g.abs()[:, :, None] + g.abs()[:, None, :])
+         * (1 - torch.eye(g.shape[1], dtype=g.dtype))).sum(2)
+
+
+def check_slopes(logits, choice, dweight, score, renorm, what):
+    """route_grad against the formulas in 64 bits, each factor by itself: 1 - s as
+    sigmoid(-x), and a share that is nearly one by the others' sum.  Gates: of an exponential
+    2U and U |x|, a sum (E / 64 + 6) U, a quotient U: of a factor (D + E / 64 + 16) U, D the
+    widest distance; three of them, the products, and the sum over the choices (and over
+    the experts where all take part) of the sum of magnitudes."""
+    T, E = logits.shape
+    top = choice.shape[1]
+    got = binding.route_grad(dweight.cuda(), logits.cuda(), choice.int().cuda(), score=score,
+                             renorm=renorm).cpu().double()
+    x, d = logits.double(), dweight.double()
+    cx = x.gather(1, choice)
+    slope = torch.sigmoid(-cx)                       # 1 - s
+    if renorm:
+        log = torch.nn.functional.logsigmoid(cx) if score == SIGMOID else cx
+        share = torch.softmax(log, 1)
+        value, mag = centred(share, d)
+        value, mag = share * value, share * mag
+        if score == SIGMOID:
+            value, mag = value * slope, mag * slope
+        zero = torch.zeros(T, E, dtype=torch.float64)
+        want = zero.scatter_add(1, choice, value)
+        mag = zero.scatter_add(1, choice, mag)
+    elif score == SIGMOID:
+        zero = torch.zeros(T, E, dtype=torch.float64)
+        want = zero.scatter_add(1, choice, torch.sigmoid(cx) * slope * d)
+        mag = want.abs()
+    else:
+        g = torch.zeros(T, E, dtype=torch.float64).scatter_add(1, choice, d)
+        share = torch.softmax(x, 1)
+        value, mag = centred(share, g)
+        want, mag = share * value, share * mag
+    D = float((x.max(1).values - x.min(1).values).max())
+    steps = 6 * D + E / 16 + 3 * top + 64
+    err = (got - want).abs()
+    bound = steps * U * mag + 2.0 ** -126
+    assert bool((err <= bound).all()), f"{what}: off by {float((err / bound).max()):.2f} of the gate"
+
+
+@pytest.mark.parametrize("T,E,top", [(40, 2, 2), (40, 1, 1), (30, 64, 8), (20, 130, 6),
+                                     (9, 300, 3), (5, 1024, 20)])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_route_grad_of_large_sigmoid_logits(gpu_lib, T, E, top, renorm):
+    """Logits of +8 to +30, where 1 - s has to come from the logit."""
+    H.say(f"route_grad sigmoid, large logits T={T} E={E} top={top} renorm={renorm}")
+    g = gen(T + E)
+    logits = 8 + 22 * torch.rand(T, E, generator=g)
+    if not renorm:   # and far below zero
+        logits[::3] *= -1
+    choice = torch.stack([torch.randperm(E, generator=g)[:top] for _ in range(T)])
+    check_slopes(logits, choice, torch.randn(T, top, generator=g), SIGMOID, renorm, "large")
