@@ -560,8 +560,35 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteProblem p) {
 //   renormalised   dl_i = q_i (g_i - sum q_k g_k), q the shares of the chosen
 //   sigmoid        dl_i = s_i (1 - s_i) g_i
 //   renormalised   dl_i = q_i (1 - s_i) (g_i - sum q_k g_k)
+// Where one share is above a half, the difference at it would have lost the bits that 1 less
+// that share has.  With m its place, and the other shares' sums,
+//   g_i - sum q_k g_k = (g_i - g_m) + (g_m sum' q_k - sum' q_k g_k)
 // Lane j forms the gradient of choice j; it is handed to the expert's lane choice
 // by choice, so an expert named twice gets both.
+
+// What is to be added to g_i: minus the sum, or (where base is g_m) the second bracket.
+struct Centre {
+  float base, add;
+  // others: the sum of the shares but the leading one; dot: of their products with g
+  __device__ __forceinline__ Centre(float share, float g, float others, float dot) {
+    const bool leads = others < 0.5f;
+    base = leads ? g : 0.f;
+    add = leads ? g * others - dot : -(share * g + dot);
+  }
+};
+
+// g - sum q_k g_k of the lanes' entries, whose shares go by x.
+__device__ __forceinline__ float centred(float x, float q, float g, bool there) {
+  const float largest = wave_max(there ? x : -INFINITY);
+  const uint64_t most = __builtin_amdgcn_ballot_w64(there && x == largest);
+  if (most == 0) return 0.f;
+  const int lane = threadIdx.x & 63, m = __builtin_ctzll(most);
+  const bool other = there && lane != m;
+  const Centre c(lane_value(q, m), lane_value(g, m), wave_sum(other ? q : 0.f),
+                 wave_sum(other ? q * g : 0.f));
+  return (g - c.base) + c.add;
+}
+
 template <int E>
 __global__ void __launch_bounds__(kThreads) route_grad_kernel(RouteProblem p) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -573,34 +600,21 @@ __global__ void __launch_bounds__(kThreads) route_grad_kernel(RouteProblem p) {
   const bool there = x > -INFINITY;
   x = fminf(x, FLT_MAX);
   const float g = there ? p.scale * p.dweight[t * p.top + lane] : 0.f;
-  float d[E];
-#pragma unroll
-  for (int i = 0; i < E; ++i) d[i] = 0.f;
-  float mine;
-  if (!p.sigmoid && !p.renorm) {
-    float l[E], sum = 0.f;
-    load_logits<E>(p, t, lane, l);
-    const float m = largest<E>(l);
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      d[i] = l[i] > -INFINITY ? expf(l[i] - m) : 0.f;
-      sum += d[i];
-    }
-    sum = wave_sum(sum);
-    mine = there ? expf(x - m) / sum * g : 0.f;
-    const float dot = wave_sum(mine);
-#pragma unroll
-    for (int i = 0; i < E; ++i) d[i] = sum > 0.f ? -(d[i] / sum * dot) : 0.f;
-  } else {
+  const bool all = !p.sigmoid && !p.renorm;   // every expert has a share
+  float mine = g;
+  if (!all) {
     // 1 - s is the sigmoid of -x: taken from s it would have no bits left above x = 17
     const float s = p.sigmoid && there ? sigmoid(x) : 0.f, rest = p.sigmoid ? sigmoid(-x) : 1.f;
     if (p.renorm) {
       const float q = p.sigmoid ? share_of_sigmoid(x, s, there) : share_of_chosen(x, there);
-      mine = q * (g - wave_sum(there ? q * g : 0.f)) * rest;
+      mine = q * centred(x, q, g, there) * rest;
     } else {
       mine = s * rest * g;
     }
   }
+  float d[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) d[i] = 0.f;
   for (int j = 0; j < p.top; ++j) {
     const int to = __builtin_amdgcn_readlane(there ? e : -1, j);
     const float y = lane_value(mine, j);
@@ -608,6 +622,29 @@ __global__ void __launch_bounds__(kThreads) route_grad_kernel(RouteProblem p) {
 #pragma unroll
     for (int i = 0; i < E; ++i)
       if (lane * E + i == to) d[i] += y;
+  }
+  if (all) {
+    float w[E], sum = 0.f, others = 0.f;
+    load_logits<E>(p, t, lane, w);
+    const float m = largest<E>(w);
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const bool less = w[i] < m;
+      w[i] = w[i] > -INFINITY ? expf(w[i] - m) : 0.f;
+      sum += w[i];
+      others += less ? w[i] : 0.f;
+    }
+    sum = wave_sum(sum);
+    // (one above a half is alone at m, and alone has w 1; more there have all a sum of 2)
+    const float share = there ? expf(x - m) / sum : 0.f;
+    const bool lead = there && x == m;
+    const Centre c(1.f / sum, wave_sum(lead ? g : 0.f),
+                   sum < 2.f ? wave_sum(others) / sum : 1.f, wave_sum(lead ? 0.f : share * g));
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const float by = c.base != 0.f && w[i] == 1.f ? 0.f : d[i] - c.base;
+      d[i] = w[i] > 0.f ? w[i] / sum * (by + c.add) : 0.f;
+    }
   }
   float* out = p.dlogits + t * p.lddl;
   store_row<E>(out, p.experts, lane, d);

@@ -7,7 +7,7 @@ import torch
 
 from dense_fp32_gemm_f32_amd import binding
 from tests import gpu_helpers as H
-from tests.test_gpu_experts import SIGMOID, SOFTMAX, check_route
+from tests.test_gpu_experts import SIGMOID, SOFTMAX, check_grad, check_route
 from tests.test_gpu_grouped import gen
 
 pytestmark = pytest.mark.gpu
@@ -126,3 +126,43 @@ def test_route_grad_of_large_sigmoid_logits(gpu_lib, T, E, top, renorm):
         logits[::3] *= -1
     choice = torch.stack([torch.randperm(E, generator=g)[:top] for _ in range(T)])
     check_slopes(logits, choice, torch.randn(T, top, generator=g), SIGMOID, renorm, "large")
+
+
+@pytest.mark.parametrize("T,E,top", [(40, 2, 1), (40, 2, 2), (30, 64, 8), (20, 130, 6),
+                                     (9, 300, 3), (5, 1024, 20)])
+@pytest.mark.parametrize("score", [SOFTMAX, SIGMOID])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_route_grad_of_one_expert_above_all(gpu_lib, T, E, top, score, renorm):
+    """One expert's share is nearly one: 1 less that share has to come from the others'.
+    Chosen in most rows, not in some, and two that share the lead."""
+    H.say(f"route_grad one above all T={T} E={E} top={top} score={score} renorm={renorm}")
+    g = gen(T * E + 1)
+    logits = torch.randn(T, E, generator=g)
+    if score == SIGMOID:   # where a sigmoid is the exponential
+        logits -= 45
+    choice = torch.stack([torch.randperm(E, generator=g)[:top] for _ in range(T)])
+    lead = choice[:, top // 2].clone()
+    lead[::5] = torch.randint(0, E, lead[::5].shape, generator=g)
+    logits[torch.arange(T), lead] += 2 + 30 * torch.rand(T, generator=g)
+    second = choice[1::4, 0]
+    logits[1::4].scatter_(1, second[:, None], logits[1::4].max(1, keepdim=True).values)
+    check_slopes(logits, choice, torch.randn(T, top, generator=g), score, renorm, "one above")
+
+
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("score", [SOFTMAX, SIGMOID])
+def test_route_grad_of_tokens_with_fewer_choices(gpu_lib, renorm, score):
+    """Tokens with some choices, but fewer than top, as routing leaves them: masks, and
+    groups that hold fewer experts.  Nothing reaches an expert that was not chosen by way of
+    the entries without a choice."""
+    H.say(f"route_grad fewer choices score={score} renorm={renorm}")
+    g = gen(17)
+    logits = torch.randn(40, 12, generator=g)
+    logits[torch.rand(40, 12, generator=g) < 0.3] = -INF
+    logits[0] = -INF
+    dweight = torch.randn(40, 7, generator=g)
+    for how in ({}, {"groups": 3, "group_top": 1}, {"groups": 6, "group_top": 2, "group_best": 2}):
+        choice, _ = check_route(logits, 7, score=score, renorm=renorm, what=str(how), **how)
+        choice = choice.cpu().long()
+        assert bool(((choice < 0).any(1) & (choice >= 0).any(1)).any())
+        check_grad(logits, choice, dweight, score, renorm, 2.5, what=str(how))
