@@ -116,8 +116,9 @@ struct Few {
     return bytes == 4 ? x : bytes == 2 ? (x >> 16 * (s & 1)) & 0xffffu : (x >> 8 * (s & 3)) & 0xffu;
   }
 
-  // The last chunk of a K that is no multiple of 128, moved into place: codes and
-  // scales behind the row's last meet parts that are zero.
+  // The last chunk of a K that is no multiple of 128, moved into place: codes behind the
+  // row's last meet parts that are zero, and scales behind its last are zeros themselves
+  // (another's could be infinite, which times a sum of zero is NaN).
   __device__ __forceinline__ void settle(It& it, int64_t k0) const {
     const int64_t want = k0 / 2 + 16 * (lane >> 4);
     // bytes, 16 and more: all behind
@@ -138,7 +139,7 @@ struct Few {
       uint32_t s[kScales];
 #pragma unroll
       for (int i = 0; i < kScales; ++i) {
-        s[i] = field(it.scale, kScales - 1, kBytes);
+        s[i] = 0;   // +0 as fp32, fp16 and bf16, 2^-127 as e8m0
 #pragma unroll
         for (int j = 0; j < kScales; ++j)
           if (i + shift == j) s[i] = field(it.scale, j, kBytes);
@@ -157,7 +158,7 @@ struct Few {
   }
 
   // acc += this wave's chunk, whose parts begin at step step0 of those in LDS.
-  __device__ __forceinline__ void multiply(It it, int chunk, int step0, f32x4 (&acc)[RT]) const {
+  __device__ __forceinline__ void multiply(It it, int chunk, int step0, float (&acc)[RT]) const {
     const int64_t k0 = (int64_t)chunk * kChunkK;
     if (__builtin_expect(k0 + kChunkK > K, 0)) settle(it, k0);
     const u32x4 codes = by_steps(it.codes);
@@ -176,8 +177,9 @@ struct Few {
       }
       if (i % kPer == kPer - 1) {
         const float scale = scale_value(field(it.scale, s, kBytes), kType);
+        // a row's three parts first: one that is zero would be NaN by an infinite scale
 #pragma unroll
-        for (int t = 0; t < RT; ++t) acc[t] += sum[t] * scale;
+        for (int t = 0; t < RT; ++t) acc[t] += (sum[t][0] + (sum[t][1] + sum[t][2])) * scale;
       }
     }
   }
@@ -217,15 +219,12 @@ struct Few {
     *out = epilogue_apply(ep, row_of[row] >= 0 ? v : 0.f, out, n);
   }
 
-  // The sums of a strip stored, those of the waves along K added: a lane has the three
-  // parts' of row lane / 16 of each instruction.  Buffer 0 and 1 in turn.
+  // The sums of a strip stored, those of the waves along K added: a lane has that of row
+  // lane / 16 of each instruction.  Buffer 0 and 1 in turn.
   __device__ __forceinline__ void store(const Epilogue& ep, int strip, int buffer,
-                                        f32x4 (&acc)[RT]) const {
+                                        const float (&v)[RT]) const {
     const int kw = 1 << kw_log2, wide = 16 * kWaves >> kw_log2;   // columns of the strip
     const int64_t n0 = (int64_t)strip * wide;
-    float v[RT];
-#pragma unroll
-    for (int t = 0; t < RT; ++t) v[t] = acc[t][0] + acc[t][1] + acc[t][2];
     if (kw == 1) {
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
@@ -304,9 +303,9 @@ struct Few {
       // (out of order here, the first would be waited for behind the others in the loop)
       __builtin_amdgcn_sched_barrier(0);
     }
-    f32x4 acc[RT];
+    float acc[RT];
 #pragma unroll
-    for (int t = 0; t < RT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int t = 0; t < RT; ++t) acc[t] = 0.f;
     bool staged = false;
     int buffer = 0;
     // kAhead steps in turn, those behind a pass's chunks empty, so that staging and
@@ -332,7 +331,7 @@ struct Few {
         store(ep, was, buffer, acc);
         buffer ^= 1;
 #pragma unroll
-        for (int t = 0; t < RT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int t = 0; t < RT; ++t) acc[t] = 0.f;
       }
     } while (now.strip < strips);
   }

@@ -93,7 +93,8 @@ struct Tiles {
   }
 
   // The same for the part of K behind the whole steps: k past the end reads the last
-  // one, and settle_rest() then makes A's values there zeros.
+  // one, and settle_rest() then makes A's values there zeros, and the scale of a step that is
+  // all behind K (an infinite one times its sum, 0, would be NaN).
   __device__ __forceinline__ void load_rest(Values& v, int step) {
     const int64_t k0 = ((int64_t)step * KS + part_k) * 32, ka = k0 + 8 * (tid & 3),
                   kw = k0 + 16 * (tid & 1);
@@ -108,12 +109,14 @@ struct Tiles {
     load_scales(v, min(k0, K - 1));
   }
   __device__ __forceinline__ void settle_rest(Values& v, int step) {
-    const int64_t ka = ((int64_t)step * KS + part_k) * 32 + 8 * (tid & 3);
+    const int64_t k0 = ((int64_t)step * KS + part_k) * 32, ka = k0 + 8 * (tid & 3);
 #pragma unroll
     for (int i = 0; i < kOctets; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         if (ka + j >= K) v.x[i][j] = 0.f;
+    if constexpr (kFold)
+      if (KS > 1 && k0 >= K) v.scale = 0;
   }
 
   // The registers' values into a buffer.

@@ -472,8 +472,10 @@ int gemm_f32_join_rows_grad(int64_t tokens, int64_t top, int64_t N,
  * (So a group's sum of a * code must not pass the largest float, also where the
  * scale would bring it back.  e8m0 scales may go into the weights first: a weight
  * that passes the largest float, as 6 * 2^127 does, gives a result that is not
- * finite.  Of an a below 2^-110 the lowest bits may be lost.)  Values that are not
- * finite give what the formula gives.
+ * finite.  Of an a below 2^-110 the lowest bits may be lost.)  Values of A, C and
+ * bias that are not finite, and scales that are NaN, give what the formula gives; an
+ * infinite scale does where that is an infinity (where it is NaN, as weights of zero or
+ * of both signs beside such a scale make it, the result is not finite).
  *
  * Errors as gemm_f32_fused; an unknown format or scale type, a group that is no
  * power of two or below 32, zero points with e2m1 GEMM_F32_ERR_INVALID_ARG; ldq
