@@ -93,8 +93,8 @@ struct Tiles {
   }
 
   // The same for the part of K behind the whole steps: k past the end reads the last
-  // one, and settle_rest() then makes A's values there zeros, and the scale of a step that is
-  // all behind K (an infinite one times its sum, 0, would be NaN).
+  // one, and settle_rest() then makes A's values there zeros, as it does the scale of a step
+  // that is all behind K (an infinite one times its sum, 0, would be NaN).
   __device__ __forceinline__ void load_rest(Values& v, int step) {
     const int64_t k0 = ((int64_t)step * KS + part_k) * 32, ka = k0 + 8 * (tid & 3),
                   kw = k0 + 16 * (tid & 1);
@@ -115,8 +115,23 @@ struct Tiles {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         if (ka + j >= K) v.x[i][j] = 0.f;
-    if constexpr (kFold)
+    if constexpr (kFold) {
       if (KS > 1 && k0 >= K) v.scale = 0;
+    } else {
+      // weights with their scale: codes behind K (half a byte that may hold anything, and
+      // copies) get the code of weight 0, as one that passes the largest float times 0 is
+      // NaN.  (A zero point above 15 has none: then 15 is nearest, and each real code's
+      // weight at least as large.)
+      const uint32_t none =
+          0x11111111u * (kForm == kE2m1 ? 0u : kForm == kInt8 ? 8u : min((uint32_t)v.zero, 15u));
+      const int64_t left = K - (k0 + 16 * (tid & 1));   // real ones of this thread's 16
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int n = (int)max((int64_t)0, min(left - 8 * h, (int64_t)8));
+        const uint32_t keep = n < 8 ? (1u << 4 * n) - 1u : ~0u;
+        v.c[h] = (v.c[h] & keep) | (none & ~keep);
+      }
+    }
   }
 
   // The registers' values into a buffer.

@@ -1,12 +1,12 @@
 """GPU tests of the products with 4-bit weights at their edges: values that are not
-finite where K ends inside a step."""
+finite, and unused codes, where K ends inside a step."""
 import pytest
 import torch
 
 from dense_fp32_gemm_f32_amd import binding, q4
 from tests import gpu_helpers as H
 from tests.test_gpu_grouped import gen
-from tests.test_gpu_q4 import KERNELS, KINDS
+from tests.test_gpu_q4 import E2M1, INT, KERNELS, KINDS
 
 pytestmark = pytest.mark.gpu
 
@@ -53,3 +53,37 @@ def test_infinite_scales_of_the_last_group(gpu_lib, kernel, kind, group):
         odd = W.sum(1)
         want[:, ~odd.isfinite()] = odd[~odd.isfinite()]
         assert equal(got, want)
+
+
+@pytest.mark.parametrize("kernel", list(KERNELS))
+@pytest.mark.parametrize("form", ["symmetric", "zeros", "e2m1"])
+def test_the_unused_half_beside_large_powers(gpu_lib, kernel, form):
+    """An odd K leaves half a byte, which may hold a code whose weight would pass the
+    largest float where the real ones do not."""
+    M, N = KERNELS[kernel]
+    for K in (515, 641) if kernel == "few" else (1, 33, 97, 203):
+        for e in (253, 254):
+            H.say(f"q4 unused half {kernel} {form} K={K} e={e}")
+            g = gen(K + M)
+            a = torch.randint(1, 3, (M, K), generator=g).float() * 2.0 ** -30
+            along = (K + 31) // 32
+            scale = torch.full((N, along), e, dtype=torch.uint8)
+            zero = None
+            if form == "e2m1":
+                codes = torch.randint(0, 3, (N, K), generator=g)        # 0, .5, 1
+            else:
+                codes = torch.randint(7, 10, (N, K), generator=g)       # -1, 0, 1
+            if form == "zeros":
+                zero = torch.randint(3, 6, (N, along), generator=g).to(torch.uint8)
+                zero[::9] = 200
+                codes = codes - 8 + zero.long().clamp_max(14)[:, torch.arange(K) // 32]
+                scale[::9] = 100
+            packed = q4.pack(codes)
+            packed[..., -1] |= 0xf0 if form == "symmetric" else 0x70
+            fmt = E2M1 if form == "e2m1" else INT
+            W = q4.dequantize(packed, scale, K, zero=zero, group=32, format=fmt,
+                              dtype=torch.float64)
+            got = binding.gemm_q4(a.cuda(), packed.cuda(), scale.cuda(), format=fmt, group=32,
+                                  zero=None if zero is None else zero.cuda())
+            # whole numbers times one power: exact in every order
+            assert torch.equal(got.cpu().double(), a.double() @ W.t())
