@@ -11,6 +11,8 @@
 // takes 187 us (5.6 TB/s), the norm and the scaled arrays 585 us (5.4 TB/s).
 #include "experts_internal.h"
 
+#include <cfloat>
+
 namespace gemmf32 {
 namespace {
 
@@ -64,15 +66,34 @@ __device__ __forceinline__ float4 load4(const float* x) {
 }
 // Past the caches, which keep the read arrays instead (120 arrays of 264 M floats: 585 us,
 // with ordinary stores 615 us).
-__device__ __forceinline__ void store4(float* y, float4 v, bool scales, float by) {
-  if (scales) {
-    v.x *= by;
-    v.y *= by;
-    v.z *= by;
-    v.w *= by;
-  }
+template <class F>
+__device__ __forceinline__ void store4(float* y, float4 v, F f) {
   typedef float vector __attribute__((ext_vector_type(4), aligned(4)));
-  __builtin_nontemporal_store(vector{v.x, v.y, v.z, v.w}, reinterpret_cast<vector*>(y));
+  __builtin_nontemporal_store(vector{f(v.x), f(v.y), f(v.z), f(v.w)},
+                              reinterpret_cast<vector*>(y));
+}
+
+// y = f(x) for every array (those in place if kInPlace), the last chunks first: they are the
+// ones that the caches still hold.
+template <bool kInPlace, class F>
+__device__ __forceinline__ void map_arrays(const Table& t, F f) {
+  for (int c = t.first[t.count] - 1 - blockIdx.x; c >= 0; c -= gridDim.x) {
+    const int a = array_of(t, c);
+    const int64_t from = (c - t.first[a]) * kChunk, to = min(t.n[a], from + kChunk);
+    const float* x = t.x[a];
+    float* y = t.y[a];
+    if (!kInPlace && x == y) continue;
+    int64_t i = from + 4 * threadIdx.x;
+    for (; i + (kAhead - 1) * kStep + 4 <= to; i += kAhead * kStep) {
+      float4 v[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) v[k] = load4(x + i + k * kStep);
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) store4(y + i + k * kStep, v[k], f);
+    }
+    for (; i + 4 <= to; i += kStep) store4(y + i, load4(x + i), f);
+    for (; i < to; ++i) y[i] = f(x[i]);
+  }
 }
 
 __global__ void __launch_bounds__(kThreads) norm_parts_kernel(Table t, double* part) {
@@ -120,31 +141,21 @@ __global__ void __launch_bounds__(kThreads)
   if (threadIdx.x == 0) *norm = (float)v;
 }
 
-// y = x limit / norm where the norm is finite and above the limit, else y = x.
+// y = x limit / norm where the norm is finite and above the limit, else y = x.  The factor
+// is a float, where that is a normal number; a smaller one would have few bits or none,
+// though its products with large elements are ordinary numbers, and stays in 64 bits.
 __global__ void __launch_bounds__(kThreads)
     norm_scale_kernel(Table t, const double* part, int parts, float limit, float* norm) {
   const double v = norm_of(part, parts);
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)v;
-  const bool scales = v > (double)limit && v < (double)INFINITY;
-  const float by = scales ? (float)((double)limit / v) : 1.f;
-  const int chunks = t.first[t.count];
-  // the last chunks first: they are the ones that the caches still hold
-  for (int c = chunks - 1 - blockIdx.x; c >= 0; c -= gridDim.x) {
-    const int a = array_of(t, c);
-    const int64_t from = (c - t.first[a]) * kChunk, to = min(t.n[a], from + kChunk);
-    const float* x = t.x[a];
-    float* y = t.y[a];
-    if (!scales && x == y) continue;
-    int64_t i = from + 4 * threadIdx.x;
-    for (; i + (kAhead - 1) * kStep + 4 <= to; i += kAhead * kStep) {
-      float4 v[kAhead];
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) v[k] = load4(x + i + k * kStep);
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) store4(y + i + k * kStep, v[k], scales, by);
-    }
-    for (; i + 4 <= to; i += kStep) store4(y + i, load4(x + i), scales, by);
-    for (; i < to; ++i) y[i] = scales ? x[i] * by : x[i];
+  const double by = (double)limit / v;
+  if (!(v > (double)limit && v < (double)INFINITY)) {
+    map_arrays<false>(t, [](float x) { return x; });
+  } else if (by >= (double)FLT_MIN) {
+    const float f = (float)by;
+    map_arrays<true>(t, [f](float x) { return x * f; });
+  } else {
+    map_arrays<true>(t, [by](float x) { return (float)((double)x * by); });
   }
 }
 

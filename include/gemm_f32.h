@@ -539,8 +539,9 @@ int gemm_f32_norm(int64_t count, const float *const *x, const int64_t *n,
 /*
  * gemm_f32_clip -- the arrays scaled so that their global norm is at most max_norm:
  * *norm as gemm_f32_norm writes it, and y[i] = x[i] * (max_norm / norm) where the norm
- * is above max_norm, else y[i] = x[i].  A norm that is not finite (one of the values
- * is not) leaves y[i] = x[i]: the caller sees it in *norm.  out: host array of the
+ * is above max_norm, else y[i] = x[i].  It goes by the norm in 64 bits: one past the
+ * largest float is infinite in *norm and scales the arrays all the same.  A value that
+ * is not finite leaves y[i] = x[i]: the caller sees it in *norm.  out: host array of the
  * y, each equal to its x (in place) or apart from everything else; NULL: all in
  * place.  Where nothing is to scale, arrays in place are not written.
  *

@@ -166,3 +166,24 @@ def test_route_grad_of_tokens_with_fewer_choices(gpu_lib, renorm, score):
         choice = choice.cpu().long()
         assert bool(((choice < 0).any(1) & (choice >= 0).any(1)).any())
         check_grad(logits, choice, dweight, score, renorm, 2.5, what=str(how))
+
+
+# ---- clipping ------------------------------------------------------------------------
+
+@pytest.mark.parametrize("limit", [1.0, 1e-3, 1e-8, 1e-30, 1e-37])
+@pytest.mark.parametrize("size", [3e38, 1e30, 1e-3])
+def test_clip_by_factors_below_the_smallest_float(gpu_lib, limit, size):
+    """limit / norm below 2^-126, where a float of it has few bits or none, times elements
+    that are as large.  Chunks of 16 bytes, ends, and elements by themselves."""
+    H.say(f"clip limit={limit} size={size}")
+    g = gen(31)
+    xs = [(torch.rand(n, generator=g) * 2 - 1) * size for n in (40000, 1, 5, 1027)]
+    big = torch.tensor(limit).item()
+    exact = math.sqrt(sum(float((x.double() ** 2).sum()) for x in xs))
+    outs = [torch.full_like(x, NAN).cuda() for x in xs]
+    norm = binding.clip_norm([x.cuda() for x in xs], limit, out=outs).item()
+    assert norm == (INF if exact > LARGEST else norm)
+    for x, y in zip(xs, outs):
+        want = x.double() * min(1.0, big / exact)
+        # the factor and the product each round; below 2^-126 by half of 2^-149
+        assert bool(((y.cpu().double() - want).abs() <= 3 * U * want.abs() + 2.0 ** -150).all())
