@@ -1035,6 +1035,8 @@ def clip_norm(tensors, max_norm, out=None, norm=None):
     """The tensors scaled by max_norm / norm where their norm together is above
     max_norm: in place, or into the tensors of ``out``.  A norm that is not finite
     leaves them as they are.  Returns the norm before, a 1-element tensor."""
+    if max_norm is None:
+        raise TypeError("max_norm must be a number")
     return _norm_of(tensors, out, max_norm, norm)
 
 
