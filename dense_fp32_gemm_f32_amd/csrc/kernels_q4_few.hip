@@ -20,6 +20,7 @@
 #include "q4_routes.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace gemmf32 {
 namespace {
@@ -337,25 +338,127 @@ struct Few {
   }
 };
 
+// Inclusive sum over the lanes of a wave, held at the largest value.
+__device__ __forceinline__ unsigned scan_lanes(unsigned x) {
+  const auto add = [&](auto ctrl, auto rows) {
+    x = __builtin_elementwise_add_sat(
+        x, (unsigned)__builtin_amdgcn_update_dpp(0, (int)x, ctrl.value, rows.value, 0xf, false));
+  };
+  // 1, 2, 4 and 8 lanes up in rows of 16; row 0 (2) into row 1 (3), both into the others
+  add(std::integral_constant<int, 0x111>{}, std::integral_constant<int, 0xf>{});
+  add(std::integral_constant<int, 0x112>{}, std::integral_constant<int, 0xf>{});
+  add(std::integral_constant<int, 0x114>{}, std::integral_constant<int, 0xf>{});
+  add(std::integral_constant<int, 0x118>{}, std::integral_constant<int, 0xf>{});
+  add(std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xa>{});
+  add(std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0xc>{});
+  return x;
+}
+
+// The row tiles of all groups in order.  A lane has a group, each wave the same ones and
+// nothing to wait for, up to 64 of them; with more a thread has a group, so that any number
+// takes one load and one sum over the workgroup (0.5 us more).
+struct GroupTiles {
+  unsigned first, tiles;   // of this lane's or thread's group
+  int begin, rows;
+  unsigned total;          // of all
+  bool waves;              // each alone
+  struct Shared {
+    unsigned sums[kWaves];
+    int found[3];
+  };
+  static_assert(kMaxGroups <= kThreads, "a thread for each group");
+
+  __device__ __forceinline__ void find_all(const Q4Problem& p, Shared& lds) {
+    waves = p.g.groups <= 64;
+    const int wave = threadIdx.x >> 6, g = waves ? threadIdx.x & 63 : threadIdx.x;
+    begin = rows = 0;
+    if (g < p.g.groups) {
+      int end;
+      group_span(p.g.offsets, g, p.g.rows, begin, end);
+      rows = end - begin;
+    }
+    tiles = q4_few_rows(p) == kQ4FewRows
+                ? ((unsigned)rows + kQ4FewRows - 1) / kQ4FewRows
+                : ((unsigned)rows + kQ4FewRowsDeep - 1) / kQ4FewRowsDeep;
+    const unsigned incl = scan_lanes(tiles);
+    first = incl - tiles;
+    total = __builtin_amdgcn_readlane(incl, 63);
+    if (waves) return;
+    if ((g & 63) == 63) lds.sums[wave] = incl;
+    __syncthreads();
+    unsigned before = 0;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      if (w == wave) before = total;
+      total = __builtin_elementwise_add_sat(total, lds.sums[w]);
+    }
+    first = __builtin_elementwise_add_sat(first, before);
+    total = __builtin_amdgcn_readfirstlane(total);
+  }
+
+  // Row tile t's group, its first place and rows: a group's tiles have one size.
+  __device__ __forceinline__ void find(unsigned t, Shared& lds, int& group, int& place,
+                                       int& count) const {
+    const bool here = t >= first && t - first < tiles;
+    const int each = tiles <= 1 ? rows : (int)(((unsigned)rows + tiles - 1) / tiles);
+    const int at = here ? (int)(t - first) * each : 0;
+    place = begin + at;
+    count = min(each, rows - at);
+    if (waves) {
+      const int lane = __builtin_ctzll(__builtin_amdgcn_ballot_w64(here));
+      group = lane;
+      place = __builtin_amdgcn_readlane(place, lane);
+      count = __builtin_amdgcn_readlane(count, lane);
+      return;
+    }
+    if (here) {
+      lds.found[0] = threadIdx.x;
+      lds.found[1] = place;
+      lds.found[2] = count;
+    }
+    __syncthreads();
+    group = __builtin_amdgcn_readfirstlane(lds.found[0]);
+    place = __builtin_amdgcn_readfirstlane(lds.found[1]);
+    count = __builtin_amdgcn_readfirstlane(lds.found[2]);
+  }
+};
+
+// Quotient of numbers from 1 to 2^9 (the real one is at least a 2^10th from a whole number
+// above it, the reciprocal off by 2^-23 of itself).
+__device__ __forceinline__ unsigned small_quotient(unsigned a, unsigned b) {
+  return (unsigned)(((float)a + 0.5f) * __builtin_amdgcn_rcpf((float)b));
+}
+
+// A row tile goes to as many workgroups as there are CUs for it, which take its strips in
+// turn; further tiles follow after one another.  Without offsets the host says how many
+// (tiles along the grid's y, of `each` rows).  With them only the device can: 192 rows of 32
+// groups of 2048 x 1024 are 32 tiles, which take 18 us, or, all in one group, 10, which take
+// 23 (183 with each group's tiles one after another on workgroups of its own).
 template <int kForm, int kScales, int kType>
-__global__ void __launch_bounds__(kThreads, 4) q4_few_kernel(Q4Problem p, Epilogue ep) {
+__global__ void __launch_bounds__(kThreads, 4)
+    q4_few_kernel(Q4Problem p, Epilogue ep, unsigned tiles, int each) {
   __shared__ __attribute__((aligned(16))) char lds[kLdsBytes];
   __shared__ int row_of[2 * kQ4FewRows];
-  const int group = blockIdx.y;
-  int begin, end;
-  group_span(p.g.offsets, group, p.g.rows, begin, end);
-  // row tiles of one size, along the grid's z and, where there are more, in turn
-  const int most = q4_few_rows(p), tiles = (end - begin + most - 1) / most;
-  if (tiles == 0) return;
-  const int each = (end - begin + tiles - 1) / tiles;
-  if (ep.bias) ep.bias += group * p.g.sbias;
-  for (int i = blockIdx.z; i < tiles; i += gridDim.z) {
-    const int first = begin + i * each, rows = min(each, end - first);
-    if (rows <= 0) break;
-    auto run = [&](auto few) {
-      const int wide = 16 * kWaves >> few.kw_log2;
-      few.run(ep, first, rows, blockIdx.x, gridDim.x, (int)(((int64_t)p.g.N + wide - 1) / wide));
-    };
+  __shared__ GroupTiles::Shared shared;
+  const int strips = q4_few_strips(p);
+  unsigned tile = blockIdx.y, share = blockIdx.x, per = gridDim.x, step = gridDim.y;
+  GroupTiles all;
+  if (p.g.offsets) {
+    all.find_all(p, shared);
+    tiles = all.total;
+    if (tiles == 0) return;
+    per = min(tiles < kQ4Cus ? small_quotient(kQ4Cus, tiles) : 1u, (unsigned)strips);
+    tile = small_quotient(blockIdx.x, per);
+    share = blockIdx.x - tile * per;
+    step = kQ4Cus;
+  }
+  for (; tile < tiles; tile += step) {
+    int group = 0, place = (int)tile * each, rows = min(each, p.g.rows - place);
+    if (p.g.offsets) all.find(tile, shared, group, place, rows);
+    Epilogue e = ep;
+    if (e.bias) e.bias += group * p.g.sbias;
+    auto run = [&](auto few) { few.run(e, place, rows, (int)share, (int)per, strips); };
     if (rows <= kRowsT)
       run(Few<1, kForm, kScales, kType>(p, group, lds, row_of));
     else if (rows <= 2 * kRowsT)
@@ -371,15 +474,16 @@ __global__ void __launch_bounds__(kThreads, 4) q4_few_kernel(Q4Problem p, Epilog
 
 template <int kForm, int kScales, int kType>
 hipError_t launch(const Q4Problem& p, const Epilogue& e, hipStream_t s) {
-  const int tiles = p.g.offsets ? 1 : (p.g.rows + q4_few_rows(p) - 1) / q4_few_rows(p);
-  const int wide = 16 * kWaves >> q4_waves_along_k(p);
-  const int64_t strips = ((int64_t)p.g.N + wide - 1) / wide;
-  // a workgroup a CU, each with as many strips
-  const int64_t most = std::max((int64_t)1, 256 / ((int64_t)p.g.groups * tiles));
-  const int64_t each = (strips + most - 1) / most;
-  const dim3 grid((unsigned)((strips + each - 1) / each), (unsigned)p.g.groups,
-                  (unsigned)(tiles < 1024 ? tiles : 1024));
-  q4_few_kernel<kForm, kScales, kType><<<grid, kThreads, 0, s>>>(p, e);
+  const int most = q4_few_rows(p);
+  dim3 grid(kQ4Cus);   // a workgroup a CU
+  unsigned tiles = 0, each = 0;
+  if (!p.g.offsets) {
+    tiles = ((unsigned)p.g.rows + most - 1) / most;
+    each = ((unsigned)p.g.rows + tiles - 1) / tiles;
+    grid = dim3(std::min(std::max(1u, kQ4Cus / tiles), (unsigned)q4_few_strips(p)),
+                std::min(tiles, 1024u));
+  }
+  q4_few_kernel<kForm, kScales, kType><<<grid, kThreads, 0, s>>>(p, e, tiles, (int)each);
   return hipGetLastError();
 }
 

@@ -27,13 +27,29 @@ constexpr Q4TileCost kQ4Tiles[] = {{256, 256, 1180}, {256, 192, 970}, {256, 128,
                                    {128, 128, 440},  {64, 128, 270},  {64, 64, 185},
                                    {32, 64, 130},    {32, 32, 100}};
 
-// Rounds of a tile: the groups' last row tiles are counted half full.
+#if defined(__HIP__)
+#define GEMM_F32_BOTH __host__ __device__
+#else
+#define GEMM_F32_BOTH
+#endif
+
+constexpr int kQ4Cus = 256;
+
+// The groups that can have rows.
+GEMM_F32_BOTH inline int q4_active(const Q4Problem& p) {
+  return p.g.groups < p.g.rows ? p.g.groups : p.g.rows;
+}
+
+// Row tiles: one for each group that can have rows, and the last ones counted half full.
+inline int64_t q4_row_tiles(const Q4Problem& p, int rows) {
+  if (p.g.groups == 1) return ((int64_t)p.g.rows + rows - 1) / rows;
+  const int64_t active = q4_active(p);
+  return std::max(active, p.g.rows / rows + (active + 1) / 2);
+}
+
 inline int64_t q4_rounds(const Q4Problem& p, const Q4TileCost& t) {
-  const int64_t row_tiles = p.g.groups == 1
-                                ? ((int64_t)p.g.rows + t.rows - 1) / t.rows
-                                : (int64_t)p.g.rows / t.rows +
-                                      (std::min(p.g.groups, p.g.rows) + 1) / 2;
-  return (row_tiles * (((int64_t)p.g.N + t.cols - 1) / t.cols) + 255) / 256;
+  const int64_t tiles = q4_row_tiles(p, t.rows) * (((int64_t)p.g.N + t.cols - 1) / t.cols);
+  return (tiles + kQ4Cus - 1) / kQ4Cus;
 }
 
 inline int64_t q4_tile_cost(const Q4Problem& p, int t) {
@@ -51,19 +67,13 @@ constexpr int kQ4FewK = 128;   // the least K that the kernel for few rows takes
 constexpr int kQ4FewWavesLog2 = 4;
 constexpr int kQ4FewRows = 20, kQ4FewRowsDeep = 12;
 
-#if defined(__HIP__)
-#define GEMM_F32_BOTH __host__ __device__
-#else
-#define GEMM_F32_BOTH
-#endif
-
 // Its waves along K, as a power of two: so many that a workgroup on each CU has columns
 // for its waves, and no more than there are chunks.
 GEMM_F32_BOTH inline int q4_waves_along_k(const Q4Problem& p) {
   const int64_t chunks = ((int64_t)p.g.K + kQ4FewK - 1) / kQ4FewK;
-  const int64_t columns = ((int64_t)p.g.N + 15) / 16 * p.g.groups;
+  const int64_t columns = ((int64_t)p.g.N + 15) / 16 * q4_active(p);
   int log2 = 0;
-  while (log2 < kQ4FewWavesLog2 && (columns << log2) < (256 << kQ4FewWavesLog2) &&
+  while (log2 < kQ4FewWavesLog2 && (columns << log2) < (kQ4Cus << kQ4FewWavesLog2) &&
          (INT64_C(1) << log2) < chunks)
     ++log2;
   return log2;
@@ -79,29 +89,47 @@ GEMM_F32_BOTH inline int q4_few_rows(const Q4Problem& p) {
   return deep ? kQ4FewRowsDeep : kQ4FewRows;
 }
 
-// Whether the kernel for few rows (kernels_q4_few.hip) is the faster one, by its time in
-// the tiles' unit: with e strips of columns for each workgroup, c columns of 16 in them,
-// and r rows a row tile takes 12 + 2 r + c (9 + 0.8 r), and 14 for each strip where all
-// waves go along K.  Row tiles of one matrix go beside each other, those of a group one
-// after another; uneven groups are counted half as long again as their average.
-// (Few against tiles in us, e8m0 scales.  4096 x 4096: 8 rows 15 against 23, 12 rows 18
-// against 23, 16 rows 24 against 23; 8192 x 8192: 8 rows 25 against 39, 12 rows 32 against
-// 39, 16 rows 42 against 39; 28672 x 8192: 16 rows 97 against 97, 24 rows 148 against 96;
-// 2048 x 1024 in 32 groups: 6 rows each 17 against 47, 32 rows 42 against 48.)
+// Its strips of columns, one for the waves of a workgroup that do not share K.
+GEMM_F32_BOTH inline int q4_few_strips(const Q4Problem& p) {
+  const int wide = 16 << kQ4FewWavesLog2 >> q4_waves_along_k(p);
+  return (int)(((int64_t)p.g.N + wide - 1) / wide);
+}
+
+// Whether the kernel for few rows (kernels_q4_few.hip) is the faster one.  In microseconds,
+// with e strips of columns for each workgroup, row tiles of r rows, c chunks along K, of which
+// a wave takes w for each strip, a round of the CUs takes
+//   5 to 6 + 0.0215 r c (staging, for each strip where LDS has no room for all chunks)
+//   + e (0.2 + 0.06 r + w (1.17 + 0.014 r))
+// and tiles whose rounds cost t take 3 + t (3.9 + 4.3 K / 1024) / 100, and 4 where the waves
+// of the smallest, which share K by 256, have a rest behind that.  These are fits of 280 sizes each: 1 to
+// 128 groups of 1 to 48 rows, 512 x 2048 to 8192 x 8192, e8m0 scales; the choices by them are
+// 0.5 % slower than the faster of both on average, and 25 % at most.  Groups are counted as
+// even: the offsets that say more are the device's.  (Few against tiles in us.  4096 x 4096: 8
+// rows 12 against 22, 24 rows 22 against 23; 8192 x 8192: 8 rows 27 against 38; 32 groups of
+// 2048 x 1024: 6 rows each 17 against 43, 32 rows 35 against 45, 48 rows 53 against 47; of
+// 7168 x 2048: 8 rows each 86 against 236, 32 rows 225 against 251, 48 rows 390 against 256.)
 inline bool q4_few(const Q4Problem& p) {
   if (p.g.K < kQ4FewK) return false;
-  const int waves = 1 << kQ4FewWavesLog2, wide = waves >> q4_waves_along_k(p);
-  const auto up = [](double x, double by) { return std::ceil(x / by); };
   const bool one = p.g.groups == 1;
-  const double strips = up(p.g.N, 16 * wide), groups = p.g.groups;
-  const double rows = one ? p.g.rows : 1.5 * p.g.rows / groups + 1;
-  const double tiles = up(rows, q4_few_rows(p)), r = up(rows, tiles);
-  const double beside = groups * (one ? tiles : 1.0), turns = one ? 1.0 : tiles;
-  const double e = up(strips, std::max(1.0, std::floor(256 / beside)));
-  const double rounds = up(beside * up(strips, e), 256);
-  const double time =
-      12 + 2 * r + e * wide * (9 + 0.8 * r) + (wide == 1 ? 14 * e : 0.0);
-  return time * rounds * turns < 0.88 * (double)q4_tile_cost(p, q4_tile(p));
+  const double tiles = (double)q4_row_tiles(p, q4_few_rows(p)), strips = q4_few_strips(p);
+  const double chunks = (p.g.K + kQ4FewK - 1) / kQ4FewK;
+  const double w = std::ceil(chunks / (1 << q4_waves_along_k(p)));
+  double r, e, rounds;
+  if (one) {
+    r = std::ceil(p.g.rows / tiles);
+    e = std::ceil(strips / std::max(1.0, std::floor(kQ4Cus / tiles)));
+    rounds = std::ceil(tiles / kQ4Cus);
+  } else {
+    r = std::min((double)q4_few_rows(p), (double)p.g.rows / q4_active(p) + 1);
+    e = std::max(1.0, strips * std::min(1.0, tiles / kQ4Cus));
+    rounds = std::max(1.0, tiles / kQ4Cus);
+  }
+  const double fixed = !one ? 5.5 : tiles > 1 ? 6 : 5;
+  const double staged = 0.0215 * r * chunks * (chunks * r > 200 ? e : 1.0);
+  const double few = rounds * (fixed + staged + e * (0.2 + 0.06 * r + w * (1.17 + 0.014 * r)));
+  const Q4Tile t = q4_tile(p);
+  const double rest = t == kTile32 && p.g.K > 256 && p.g.K % 256 != 0 ? 4 : 0;
+  return few < 3 + rest + 1e-2 * (double)q4_tile_cost(p, t) * (3.9 + 4.3 / 1024 * p.g.K);
 }
 
 }  // namespace gemmf32

@@ -1,12 +1,12 @@
 """GPU tests of the products with 4-bit weights at their edges: values that are not
-finite, and unused codes, where K ends inside a step."""
+finite and unused codes where K ends inside a step, and groups of very uneven sizes."""
 import pytest
 import torch
 
 from dense_fp32_gemm_f32_amd import binding, q4
 from tests import gpu_helpers as H
 from tests.test_gpu_grouped import gen
-from tests.test_gpu_q4 import E2M1, INT, KERNELS, KINDS
+from tests.test_gpu_q4 import E2M1, INT, KERNELS, KINDS, grouped
 
 pytestmark = pytest.mark.gpu
 
@@ -87,3 +87,48 @@ def test_the_unused_half_beside_large_powers(gpu_lib, kernel, form):
                                   zero=None if zero is None else zero.cuda())
             # whole numbers times one power: exact in every order
             assert torch.equal(got.cpu().double(), a.double() @ W.t())
+
+
+# counts and columns: all places in one group, in the last, nearly all, one each in a few of many
+UNEVEN = {"one": [192] + [0] * 31, "last": [0] * 31 + [192], "most": [150, 0, 1, 0, 20, 1, 0, 20],
+          "alone": [150], "few of many": [1, 0, 0, 0, 2] + [0] * 200 + [5],
+          "ends of many": [300] + [0] * 998 + [4] + [1] * 24, "nobody": [0, 0, 0],
+          "even": [3] * 100, "full": [12, 13, 20, 21, 24, 25, 40, 41]}
+
+
+@pytest.mark.parametrize("name", list(UNEVEN))
+@pytest.mark.parametrize("K,N", [(640, 300), (131, 16), (2100, 64)])
+def test_uneven_groups_of_few_rows(gpu_lib, name, K, N):
+    if len(UNEVEN[name]) > 300 and N > 16:
+        pytest.skip("as many weights of this size take gigabytes on the host")
+    grouped(UNEVEN[name], K, N, "zeros", "f16", group=32, spare=4)
+    grouped(UNEVEN[name], K, N, "e2m1", "e8m0", group=64, integer=False, gather=False,
+            scatter=False, bias=False, act=0, beta=0.5)
+
+
+@pytest.mark.parametrize("counts", [[192] + [0] * 31, [0] * 31 + [192],
+                                    [96, 40, 20, 10, 10, 8, 4, 4] + [0] * 24])
+def test_uneven_groups_fill_the_device(gpu_lib, counts):
+    """All rows in one of 32 groups are 10 row tiles, which go beside each other: about as
+    long as 6 rows in each (one after another they took 9 times as long).  A factor of 4 is
+    far from either."""
+    H.say(f"q4 uneven groups in time {counts[:4]}")
+    K, N, G = 1024, 2048, 32
+    g = torch.Generator(device="cuda").manual_seed(3)
+    codes = torch.randint(0, 256, (G, N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    scale = torch.randint(120, 125, (G, N, K // 32), generator=g, device="cuda").to(torch.uint8)
+    a, c = torch.randn(192, K, generator=g, device="cuda"), torch.empty(192, N, device="cuda")
+
+    def time(rows):
+        off = torch.tensor([0, *torch.tensor(rows).cumsum(0).tolist()], dtype=torch.int32).cuda()
+        took = []
+        for _ in range(20):
+            begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            begin.record()
+            for _ in range(20):
+                binding.gemm_q4_grouped(a, codes, scale, off, c, group=32, format=E2M1)
+            end.record()
+            end.synchronize()
+            took.append(begin.elapsed_time(end))
+        return sorted(took)[10]
+    assert time(counts) < 4 * time([6] * G)
