@@ -566,27 +566,14 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteProblem p) {
 // Lane j forms the gradient of choice j; it is handed to the expert's lane choice
 // by choice, so an expert named twice gets both.
 
-// What is to be added to g_i: minus the sum, or (where base is g_m) the second bracket.
-struct Centre {
-  float base, add;
-  // others: the sum of the shares but the leading one; dot: of their products with g
-  __device__ __forceinline__ Centre(float share, float g, float others, float dot) {
-    const bool leads = others < 0.5f;
-    base = leads ? g : 0.f;
-    add = leads ? g * others - dot : -(share * g + dot);
-  }
-};
-
-// g - sum q_k g_k of the lanes' entries, whose shares go by x.
-__device__ __forceinline__ float centred(float x, float q, float g, bool there) {
-  const float largest = wave_max(there ? x : -INFINITY);
-  const uint64_t most = __builtin_amdgcn_ballot_w64(there && x == largest);
-  if (most == 0) return 0.f;
-  const int lane = threadIdx.x & 63, m = __builtin_ctzll(most);
-  const bool other = there && lane != m;
-  const Centre c(lane_value(q, m), lane_value(g, m), wave_sum(other ? q : 0.f),
-                 wave_sum(other ? q * g : 0.f));
-  return (g - c.base) + c.add;
+// g - sum q_k g_k of the lanes' entries.
+__device__ __forceinline__ float centred(float q, float g, bool there) {
+  const uint64_t most = __builtin_amdgcn_ballot_w64(there && q > 0.5f);
+  if (most == 0) return g - wave_sum(there ? q * g : 0.f);
+  const int m = __builtin_ctzll(most);
+  const bool other = there && (int)(threadIdx.x & 63) != m;
+  const float gm = lane_value(g, m);
+  return (g - gm) + (gm * wave_sum(other ? q : 0.f) - wave_sum(other ? q * g : 0.f));
 }
 
 template <int E>
@@ -607,7 +594,7 @@ __global__ void __launch_bounds__(kThreads) route_grad_kernel(RouteProblem p) {
     const float s = p.sigmoid && there ? sigmoid(x) : 0.f, rest = p.sigmoid ? sigmoid(-x) : 1.f;
     if (p.renorm) {
       const float q = p.sigmoid ? share_of_sigmoid(x, s, there) : share_of_chosen(x, there);
-      mine = q * centred(x, q, g, there) * rest;
+      mine = q * centred(q, g, there) * rest;
     } else {
       mine = s * rest * g;
     }
@@ -635,15 +622,21 @@ __global__ void __launch_bounds__(kThreads) route_grad_kernel(RouteProblem p) {
       others += less ? w[i] : 0.f;
     }
     sum = wave_sum(sum);
-    // (one above a half is alone at m, and alone has w 1; more there have all a sum of 2)
     const float share = there ? expf(x - m) / sum : 0.f;
-    const bool lead = there && x == m;
-    const Centre c(1.f / sum, wave_sum(lead ? g : 0.f),
-                   sum < 2.f ? wave_sum(others) / sum : 1.f, wave_sum(lead ? 0.f : share * g));
+    // one above a half is alone at m, and alone has w 1: two there have a sum of 2
+    const bool leads = sum < 2.f;
+    float base = 0.f, add;
+    if (leads) {
+      const bool lead = there && x == m;
+      base = wave_sum(lead ? g : 0.f);
+      add = base * (wave_sum(others) / sum) - wave_sum(lead ? 0.f : share * g);
+    } else {
+      add = -wave_sum(share * g);
+    }
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-      const float by = c.base != 0.f && w[i] == 1.f ? 0.f : d[i] - c.base;
-      d[i] = w[i] > 0.f ? w[i] / sum * (by + c.add) : 0.f;
+      const float by = leads && w[i] == 1.f ? 0.f : d[i] - base;
+      d[i] = w[i] > 0.f ? w[i] / sum * (by + add) : 0.f;
     }
   }
   float* out = p.dlogits + t * p.lddl;
