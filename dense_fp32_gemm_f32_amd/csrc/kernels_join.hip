@@ -1,7 +1,7 @@
 // The join of the experts' rows: y_t = sum_j w_tj H[t top + j] + beta y_t, and its
 // gradient dH_tj = w_tj dy_t, dw_tj = <dy_t, H_tj>.  Bound by HBM: every row of H is
-// read once, every row of Y (of dH) written once: 8192 x 2 rows of 2048 take 33 us (6.1 TB/s)
-// and 61 us (5.5 TB/s).
+// read once, every row of Y (of dH) written once: 8192 x 2 rows of 2048 take 41 us (4.8 TB/s,
+// a copy's rate) and 55 us (6.2 TB/s), with inputs that the caches do not hold.
 #include "experts_internal.h"
 
 namespace gemmf32 {
@@ -47,7 +47,7 @@ __device__ __forceinline__ bool counts(const JoinProblem& p, int64_t i) {
 // behind them the columns beside those.  kAtOnce entries' rows are on the way at once.
 __global__ void __launch_bounds__(kThreads)
     join_kernel(JoinProblem p, int across_log2, int blocks) {
-  constexpr int kAtOnce = 4;   // (8192 x 2 rows of 2048: 33 us, with 8 37 us)
+  constexpr int kAtOnce = 4;   // (2048 x 8 rows of 2048: 28.7 us, with 2 30.1, with 8 28.0)
   const unsigned id = tile_id(), rows = id / (unsigned)blocks;
   const int64_t t = (int64_t)rows * (kThreads >> across_log2) + (threadIdx.x >> across_log2);
   const int64_t c = 4 * (((int64_t)(id - rows * blocks) << across_log2) +

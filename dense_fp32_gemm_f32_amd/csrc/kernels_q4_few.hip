@@ -1,8 +1,8 @@
 // Products with 4-bit weights for few rows (q4_routes.h) and at least 128 k: tiles of up
 // to 20 rows.  Bound by the conversion of the codes (95 vector instructions for 2048 of
-// them) beside their read: one row of 8192 x 8192 takes 16.6 us from HBM (33.5 MB of codes,
-// 2.1 TB/s), one of 28672 x 8192 43 us (2.8 TB/s), where loads alone in the same order
-// take 33 us.
+// them) beside their read: one row of 8192 x 8192 with fp16 scales and zero points takes 18
+// us (2.0 TB/s), one of 28672 x 8192, whose codes the caches do not hold, 53, and without
+// zero points 41 (2.9 TB/s), where loads alone in the same order take 33.
 //
 // The rows' three bf16 parts are rows of the matrix instruction: a row has four of its
 // 16, of which the last is not used, so that a lane gets the sums of one row's parts and
@@ -15,7 +15,7 @@
 // others have the strips beside it.  Each wave has the codes and scales of its next two
 // chunks on the way into registers, whichever strip they are of (four chunks were no
 // faster, nor were two chunks of one line of codes in turn).  With 8 waves a workgroup
-// the row of 8192 x 8192 took 19 us where it took 16, as fewer loads are on the way.
+// the row of 8192 x 8192 took 3 us more, as fewer loads are on the way.
 #include "q4_common.h"
 #include "q4_routes.h"
 
@@ -424,8 +424,8 @@ struct GroupTiles {
   }
 };
 
-// Quotient of numbers from 1 to 2^9 (the real one is at least a 2^10th from a whole number
-// above it, the reciprocal off by 2^-23 of itself).
+// Quotient of numbers up to 256, rounded down: a + 1/2 over b is at least 2^-9 from the whole
+// numbers, the reciprocal and the product are off by 2^-14 at most.
 __device__ __forceinline__ unsigned small_quotient(unsigned a, unsigned b) {
   return (unsigned)(((float)a + 0.5f) * __builtin_amdgcn_rcpf((float)b));
 }

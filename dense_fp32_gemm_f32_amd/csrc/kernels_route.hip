@@ -10,9 +10,10 @@
 // hold where the chosen scores would underflow.
 //
 // Each lane sorts its keys once; a choice is then the largest head of 64 lists, six DPP
-// steps and a pop.  Bound by the vector instructions: 16384 x 256, 8 choices, take 11 us
-// without a bias, 14 with one, 19 with the best 4 of 8 groups (54 where every choice was
-// made in 64 bits); the read of the logits alone would take 3.5.
+// steps and a pop.  Bound by the vector instructions: 16384 x 256, 8 choices, take 12 us
+// without a bias, 15 with one, 18 with the best 4 of 8 groups (54 where every choice was
+// made in 64 bits); the read of the logits alone would take 3.5.  Groups that are no whole
+// number of lanes are done in 64 bits from the start: 16384 x 144 in 8 groups take 73 us.
 #include "experts_internal.h"
 
 #include <cfloat>

@@ -21,8 +21,8 @@ struct Q4TileCost {
 
 // A CU holds one workgroup of each tile, so a product takes as long as the rounds its
 // workgroups make, times the round's time, which grows with K alike for all of them
-// (measured at K = 4096 in the table's order, with e8m0 scales: 292, 238, 189, 107, 70, 47, 33
-// and 26 us; with fp16 scales 343, 284, 220, 130, 75, 51, 38 and 28 us).
+// (measured at K = 4096 in the table's order, with e8m0 scales: 299, 245, 192, 111, 67, 43, 30
+// and 24 us; with fp16 scales 350, 290, 223, 131, 76, 50, 36 and 27 us).
 constexpr Q4TileCost kQ4Tiles[] = {{256, 256, 1180}, {256, 192, 970}, {256, 128, 760},
                                    {128, 128, 440},  {64, 128, 270},  {64, 64, 185},
                                    {32, 64, 130},    {32, 32, 100}};
@@ -101,13 +101,14 @@ GEMM_F32_BOTH inline int q4_few_strips(const Q4Problem& p) {
 //   5 to 6 + 0.0215 r c (staging, for each strip where LDS has no room for all chunks)
 //   + e (0.2 + 0.06 r + w (1.17 + 0.014 r))
 // and tiles whose rounds cost t take 3 + t (3.9 + 4.3 K / 1024) / 100, and 4 where the waves
-// of the smallest, which share K by 256, have a rest behind that.  These are fits of 280 sizes each: 1 to
-// 128 groups of 1 to 48 rows, 512 x 2048 to 8192 x 8192, e8m0 scales; the choices by them are
-// 0.5 % slower than the faster of both on average, and 25 % at most.  Groups are counted as
-// even: the offsets that say more are the device's.  (Few against tiles in us.  4096 x 4096: 8
-// rows 12 against 22, 24 rows 22 against 23; 8192 x 8192: 8 rows 27 against 38; 32 groups of
-// 2048 x 1024: 6 rows each 17 against 43, 32 rows 35 against 45, 48 rows 53 against 47; of
-// 7168 x 2048: 8 rows each 86 against 236, 32 rows 225 against 251, 48 rows 390 against 256.)
+// of the smallest, which share K by 256, have a rest behind that.  These are fits over 275
+// sizes, 1 to 128 groups of 1 to 48 rows each, 512 x 2048 to 8192 x 8192, e8m0 scales; the
+// choices by them take 0.5 % longer than the faster kernel on average, 25 % at most.  Groups
+// are counted as even: the offsets that say more are the device's.  (Few against tiles in us.
+// 4096 x 4096: 8 rows 15 against 23, 24 rows 30 against 24; 8192 x 8192: 8 rows 26 against 38;
+// 32 groups of 2048 x 1024: 8 rows each 17 against 45, 32 rows 34 against 45, 48 rows 52
+// against 47; of 7168 x 2048: 8 rows each 86 against 236, 32 rows 214 against 251, 48 rows
+// 384 against 255.)
 inline bool q4_few(const Q4Problem& p) {
   if (p.g.K < kQ4FewK) return false;
   const bool one = p.g.groups == 1;

@@ -132,3 +132,75 @@ def test_uneven_groups_fill_the_device(gpu_lib, counts):
             took.append(begin.elapsed_time(end))
         return sorted(took)[10]
     assert time(counts) < 4 * time([6] * G)
+
+
+@pytest.mark.parametrize("G", [3, 64, 65, 1024])
+@pytest.mark.parametrize("K", [160, 1100])
+def test_offsets_that_leave_the_places_with_few_rows(gpu_lib, G, K):
+    """Offsets are taken into [0, rows], a group that ends before it begins is empty, and
+    rows of no group stay as they were: with the groups in lanes and in threads."""
+    H.say(f"q4 few rows, odd offsets G={G} K={K}")
+    g = gen(G)
+    N, rows = 24, 40
+    a = torch.randint(-2, 3, (rows, K), generator=g).float()
+    packed = torch.randint(0, 256, (G, N, K // 2), generator=g, dtype=torch.uint8)
+    scale = torch.ones(G, N, (K + 31) // 32)
+    middle = G // 2
+    # (groups between the three are empty)
+    cases = [([first] + [10] * middle + [33] * (G - 1 - middle) + [last],
+              {0: (max(first, 0), 10), middle: (10, 33), G - 1: (33, min(last, rows))})
+             for first, last in ((-5, 99), (4, 36))]
+    cases.append(([50 - i for i in range(G + 1)], {}))   # each ends before it begins
+    for off, span in cases:
+        c = torch.full((rows, N), 7.0, device="cuda")
+        binding.gemm_q4_grouped(a.cuda(), packed.cuda(), scale.cuda(),
+                                torch.tensor(off, dtype=torch.int32).cuda(), c, group=32)
+        want = torch.full((rows, N), 7.0, dtype=torch.float64)
+        for e, (b, t) in span.items():
+            W = q4.dequantize(packed[e], scale[e], K, group=32, dtype=torch.float64)
+            want[b:t] = a[b:t].double() @ W.t()
+        assert torch.equal(c.cpu().double(), want)
+
+
+@pytest.mark.parametrize("G", [32, 200])
+def test_captured_few_rows_follow_new_offsets(gpu_lib, G):
+    """A replay finds the row tiles from the offsets that are there then."""
+    H.say(f"q4 few rows captured, new offsets G={G}")
+    g = gen(G + 5)
+    K, N, rows = 512, 640, 130
+    a = torch.randint(-2, 3, (rows, K), generator=g).float().cuda()
+    packed = torch.randint(0, 256, (G, N, K // 2), generator=g, dtype=torch.uint8).cuda()
+    scale = (2.0 ** torch.randint(-1, 2, (G, N, K // 64), generator=g)).cuda()
+    offsets, c = torch.zeros(G + 1, dtype=torch.int32, device="cuda"), torch.zeros(rows, N).cuda()
+
+    def step():
+        return binding.gemm_q4_grouped(a, packed, scale, offsets, c, group=64)
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        step()
+        stream.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            step()
+        for counts in ([rows] + [0] * (G - 1), [0] * (G - 1) + [rows - 7],
+                       [rows // G + (i < rows % G) for i in range(G)], [0] * G,
+                       [60] + [0] * (G - 3) + [1, 50]):
+            offsets.copy_(torch.tensor([0, *torch.tensor(counts).cumsum(0).tolist()]))
+            c.fill_(3.0)
+            graph.replay()
+            stream.synchronize()
+            got = c.clone()
+            c.fill_(3.0)
+            step()
+            stream.synchronize()
+            assert torch.equal(got, c)
+            end = sum(counts)
+            assert bool((got[end:] == 3.0).all())
+            at = 0
+            for e, n in enumerate(counts):
+                if n:
+                    W = q4.dequantize(packed[e].cpu(), scale[e].cpu(), K, group=64,
+                                      dtype=torch.float64)
+                    assert torch.equal(got[at:at + n].cpu().double(),
+                                       a[at:at + n].cpu().double() @ W.t())
+                at += n
