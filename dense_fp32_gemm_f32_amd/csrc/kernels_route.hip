@@ -562,8 +562,9 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteProblem p) {
 //   sigmoid        dl_i = s_i (1 - s_i) g_i
 //   renormalised   dl_i = q_i (1 - s_i) (g_i - sum q_k g_k)
 // Where one share is above a half, the difference at it would have lost the bits that 1 less
-// that share has.  With m its place, and the other shares' sums,
-//   g_i - sum q_k g_k = (g_i - g_m) + (g_m sum' q_k - sum' q_k g_k)
+// that share has.  With m its place,
+//   g_i - sum q_k g_k = (g_i - g_m) + sum q_k (g_m - g_k)
+// where m itself adds nothing.
 // Lane j forms the gradient of choice j; it is handed to the expert's lane choice
 // by choice, so an expert named twice gets both.
 
@@ -571,10 +572,8 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteProblem p) {
 __device__ __forceinline__ float centred(float q, float g, bool there) {
   const uint64_t most = __builtin_amdgcn_ballot_w64(there && q > 0.5f);
   if (most == 0) return g - wave_sum(there ? q * g : 0.f);
-  const int m = __builtin_ctzll(most);
-  const bool other = there && (int)(threadIdx.x & 63) != m;
-  const float gm = lane_value(g, m);
-  return (g - gm) + (gm * wave_sum(other ? q : 0.f) - wave_sum(other ? q * g : 0.f));
+  const float gm = lane_value(g, __builtin_ctzll(most));
+  return (g - gm) + wave_sum(there ? q * (gm - g) : 0.f);
 }
 
 template <int E>
@@ -612,27 +611,26 @@ __global__ void __launch_bounds__(kThreads) route_grad_kernel(RouteProblem p) {
       if (lane * E + i == to) d[i] += y;
   }
   if (all) {
-    float w[E], sum = 0.f, others = 0.f;
+    float w[E], sum = 0.f;
     load_logits<E>(p, t, lane, w);
     const float m = largest<E>(w);
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-      const bool less = w[i] < m;
       w[i] = w[i] > -INFINITY ? expf(w[i] - m) : 0.f;
       sum += w[i];
-      others += less ? w[i] : 0.f;
     }
     sum = wave_sum(sum);
-    const float share = there ? expf(x - m) / sum : 0.f;
     // one above a half is alone at m, and alone has w 1: two there have a sum of 2
     const bool leads = sum < 2.f;
     float base = 0.f, add;
     if (leads) {
-      const bool lead = there && x == m;
-      base = wave_sum(lead ? g : 0.f);
-      add = base * (wave_sum(others) / sum) - wave_sum(lead ? 0.f : share * g);
+      base = wave_sum(there && x == m ? g : 0.f);
+      float others = 0.f;
+#pragma unroll
+      for (int i = 0; i < E; ++i) others += w[i] < 1.f ? w[i] * (base - d[i]) : 0.f;
+      add = wave_sum(others) / sum;
     } else {
-      add = -wave_sum(share * g);
+      add = -wave_sum(there ? expf(x - m) / sum * g : 0.f);
     }
 #pragma unroll
     for (int i = 0; i < E; ++i) {

@@ -149,6 +149,30 @@ def test_route_grad_of_one_expert_above_all(gpu_lib, T, E, top, score, renorm):
     check_slopes(logits, choice, torch.randn(T, top, generator=g), score, renorm, "one above")
 
 
+@pytest.mark.parametrize("T,E,top", [(40, 2, 2), (30, 64, 8), (9, 300, 3)])
+@pytest.mark.parametrize("score", [SOFTMAX, SIGMOID])
+def test_route_grad_of_one_above_and_nearly_equal_gradients(gpu_lib, T, E, top, score):
+    """Where a share is above a half the gradients enter by their differences, which are
+    exact: the gate is of sum_k share_k |g_i - g_k|, for g that differ by 2^-20 of
+    themselves."""
+    H.say(f"route_grad nearly equal T={T} E={E} top={top} score={score}")
+    g = gen(T + E + 3)
+    logits = torch.randn(T, E, generator=g) - (45 if score == SIGMOID else 0)
+    choice = torch.stack([torch.randperm(E, generator=g)[:top] for _ in range(T)])
+    logits.scatter_add_(1, choice[:, :1], 9 + 20 * torch.rand(T, 1, generator=g))
+    dweight = 1 + torch.randint(-8, 9, (T, top), generator=g) * 2.0 ** -23
+    got = binding.route_grad(dweight.cuda(), logits.cuda(), choice.int().cuda(), score=score,
+                             renorm=True).cpu().double().gather(1, choice)
+    cx, d = logits.double().gather(1, choice), dweight.double()
+    share = torch.softmax(torch.nn.functional.logsigmoid(cx) if score == SIGMOID else cx, 1)
+    by = share[:, None, :] * (d[:, :, None] - d[:, None, :])
+    slope = torch.sigmoid(-cx) if score == SIGMOID else torch.ones_like(cx)
+    want, mag = share * slope * by.sum(2), share * slope * by.abs().sum(2)
+    # as check_slopes; g_i - g_m and the sum are each at most twice the sum of magnitudes
+    steps = 4 * (6 * float((cx.max(1).values - cx.min(1).values).max()) + 3 * top + 64)
+    assert bool(((got - want).abs() <= steps * U * mag + 2.0 ** -126).all())
+
+
 @pytest.mark.parametrize("renorm", [False, True])
 @pytest.mark.parametrize("score", [SOFTMAX, SIGMOID])
 def test_route_grad_of_tokens_with_fewer_choices(gpu_lib, renorm, score):
