@@ -102,9 +102,11 @@ GEMM_F32_BOTH inline int q4_few_strips(const Q4Problem& p) {
 //   + e (0.2 + 0.06 r + w (1.17 + 0.014 r))
 // and tiles whose rounds cost t take 3 + t (3.9 + 4.3 K / 1024) / 100, and 4 where the waves
 // of the smallest, which share K by 256, have a rest behind that.  These are fits over 275
-// sizes, 1 to 128 groups of 1 to 48 rows each, 512 x 2048 to 8192 x 8192, e8m0 scales; the
-// choices by them take 0.5 % longer than the faster kernel on average, 25 % at most.  Groups
-// are counted as even: the offsets that say more are the device's.  (Few against tiles in us.
+// sizes, 1 to 128 groups of 1 to 48 rows each, 512 x 2048 to 8192 x 8192, e8m0 scales.  Over
+// these and others with up to 200 rows a group the choices by them take 1.4 % longer than the
+// faster kernel on average, and 4 % where groups have from half to three halves of the
+// average.  (Groups are counted as even, the largest with one row more: the offsets that say
+// better are the device's.  Few against tiles in us.
 // 4096 x 4096: 8 rows 15 against 23, 24 rows 30 against 24; 8192 x 8192: 8 rows 26 against 38;
 // 32 groups of 2048 x 1024: 8 rows each 17 against 45, 32 rows 34 against 45, 48 rows 52
 // against 47; of 7168 x 2048: 8 rows each 86 against 236, 32 rows 214 against 251, 48 rows
@@ -112,19 +114,15 @@ GEMM_F32_BOTH inline int q4_few_strips(const Q4Problem& p) {
 inline bool q4_few(const Q4Problem& p) {
   if (p.g.K < kQ4FewK) return false;
   const bool one = p.g.groups == 1;
-  const double tiles = (double)q4_row_tiles(p, q4_few_rows(p)), strips = q4_few_strips(p);
-  const double chunks = (p.g.K + kQ4FewK - 1) / kQ4FewK;
+  const int most = q4_few_rows(p), active = q4_active(p);
+  const bool small = !one && p.g.rows <= (int64_t)active * most;   // a tile each
+  const double tiles = small ? active : (double)q4_row_tiles(p, most);
+  const double strips = q4_few_strips(p), chunks = (p.g.K + kQ4FewK - 1) / kQ4FewK;
   const double w = std::ceil(chunks / (1 << q4_waves_along_k(p)));
-  double r, e, rounds;
-  if (one) {
-    r = std::ceil(p.g.rows / tiles);
-    e = std::ceil(strips / std::max(1.0, std::floor(kQ4Cus / tiles)));
-    rounds = std::ceil(tiles / kQ4Cus);
-  } else {
-    r = std::min((double)q4_few_rows(p), (double)p.g.rows / q4_active(p) + 1);
-    e = std::max(1.0, strips * std::min(1.0, tiles / kQ4Cus));
-    rounds = std::max(1.0, tiles / kQ4Cus);
-  }
+  const double r = one ? std::ceil(p.g.rows / tiles)
+                       : std::min((double)most, (double)p.g.rows / active + 1);
+  const double e = std::ceil(strips / std::max(1.0, std::floor(kQ4Cus / tiles)));
+  const double rounds = std::ceil(tiles / kQ4Cus);
   const double fixed = !one ? 5.5 : tiles > 1 ? 6 : 5;
   const double staged = 0.0215 * r * chunks * (chunks * r > 200 ? e : 1.0);
   const double few = rounds * (fixed + staged + e * (0.2 + 0.06 * r + w * (1.17 + 0.014 * r)));
